@@ -674,3 +674,21 @@ def pq2_matmul_prefill_planes(qp, xs, planes, y, stream=None) -> None:
 def pq2_matmul_prefill_planes_tuned(qp, xs, planes, y, tile=0, stream=None) -> None:
     _check(lib.pq2_matmul_prefill_planes_tuned(*_matmul_args(qp, xs, planes, y), tile, _stream(stream)),
            "pq2_matmul_prefill_planes_tuned")
+
+
+# The operators of include/pq2_block.h (imported last: the module uses the
+# names above).
+from .block import (  # noqa: E402
+    ACT_GELU_TANH,
+    ACT_SILU,
+    BLOCK_EXPORTED,
+    pq2_block_norm,
+    pq2_gated_linear_tiles,
+    pq2_gated_linear_w4,
+    pq2_gated_matmul_tiles,
+    pq2_gated_matmul_w4,
+    pq2_linear_w4,
+    pq2_matmul_w4,
+    pq2_prepare_w4_tiles,
+    pq2_w4_tiles_bytes,
+)

@@ -1,0 +1,287 @@
+"""Binding of include/pq2_block.h: products with 4-bit weights, the gated
+feed-forward product, and the norms around a block with the INT8 quantiser.
+
+Like the rest of the package these functions marshal arguments only.  All
+tensors of a call are on one device; the work goes to that device's current
+torch stream (or ``stream``), whichever device is current.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import PQ2_BF16, PQ2_F16, PQ2_F32, _check, lib, pq2_tiles_bytes
+
+ACT_SILU, ACT_GELU_TANH = 0, 1
+
+BLOCK_EXPORTED = (
+    "pq2_w4_tiles_bytes",
+    "pq2_prepare_w4_tiles",
+    "pq2_matmul_w4",
+    "pq2_linear_w4",
+    "pq2_gated_matmul_tiles",
+    "pq2_gated_matmul_w4",
+    "pq2_gated_linear_tiles",
+    "pq2_gated_linear_w4",
+    "pq2_block_norm",
+)
+
+_DTYPE = {torch.bfloat16: PQ2_BF16, torch.float16: PQ2_F16, torch.float32: PQ2_F32}
+
+
+class BlockNormArgs(ctypes.Structure):
+    """pq2_block_norm_args of include/pq2_block.h."""
+    _fields_ = [
+        ("r", ctypes.c_void_p), ("r_stride", ctypes.c_int64),
+        ("block", ctypes.c_void_p), ("block_stride", ctypes.c_int64),
+        ("post_w", ctypes.c_void_p),
+        ("gate", ctypes.c_void_p), ("gate_stride", ctypes.c_int64),
+        ("w", ctypes.c_void_p),
+        ("r_out", ctypes.c_void_p), ("r_out_stride", ctypes.c_int64),
+        ("x_out", ctypes.c_void_p), ("x_out_stride", ctypes.c_int64),
+        ("q", ctypes.c_void_p), ("xs", ctypes.c_void_p),
+        ("m", ctypes.c_int64), ("k", ctypes.c_int64), ("agroup", ctypes.c_int64),
+        ("eps", ctypes.c_double), ("alpha", ctypes.c_float),
+        ("r_dtype", ctypes.c_int), ("block_dtype", ctypes.c_int), ("w_dtype", ctypes.c_int),
+        ("x_dtype", ctypes.c_int), ("unit_offset", ctypes.c_int),
+    ]
+
+
+def _bind():
+    p, i64, i32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
+    product = [p, p, p, i64, i64, i64]
+    for name, args in {
+        "pq2_w4_tiles_bytes": [i64, i64, i64],
+        "pq2_prepare_w4_tiles": [p, i64, p, i64, i64, i64, i64, p, p],
+        "pq2_matmul_w4": product + [i64, p, p],
+        "pq2_linear_w4": [p, i32, i64, p, i64, i64, i64, i64, p, p, p, p],
+        "pq2_gated_matmul_tiles": [p, p, p, p, i64, i64, i64, i32, p, i32, p],
+        "pq2_gated_matmul_w4": [p, p, p, p, i64, i64, i64, i64, i32, p, i32, p],
+        "pq2_gated_linear_tiles": [p, i32, i64, p, p, i64, i64, i64, i32, p, i32, p, p, p],
+        "pq2_gated_linear_w4": [p, i32, i64, p, p, i64, i64, i64, i64, i32, p, i32, p, p, p],
+        "pq2_block_norm": [ctypes.POINTER(BlockNormArgs), p],
+    }.items():
+        fn = getattr(lib, name)
+        fn.argtypes = args
+        fn.restype = i64 if name == "pq2_w4_tiles_bytes" else i32
+
+
+_bind()
+
+
+def _dtype(t, name):
+    code = _DTYPE.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name}: unsupported dtype {t.dtype}")
+    return code
+
+
+def _same_device(first, *rest):
+    """The device of the call's tensors: one GPU for all of them."""
+    dev = first.device
+    if dev.type != "cuda":
+        raise ValueError("device tensors expected")
+    for t in rest:
+        if t is not None and t.device != dev:
+            raise ValueError("all tensors of a call must be on one device")
+    return dev
+
+
+def _call(name, dev, stream, *args):
+    """Calls the entry point on device ``dev``: its current stream unless one is given."""
+    if stream is None:
+        s = torch.cuda.current_stream(dev).cuda_stream
+    else:
+        s = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    fn = getattr(lib, name)
+    if dev.index == torch.cuda.current_device():
+        status = fn(*args, s)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, s)
+    if status:
+        _check(status, name)
+
+
+def pq2_w4_tiles_bytes(n: int, k: int, wgroup: int) -> int:
+    """Bytes of the w4 tile layout of an n x k weight matrix (ValueError on a bad shape or group)."""
+    size = lib.pq2_w4_tiles_bytes(n, k, wgroup)
+    if size < 0:
+        raise ValueError(f"pq2_w4_tiles_bytes: unsupported shape n={n} k={k} wgroup={wgroup}")
+    return size
+
+
+def pq2_prepare_w4_tiles(codes, scales, wgroup: int, tiles, stream=None) -> None:
+    """codes: uint8 [n][>= k/2], two 4-bit codes a byte (the even weight in the low half, weight = code - 8);
+    scales: float16 [n][k/wgroup]; both with unit column stride.  tiles: contiguous uint8 of
+    pq2_w4_tiles_bytes(n, k, wgroup) bytes.  n and k come from scales."""
+    if codes.dtype != torch.uint8 or scales.dtype != torch.float16 or tiles.dtype != torch.uint8:
+        raise ValueError("codes uint8, scales float16, tiles uint8 expected")
+    if codes.dim() != 2 or scales.dim() != 2 or codes.stride(1) != 1 or scales.stride(1) != 1:
+        raise ValueError("codes and scales must be 2-D with unit column stride")
+    n, k = scales.shape[0], scales.shape[1] * wgroup
+    if codes.shape[0] != n or codes.shape[1] < k // 2:
+        raise ValueError("shape mismatch between codes and scales")
+    if not tiles.is_contiguous() or tiles.numel() < pq2_w4_tiles_bytes(n, k, wgroup):
+        raise ValueError("tiles must be a contiguous uint8 tensor of pq2_w4_tiles_bytes(n, k, wgroup) bytes")
+    _call("pq2_prepare_w4_tiles", _same_device(codes, scales, tiles), stream, codes.data_ptr(),
+          _row_stride(codes), scales.data_ptr(), _row_stride(scales), n, k, wgroup, tiles.data_ptr())
+
+
+def _row_stride(t):
+    """Row stride in elements; a single row's is its length, whatever the tensor says."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def _weights(tiles, need):
+    if tiles.dtype != torch.uint8 or not tiles.is_contiguous() or tiles.numel() < need:
+        raise ValueError("weights: contiguous uint8 tensor of the prepared layout's size expected")
+    return tiles.data_ptr()
+
+
+def _codes(q, xs, m):
+    if q.dtype != torch.int8 or xs.dtype != torch.float32 or not q.is_contiguous() or not xs.is_contiguous():
+        raise ValueError("q contiguous int8 and xs contiguous float32 expected")
+    if q.dim() != 2 or q.shape[0] != m or xs.numel() != m * (q.shape[1] // 128):
+        raise ValueError("shape mismatch: q [m][k], xs [m][k/128] expected")
+    return q.shape[1]
+
+
+def _out(t, name, dtypes):
+    if t.dtype not in dtypes or t.dim() != 2 or not t.is_contiguous():
+        raise ValueError(f"{name}: contiguous 2-D tensor of {', '.join(str(d) for d in dtypes)} expected")
+    return t.shape
+
+
+def _x(x, m, k):
+    if x.dim() != 2 or x.stride(1) != 1 or x.shape[0] != m or x.shape[1] < k:
+        raise ValueError("x must be [m][>= k] with unit column stride")
+    return x.data_ptr(), _dtype(x, "x"), _row_stride(x)
+
+
+def pq2_matmul_w4(q, xs, tiles, y, wgroup: int, stream=None) -> None:
+    """y [m][n] (float32) = 4-bit weights x INT8 activations, any m >= 1; q int8 [m][k] and xs float32 [m][k/128]
+    from pq2_quantize_act_i8 or pq2_block_norm."""
+    m, n = _out(y, "y", (torch.float32,))
+    k = _codes(q, xs, m)
+    w = _weights(tiles, pq2_w4_tiles_bytes(n, k, wgroup))
+    _call("pq2_matmul_w4", _same_device(q, xs, tiles, y), stream, q.data_ptr(), xs.data_ptr(), w, m, n, k, wgroup,
+          y.data_ptr())
+
+
+def pq2_linear_w4(x, tiles, y, wgroup: int, q_work, xs_work, stream=None) -> None:
+    """The complete call: x [m][>= k] bf16/f16/f32 quantised into q_work / xs_work (scratch, int8 [m][k] and float32
+    [m][k/128]), then pq2_matmul_w4."""
+    m, n = _out(y, "y", (torch.float32,))
+    k = _codes(q_work, xs_work, m)
+    w = _weights(tiles, pq2_w4_tiles_bytes(n, k, wgroup))
+    _call("pq2_linear_w4", _same_device(x, tiles, y, q_work, xs_work), stream, *_x(x, m, k), w, m, n, k, wgroup,
+          y.data_ptr(), q_work.data_ptr(), xs_work.data_ptr())
+
+
+def pq2_gated_matmul_tiles(q, xs, gate, up, h, act: int = ACT_SILU, stream=None) -> None:
+    """h [m][n] (bf16/f16/f32) = act(gate product) * up product in one kernel; gate and up are ternary tile layouts of
+    one shape, q / xs as pq2_matmul_w4."""
+    m, n = _out(h, "h", tuple(_DTYPE))
+    k = _codes(q, xs, m)
+    need = pq2_tiles_bytes(n, k)
+    _call("pq2_gated_matmul_tiles", _same_device(q, xs, gate, up, h), stream, q.data_ptr(), xs.data_ptr(),
+          _weights(gate, need), _weights(up, need), m, n, k, act, h.data_ptr(), _DTYPE[h.dtype])
+
+
+def pq2_gated_matmul_w4(q, xs, gate, up, h, wgroup: int, act: int = ACT_SILU, stream=None) -> None:
+    """pq2_gated_matmul_tiles with 4-bit weights in the w4 tile layout."""
+    m, n = _out(h, "h", tuple(_DTYPE))
+    k = _codes(q, xs, m)
+    need = pq2_w4_tiles_bytes(n, k, wgroup)
+    _call("pq2_gated_matmul_w4", _same_device(q, xs, gate, up, h), stream, q.data_ptr(), xs.data_ptr(),
+          _weights(gate, need), _weights(up, need), m, n, k, wgroup, act, h.data_ptr(), _DTYPE[h.dtype])
+
+
+def pq2_gated_linear_tiles(x, gate, up, h, q_work, xs_work, act: int = ACT_SILU, stream=None) -> None:
+    """The complete call of pq2_gated_matmul_tiles: x quantised into the scratch first."""
+    m, n = _out(h, "h", tuple(_DTYPE))
+    k = _codes(q_work, xs_work, m)
+    need = pq2_tiles_bytes(n, k)
+    _call("pq2_gated_linear_tiles", _same_device(x, gate, up, h, q_work, xs_work), stream, *_x(x, m, k),
+          _weights(gate, need), _weights(up, need), m, n, k, act, h.data_ptr(), _DTYPE[h.dtype], q_work.data_ptr(),
+          xs_work.data_ptr())
+
+
+def pq2_gated_linear_w4(x, gate, up, h, wgroup: int, q_work, xs_work, act: int = ACT_SILU, stream=None) -> None:
+    """The complete call of pq2_gated_matmul_w4: x quantised into the scratch first."""
+    m, n = _out(h, "h", tuple(_DTYPE))
+    k = _codes(q_work, xs_work, m)
+    need = pq2_w4_tiles_bytes(n, k, wgroup)
+    _call("pq2_gated_linear_w4", _same_device(x, gate, up, h, q_work, xs_work), stream, *_x(x, m, k),
+          _weights(gate, need), _weights(up, need), m, n, k, wgroup, act, h.data_ptr(), _DTYPE[h.dtype],
+          q_work.data_ptr(), xs_work.data_ptr())
+
+
+def _rows(t, name, m, k):
+    if t.dim() != 2 or t.shape != (m, k) or t.stride(1) != 1:
+        raise ValueError(f"{name} must be [m][k] with unit column stride")
+    return t.data_ptr(), _row_stride(t)
+
+
+def _vector(t, name, k, dtype):
+    if t.dim() != 1 or t.shape[0] != k or t.stride(0) != 1 or t.dtype != dtype:
+        raise ValueError(f"{name} must be a contiguous [k] tensor of the norm weights' dtype")
+    return t.data_ptr()
+
+
+def pq2_block_norm(r, w, eps: float, *, block=None, post_w=None, gate=None, alpha: float = 1.0,
+                   unit_offset: bool = False, r_out=None, x_out=None, x_dtype=None, q=None, xs=None,
+                   agroup: int = 128, stream=None) -> None:
+    """Between two blocks, one launch: r' = r + alpha * gate * norm(block), x = norm(r'), codes of x.
+
+    r [m][k]; block [m][k] (the block's output) or None; post_w [k]: weights of the norm after the block, or None for
+    none; gate [k] or [m][k]; w [k]: weights of the norm before the next block.  Outputs, each optional: r_out (r's
+    dtype; may be r itself), x_out (x_dtype), and q int8 [m][k] with xs float32 [m][k/agroup].  x is rounded to
+    x_dtype (x_out's dtype if not given, else r's) before it is quantised, so q and xs are those of
+    pq2_quantize_act_i8_g on x_out.  post_w and gate have w's dtype."""
+    if r.dim() != 2:
+        raise ValueError("r must be [m][k]")
+    m, k = r.shape
+    a = BlockNormArgs()
+    a.m, a.k, a.agroup = m, k, agroup
+    a.eps, a.alpha, a.unit_offset = eps, alpha, 1 if unit_offset else 0
+    a.r, a.r_stride = _rows(r, "r", m, k)
+    a.r_dtype, a.w_dtype = _dtype(r, "r"), _dtype(w, "w")
+    a.w = _vector(w, "w", k, w.dtype)
+    if block is not None:
+        a.block, a.block_stride = _rows(block, "block", m, k)
+        a.block_dtype = _dtype(block, "block")
+    if post_w is not None:
+        a.post_w = _vector(post_w, "post_w", k, w.dtype)
+    if gate is not None:
+        if gate.dim() == 1:
+            a.gate = _vector(gate, "gate", k, w.dtype)
+        else:
+            if gate.dtype != w.dtype:
+                raise ValueError("gate must have the norm weights' dtype")
+            a.gate, a.gate_stride = _rows(gate, "gate", m, k)
+    if r_out is not None:
+        if r_out.dtype != r.dtype:
+            raise ValueError("r_out must have r's dtype")
+        a.r_out, a.r_out_stride = _rows(r_out, "r_out", m, k)
+    if x_out is not None:
+        if x_dtype is not None and x_out.dtype != x_dtype:
+            raise ValueError("x_out must have x_dtype")
+        a.x_out, a.x_out_stride = _rows(x_out, "x_out", m, k)
+        x_dtype = x_out.dtype
+    code = _DTYPE.get(r.dtype if x_dtype is None else x_dtype)
+    if code is None:
+        raise ValueError(f"unsupported x_dtype {x_dtype}")
+    a.x_dtype = code
+    if q is not None:
+        if q.dtype != torch.int8 or not q.is_contiguous() or q.shape != (m, k):
+            raise ValueError("q must be a contiguous int8 [m][k] tensor")
+        a.q = q.data_ptr()
+    if xs is not None:
+        if xs.dtype != torch.float32 or not xs.is_contiguous() or agroup not in (128, 64, 32) or \
+                xs.numel() != m * (k // agroup):
+            raise ValueError("xs must be a contiguous float32 [m][k/agroup] tensor, agroup 128, 64 or 32")
+        a.xs = xs.data_ptr()
+    _call("pq2_block_norm", _same_device(r, w, block, post_w, gate, r_out, x_out, q, xs), stream, ctypes.byref(a))

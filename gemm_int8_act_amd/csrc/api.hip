@@ -49,6 +49,16 @@ int launch_status(hipError_t e) {
     return e == hipSuccess ? PQ2_OK : PQ2_ELAUNCH;
 }
 
+}  // namespace
+
+// The same checks and error slot for the other C ABI sources.
+namespace pq2 {
+int api_check_device() { return check_device(); }
+int api_launch_status(hipError_t e) { return launch_status(e); }
+}  // namespace pq2
+
+namespace {
+
 int check_k(int64_t k) {
     if (k < kGroup || k % kGroup || k > PQ2_MAX_K) return PQ2_ESHAPE;
     return PQ2_OK;

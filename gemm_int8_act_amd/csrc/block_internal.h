@@ -1,0 +1,93 @@
+// block_internal.h -- host-side launchers of the feed-forward block operators
+// (declared in include/pq2_block.h), and the pieces their kernels share.
+// Arguments reaching the launchers are already validated by the C ABI layer.
+#pragma once
+
+#include "pq2_device.h"
+#include "pq2_internal.h"
+
+#include <hip/hip_fp16.h>
+
+struct pq2_block_norm_args;
+
+namespace pq2 {
+
+// Weight formats of the block kernels: ternary tiles (128-weight groups) and
+// w4 tiles with S = 1, 2 or 4 weight groups per 128 weights.
+enum : int { kFmtTernary = 0, kFmtW4 = 1 };
+
+struct BlockMatmul {
+    const int8_t* q;
+    const float* xs;
+    const uint8_t* w0;   // the matrix, or the gate's
+    const uint8_t* w1;   // the up matrix (gated only)
+    int64_t m, n, k;
+    int fmt, s;          // weight format, weight groups per 128
+    int act;             // -1: plain product, fp32 out; else PQ2_ACT_*
+    void* out;
+    int out_dtype;
+    hipStream_t stream;
+};
+
+int64_t w4_tiles_bytes(int64_t n, int64_t k, int64_t wgroup);
+hipError_t launch_prepare_w4(const uint8_t* codes, int64_t codes_stride, const uint16_t* scales, int64_t scales_stride,
+                             int64_t n, int64_t k, int wgroup, uint8_t* tiles, hipStream_t stream);
+hipError_t launch_block_small_m(const BlockMatmul& a);
+hipError_t launch_block_prefill(const BlockMatmul& a);
+bool block_takes_small_m(const BlockMatmul& a);
+hipError_t launch_block_norm(const pq2_block_norm_args& a, hipStream_t stream);
+
+typedef int v4i __attribute__((ext_vector_type(4)));
+typedef float v4f __attribute__((ext_vector_type(4)));
+
+constexpr int kTernaryUnit = 4352;                                    // bytes of a ternary segment unit
+__host__ __device__ constexpr int w4_unit(int s) { return 8192 + 256 * s; }
+__host__ __device__ constexpr int block_unit(int fmt, int s) { return fmt == kFmtTernary ? kTernaryUnit : w4_unit(s); }
+__host__ __device__ constexpr int block_code_bytes(int fmt) { return fmt == kFmtTernary ? 4096 : 8192; }
+
+// Four INT8 operand dwords (16 weights in k order) of one ternary code dword:
+// code c -> c - 1 through one byte-table lookup per bit plane.
+__device__ __forceinline__ v4i ternary_operand(uint32_t d) {
+    constexpr uint32_t kTable = 0x020100FFu;  // bytes 0..3: the values of codes 0..3
+    return v4i{(int)__builtin_amdgcn_perm(0u, kTable, d & 0x03030303u),
+               (int)__builtin_amdgcn_perm(0u, kTable, (d >> 2) & 0x03030303u),
+               (int)__builtin_amdgcn_perm(0u, kTable, (d >> 4) & 0x03030303u),
+               (int)__builtin_amdgcn_perm(0u, kTable, (d >> 6) & 0x03030303u)};
+}
+
+// The same of two w4 code dwords.  A four-bit two's complement value in the
+// high half of a byte is that value times 16 as an INT8, so no offset or sign
+// extension is needed; every dot is 16 times too large and kW4Scale undoes
+// it on the finished sum (a power of two: exact).  |16 dot| <= 16*8*127*128 <
+// 2^24 stays exact as a float.
+constexpr float kW4Scale = 0.0625f;
+__device__ __forceinline__ v4i w4_operand(uint32_t d0, uint32_t d1) {
+    return v4i{(int)((d0 << 4) & 0xF0F0F0F0u), (int)(d0 & 0xF0F0F0F0u), (int)((d1 << 4) & 0xF0F0F0F0u),
+               (int)(d1 & 0xF0F0F0F0u)};
+}
+
+__device__ __forceinline__ float half_bits(uint32_t h) { return __half2float(__ushort_as_half((unsigned short)h)); }
+
+// fp16 number i (0..7) of 16 bytes.
+__device__ __forceinline__ float half_at(const uint4& v, int i) {
+    const uint32_t w = word_of(v, i >> 1);
+    return half_bits((i & 1) ? (w >> 16) : (w & 0xFFFFu));
+}
+
+// The gate's activation on an fp32 sum (PQ2_ACT_SILU = 0, PQ2_ACT_GELU_TANH = 1).
+// tanh(z) = 1 - 2 / (1 + exp(2z)) turns the GELU into g * sigmoid(2z) with
+// z = sqrt(2/pi) (g + 0.044715 g^3): one exp and one division for both, and
+// the limits (exp -> 0 or inf) come out as g and -0.
+__device__ __forceinline__ float gate_activation(float g, int act) {
+    const float z = act == 0 ? g : 1.5957691216057308f * (g + 0.044715f * g * g * g);
+    return g / (1.0f + expf(-z));
+}
+
+// v rounded to nearest even into element i of `out`.
+__device__ __forceinline__ void store_as(void* out, size_t i, float v, int dtype) {
+    if (dtype == 0) static_cast<__bf16*>(out)[i] = (__bf16)v;
+    else if (dtype == 1) static_cast<_Float16*>(out)[i] = (_Float16)v;
+    else static_cast<float*>(out)[i] = v;
+}
+
+}  // namespace pq2

@@ -24,6 +24,11 @@ inline int src_of_dtype(int dtype) { return dtype == 0 ? kSrcBf16 : dtype == 1 ?
 // the hipGetLastError() that follows our launch reports our launch only.
 inline void clear_stale_error() { (void)hipGetLastError(); }
 
+// Shared by the C ABI sources: PQ2_OK on a gfx950 device (else PQ2_EDEVICE),
+// and the status of a launch (kept for pq2_last_hip_error).
+int api_check_device();
+int api_launch_status(hipError_t e);
+
 // Returns a hipError_t from launching (hipSuccess on success).
 hipError_t launch_prepare(const uint8_t* raw, int64_t stride, int64_t n, int64_t k, uint8_t* planes,
                           hipStream_t stream);

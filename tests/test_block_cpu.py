@@ -1,0 +1,186 @@
+"""The block operators' C ABI without a GPU: the symbols of pq2_block.h are
+exported and bound, and bad arguments are refused on the host (every case
+fails validation or the device check, so nothing is launched)."""
+import ctypes
+import os
+import re
+
+import pytest
+import torch
+
+import block_reference as ref
+import gemm_int8_act_amd as pq2
+from gemm_int8_act_amd.block import BlockNormArgs
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+OK, EINVAL, ESHAPE, EALIGN, EDEVICE = pq2.PQ2_OK, pq2.PQ2_EINVAL, pq2.PQ2_ESHAPE, pq2.PQ2_EALIGN, pq2.PQ2_EDEVICE
+
+# Fake device addresses, never dereferenced: validation fails first.
+A, B, C, D, E, F = (0x7F0000000000 + (i << 36) for i in range(6))
+
+no_gpu = pytest.mark.skipif(torch.cuda.device_count() > 0, reason="the device check passes on a GPU")
+
+
+def test_header_symbols_exported():
+    text = open(os.path.join(ROOT, "include", "pq2_block.h")).read()
+    names = set(re.findall(r"^(?:int|int64_t)\s+(pq2_\w+)\s*\(", text, re.M))
+    assert names == set(pq2.BLOCK_EXPORTED)
+    for name in names:
+        assert hasattr(pq2.lib, name) and hasattr(pq2, name), name
+
+
+def test_args_struct_matches_the_header(tmp_path):
+    """Field order and offsets of the binding's structure, by the C compiler."""
+    import subprocess
+    fields = [f for f, _ in BlockNormArgs._fields_]
+    src = tmp_path / "offsets.c"
+    src.write_text('#include <stddef.h>\n#include <stdio.h>\n#include "pq2_block.h"\nint main(void) {\n'
+                   + "".join(f'printf("%zu\\n", offsetof(pq2_block_norm_args, {f}));\n' for f in fields)
+                   + 'printf("%zu\\n", sizeof(pq2_block_norm_args)); return 0; }\n')
+    exe = tmp_path / "offsets"
+    subprocess.run(["gcc", "-I", os.path.join(ROOT, "include"), str(src), "-o", str(exe)], check=True)
+    got = [int(v) for v in subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout.split()]
+    assert got == [getattr(BlockNormArgs, f).offset for f in fields] + [ctypes.sizeof(BlockNormArgs)]
+
+
+def test_w4_tiles_bytes():
+    f = pq2.pq2_w4_tiles_bytes
+    assert f(10240, 5120, 128) == 10240 * 5120 // 2 + 10240 * 40 * 2
+    assert f(1, 128, 32) == 8192 + 1024
+    assert f(17, 1152, 64) == 2 * 2 * (8192 + 512)
+    for n, k, g in ((0, 128, 128), (1, 100, 128), (1, 0, 64), (1, 1 << 17, 32), ((1 << 30) + 1, 128, 128),
+                    (1, 128, 16), (1, 128, 0), (1, 128, 256)):
+        with pytest.raises(ValueError):
+            f(n, k, g)
+
+
+def test_reference_layout_is_a_permutation():
+    """The scatter of the reference layout read back weight by weight."""
+    n, k, wg = 19, 1152, 64
+    _, scales, c = ref.make_w4(n, k, wg, 3)
+    t = ref.w4_tiles(c, scales, wg)
+    unit = 8192 + 512
+    for row, kk in ((0, 0), (18, 1151), (5, 77), (16, 1024), (7, 200), (3, 95)):
+        base = (row // 16 * 2 + kk // 1024) * unit + kk % 1024 // 128 * 1024
+        lane = row % 16 + 16 * (kk % 64 // 16)
+        u = 2 * (kk % 128 // 64) + kk % 16 // 8
+        byte = int(t[base + 16 * lane + 4 * u + kk % 4])
+        nib = (byte >> 4) if kk % 8 >= 4 else (byte & 15)
+        assert (nib ^ 8) == int(c[row, kk]), (row, kk)
+
+
+def test_prepare_w4_validation():
+    f = pq2.lib.pq2_prepare_w4_tiles
+    assert f(None, 64, B, 1, 4, 128, 128, C, None) == EINVAL
+    assert f(A, 64, None, 1, 4, 128, 128, C, None) == EINVAL
+    assert f(A, 64, B, 1, 4, 128, 128, None, None) == EINVAL
+    assert f(A, 64, B, 1, 4, 128, 48, C, None) == EINVAL
+    assert f(A, 64, B, 1, 0, 128, 128, C, None) == ESHAPE
+    assert f(A, 64, B, 1, 4, 192, 128, C, None) == ESHAPE
+    assert f(A, 63, B, 1, 4, 128, 128, C, None) == ESHAPE
+    assert f(A, 64, B, 3, 4, 128, 32, C, None) == ESHAPE
+    assert f(A, 64, B, 1, 4, 128, 128, C + 8, None) == EALIGN
+    assert f(A, 64, B + 1, 1, 4, 128, 128, C, None) == EALIGN
+    assert f(A, 64, B, 1, 4, 128, 128, A + 128, None) == EINVAL
+    assert f(A, 64, B, 1, 4, 128, 128, B - 16, None) == EINVAL
+
+
+@pytest.mark.parametrize("kind", ["w4", "gated_tiles", "gated_w4"])
+def test_product_validation(kind):
+    def f(q=A, xs=B, w=C, m=1, n=8, k=128, wg=128, y=D, up=E, act=0, dt=2):
+        if kind == "w4":
+            return pq2.lib.pq2_matmul_w4(q, xs, w, m, n, k, wg, y, None)
+        if kind == "gated_w4":
+            return pq2.lib.pq2_gated_matmul_w4(q, xs, w, up, m, n, k, wg, act, y, dt, None)
+        return pq2.lib.pq2_gated_matmul_tiles(q, xs, w, up, m, n, k, act, y, dt, None)
+    for name in ("q", "xs", "w", "y"):
+        assert f(**{name: None}) == EINVAL
+    assert f(m=0) == ESHAPE and f(m=65535 * 16 + 1) == ESHAPE
+    assert f(n=0) == ESHAPE and f(n=(1 << 30) + 1) == ESHAPE
+    assert f(k=0) == ESHAPE and f(k=200) == ESHAPE and f(k=1 << 17) == ESHAPE
+    assert f(q=A + 8) == EALIGN and f(xs=B + 2) == EALIGN and f(w=C + 8) == EALIGN and f(y=D + 2) == EALIGN
+    assert f(y=C + 64) == EINVAL and f(y=A) == EINVAL and f(y=B) == EINVAL
+    if kind != "gated_tiles":
+        assert f(wg=0) == EINVAL and f(wg=16) == EINVAL and f(wg=-128) == EINVAL
+    if kind != "w4":
+        assert f(up=None) == EINVAL and f(up=E + 8) == EALIGN and f(y=E) == EINVAL
+        assert f(act=2) == EINVAL and f(act=-1) == EINVAL and f(dt=3) == EINVAL and f(dt=-1) == EINVAL
+        assert f(y=D + 1, dt=0) == EALIGN
+    if torch.cuda.device_count() == 0:
+        assert f() == EDEVICE and f(m=65535 * 16) == EDEVICE and f(up=C) == EDEVICE
+
+
+@pytest.mark.parametrize("kind", ["w4", "gated_tiles", "gated_w4"])
+def test_linear_validation(kind):
+    def f(x=F, dt=0, stride=128, w=C, m=2, n=8, k=128, wg=64, y=D, up=E, q=A, xs=B):
+        if kind == "w4":
+            return pq2.lib.pq2_linear_w4(x, dt, stride, w, m, n, k, wg, y, q, xs, None)
+        if kind == "gated_w4":
+            return pq2.lib.pq2_gated_linear_w4(x, dt, stride, w, up, m, n, k, wg, 0, y, 0, q, xs, None)
+        return pq2.lib.pq2_gated_linear_tiles(x, dt, stride, w, up, m, n, k, 0, y, 0, q, xs, None)
+    for name in ("x", "q", "xs", "w", "y"):
+        assert f(**{name: None}) == EINVAL
+    assert f(dt=3) == EINVAL and f(stride=127) == ESHAPE and f(m=0) == ESHAPE and f(k=64) == ESHAPE
+    assert f(x=F + 1) == EALIGN and f(dt=2, x=F + 2) == EALIGN and f(q=A + 8) == EALIGN
+    assert f(q=F) == EINVAL and f(xs=F) == EINVAL and f(y=F) == EINVAL    # x overlapped
+    assert f(q=C) == EINVAL and f(xs=C + 64) == EINVAL                    # the weights overlapped
+    assert f(xs=A + 16) == EINVAL and f(y=A) == EINVAL and f(y=B) == EINVAL
+    if kind != "w4":
+        assert f(q=E) == EINVAL and f(xs=E + 64) == EINVAL
+    if torch.cuda.device_count() == 0:
+        assert f() == EDEVICE and f(x=F + 2) == EDEVICE
+
+
+def norm_args(**kw):
+    a = BlockNormArgs()
+    a.r, a.r_stride, a.w, a.r_out, a.r_out_stride = A, 128, B, C, 128
+    a.m, a.k, a.agroup, a.eps, a.alpha = 4, 128, 128, 1e-6, 1.0
+    for name, v in kw.items():
+        setattr(a, name, v)
+    return pq2.lib.pq2_block_norm(ctypes.byref(a), None)
+
+
+def test_block_norm_validation():
+    f = norm_args
+    assert pq2.lib.pq2_block_norm(None, None) == EINVAL
+    assert f(r=None) == EINVAL and f(w=None) == EINVAL and f(r_out=None) == EINVAL
+    assert f(q=D) == EINVAL and f(xs=D) == EINVAL
+    assert f(post_w=D) == EINVAL and f(gate=D) == EINVAL               # no block
+    assert f(r_dtype=3) == EINVAL and f(w_dtype=-1) == EINVAL and f(x_dtype=9) == EINVAL
+    assert f(block=D, block_stride=128, block_dtype=4) == EINVAL
+    assert f(q=D, xs=E, agroup=16) == EINVAL
+    for eps in (0.0, -1e-6, float("inf"), float("nan")):
+        assert f(eps=eps) == EINVAL
+    assert f(alpha=float("nan")) == EINVAL and f(alpha=float("inf")) == EINVAL and f(unit_offset=2) == EINVAL
+    assert f(m=0) == ESHAPE and f(m=1 << 31) == ESHAPE and f(k=64) == ESHAPE and f(k=1 << 17) == ESHAPE
+    assert f(r_stride=127) == ESHAPE and f(r_out_stride=1) == ESHAPE
+    assert f(block=D, block_stride=0) == ESHAPE
+    assert f(block=D, block_stride=128, gate=E, gate_stride=5) == ESHAPE
+    assert f(x_out=D, x_out_stride=100) == ESHAPE
+    assert f(r=A + 1) == EALIGN and f(w=B + 1) == EALIGN and f(r_out=C + 1) == EALIGN
+    assert f(q=D + 4, xs=E) == EALIGN and f(q=D, xs=E + 2) == EALIGN
+    assert f(block=D + 2, block_stride=128, block_dtype=2) == EALIGN
+    assert f(r_out=A + 256) == EINVAL and f(r_out=A, r_out_stride=256) == EINVAL   # partly over r
+    assert f(r_out=B) == EINVAL and f(x_out=A, x_out_stride=128) == EINVAL
+    assert f(x_out=C, x_out_stride=128) == EINVAL and f(q=C, xs=E) == EINVAL and f(q=D, xs=D) == EINVAL
+    assert f(block=C, block_stride=128) == EINVAL
+    if torch.cuda.device_count() == 0:
+        assert f() == EDEVICE and f(r_out=A) == EDEVICE
+        assert f(block=D, block_stride=128, gate=E, gate_stride=0, post_w=F) == EDEVICE
+
+
+@no_gpu
+def test_binding_refuses_host_tensors_and_shapes():
+    t = torch.zeros
+    with pytest.raises(ValueError):
+        pq2.pq2_block_norm(t((2, 128)), t(128), 1e-6, r_out=t((2, 128)))
+    with pytest.raises(ValueError):
+        pq2.pq2_block_norm(t((2, 128)), t(64), 1e-6, r_out=t((2, 128)))
+    with pytest.raises(ValueError):
+        pq2.pq2_block_norm(t((2, 128)), t(128), 1e-6, q=t((2, 128), dtype=torch.int8), xs=t((2, 4)), agroup=16)
+    with pytest.raises(ValueError):
+        pq2.pq2_matmul_w4(t((2, 128), dtype=torch.int8), t((2, 1)), t(9216, dtype=torch.uint8), t((3, 5)), 32)
+    with pytest.raises(ValueError):
+        pq2.pq2_matmul_w4(t((2, 128), dtype=torch.int8), t((2, 1)), t(9215, dtype=torch.uint8), t((2, 5)), 32)
+    with pytest.raises(ValueError):
+        pq2.pq2_linear_w4(t((2, 127)), t(9216, dtype=torch.uint8), t((2, 5)), 32, t((2, 128), dtype=torch.int8), t((2, 1)))

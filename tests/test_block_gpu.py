@@ -1,0 +1,504 @@
+"""The block operators on the GPU against plain 64-bit references: products
+with 4-bit weights, the gated feed-forward product, the block norms.  Bounds
+are those of tests/block_reference.py; outputs are poisoned before a call and
+followed by guard elements that must not change."""
+import functools
+
+import pytest
+import torch
+
+import block_reference as ref
+import workloads
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+DT = {"bf16": torch.bfloat16, "f16": torch.float16, "f32": torch.float32}
+
+
+@functools.lru_cache(maxsize=None)
+def _pq2():
+    import gemm_int8_act_amd as pq2
+    return pq2
+
+
+def announce(msg):
+    print(f"[gpu-case] {msg}", flush=True)
+
+
+class Guarded:
+    """A poisoned contiguous output of a shape, with guard elements behind it."""
+
+    def __init__(self, shape, dtype):
+        self.count = 1
+        for s in shape:
+            self.count *= s
+        value = -77 if dtype == torch.int8 else float("nan")
+        self.all = torch.full((self.count + 64,), value, dtype=dtype, device=DEV)
+        self.all[self.count:] = 42
+        self.t = self.all[:self.count].view(shape)
+
+    def read(self):
+        torch.cuda.synchronize()
+        assert bool((self.all[self.count:] == 42).all()), "wrote behind the output"
+        return self.t.cpu()
+
+
+def within(got, want, bound, what):
+    got = got.double()
+    assert bool(torch.isfinite(got).all()), f"{what}: non-finite output"
+    excess = (got - want).abs() - bound
+    worst = int(excess.argmax())
+    assert float(excess.max()) <= 0, (f"{what}: off by {float((got - want).abs().flatten()[worst]):.3e}, bound "
+                                      f"{float(bound.flatten()[worst]):.3e} at {worst}")
+
+
+def activations(m, k, seed, dtype=torch.bfloat16, pad=0):
+    x = workloads.make_activations(m, k + pad, seed, "normal+outliers").to(dtype)
+    return x
+
+
+def w4(n, k, wg, seed, pad=0):
+    pq2 = _pq2()
+    codes, scales, c = ref.make_w4(n, k, wg, seed, pad)
+    out = torch.full((pq2.pq2_w4_tiles_bytes(n, k, wg),), 0xA5, dtype=torch.uint8, device=DEV)
+    cd, sd = codes.to(DEV), scales.to(DEV)
+    pq2.pq2_prepare_w4_tiles(cd, sd[:, :k // wg], wg, out)
+    return out, c, scales
+
+
+def quantise(x, k):
+    pq2 = _pq2()
+    q = torch.empty((x.shape[0], k), dtype=torch.int8, device=DEV)
+    xs = torch.empty((x.shape[0], k // 128), dtype=torch.float32, device=DEV)
+    pq2.pq2_quantize_act_i8(x.to(DEV), q, xs)
+    return q, xs
+
+
+# ---------------------------------------------------------------- 4-bit layout
+@pytest.mark.parametrize("wg", [128, 64, 32])
+@pytest.mark.parametrize("n,k,pad", [(1, 128, 0), (19, 1152, 0), (37, 384, 5), (256, 5120, 3), (16, 17408, 0)])
+def test_prepare_w4_byte_exact(n, k, pad, wg):
+    announce(f"prepare w4 n={n} k={k} wg={wg} pad={pad}")
+    tiles, c, scales = w4(n, k, wg, n + k, pad)
+    torch.cuda.synchronize()
+    assert torch.equal(tiles.cpu(), ref.w4_tiles(c, scales, wg))
+
+
+# ---------------------------------------------------------------- 4-bit products
+W4_SHAPES = [(1, 1, 128), (1, 200, 512), (2, 17, 384), (3, 33, 1024), (4, 300, 1152), (5, 16, 128), (4, 40, 16384),
+             (9, 150, 2176), (16, 64, 5120), (16, 31, 17408), (17, 100, 640), (33, 70, 5120), (64, 128, 1024),
+             (100, 257, 1152), (131, 40, 3200), (1, 24, 65536), (300, 600, 1280)]
+
+
+@pytest.mark.parametrize("wg", [128, 64, 32])
+@pytest.mark.parametrize("m,n,k", W4_SHAPES)
+def test_matmul_w4(m, n, k, wg):
+    announce(f"matmul w4 m={m} n={n} k={k} wg={wg}")
+    tiles, c, scales = w4(n, k, wg, m + n)
+    x = activations(m, k, m + k)
+    q, xs = quantise(x, k)
+    y = Guarded((m, n), torch.float32)
+    _pq2().pq2_matmul_w4(q, xs, tiles, y.t, wg)
+    want, bound = ref.product(*ref.quantised(x, k), (c - 8).double(), scales, wg)
+    within(y.read(), want, bound, "y")
+
+
+@pytest.mark.parametrize("wg", [128, 64, 32])
+@pytest.mark.parametrize("k", [1152, 17408])
+def test_matmul_w4_columns_do_not_depend_on_the_batch(k, wg):
+    announce(f"w4 batch invariance k={k} wg={wg}")
+    n = 90
+    tiles, _, _ = w4(n, k, wg, 5)
+    q, xs = quantise(activations(16, k, 6), k)
+    whole = torch.empty((16, n), device=DEV)
+    _pq2().pq2_matmul_w4(q, xs, tiles, whole, wg)
+    for m in (1, 2, 3, 4, 5, 11):
+        y = torch.empty((m, n), device=DEV)
+        _pq2().pq2_matmul_w4(q[16 - m:].clone(), xs[16 - m:].clone(), tiles, y, wg)
+        torch.cuda.synchronize()
+        assert torch.equal(y, whole[16 - m:]), m
+
+
+@pytest.mark.parametrize("m", [3, 16, 150])
+def test_w4_extreme_codes(m):
+    """All weights -8 or 7 against codes of +-127: the largest dots, exact as floats."""
+    announce(f"w4 extremes m={m}")
+    n, k, wg = 48, 1024, 128
+    c = torch.zeros((n, k), dtype=torch.uint8)
+    c[n // 2:] = 15
+    tiles = torch.empty(_pq2().pq2_w4_tiles_bytes(n, k, wg), dtype=torch.uint8, device=DEV)
+    scales = torch.full((n, k // wg), 0.5, dtype=torch.float16)
+    _pq2().pq2_prepare_w4_tiles((c[:, 0::2] | (c[:, 1::2] << 4)).contiguous().to(DEV), scales.to(DEV), wg, tiles)
+    x = torch.full((m, k), 127.0).to(torch.bfloat16)
+    x[1::2] *= -1
+    q, xs = quantise(x, k)
+    y = torch.empty((m, n), device=DEV)
+    _pq2().pq2_matmul_w4(q, xs, tiles, y, wg)
+    torch.cuda.synchronize()
+    sign = torch.ones(m, 1)
+    sign[1::2] = -1
+    want = sign * torch.where(torch.arange(n) < n // 2, -8.0, 7.0) * 0.5 * 127 * k
+    assert torch.equal(y.cpu(), want)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("m,n,k,pad", [(1, 50, 1024, 0), (3, 130, 640, 5), (20, 33, 1152, 8)])
+def test_linear_w4_is_quantise_then_matmul(dtype, m, n, k, pad):
+    announce(f"linear w4 {dtype} m={m} pad={pad}")
+    tiles, _, _ = w4(n, k, 64, 9)
+    x = activations(m, k, 4, DT[dtype], pad).to(DEV)
+    q, xs = quantise(x, k)
+    want = torch.empty((m, n), device=DEV)
+    _pq2().pq2_matmul_w4(q, xs, tiles, want, 64)
+    y, qw, sw = Guarded((m, n), torch.float32), torch.zeros_like(q), torch.zeros_like(xs)
+    _pq2().pq2_linear_w4(x, tiles, y.t, 64, qw, sw)
+    assert torch.equal(y.read(), want.cpu())
+
+
+@pytest.mark.parametrize("m", [4, 16, 64])
+def test_w4_a_bad_row_stays_alone(m):
+    """NaN scales in one row of xs reach that row's outputs only (k ends inside a segment)."""
+    announce(f"w4 one bad row m={m}")
+    n, k = 40, 1152
+    tiles, _, _ = w4(n, k, 128, 2)
+    q, xs = quantise(activations(m, k, 3), k)
+    y = torch.empty((m, n), device=DEV)
+    _pq2().pq2_matmul_w4(q, xs, tiles, y, 128)
+    xs[2] = float("nan")
+    z = torch.empty((m, n), device=DEV)
+    _pq2().pq2_matmul_w4(q, xs, tiles, z, 128)
+    torch.cuda.synchronize()
+    rows = [i for i in range(m) if i != 2]
+    assert torch.equal(y[rows], z[rows]) and bool(torch.isnan(z[2]).all())
+
+
+def test_w4_zero_activations():
+    announce("w4 zero activations")
+    tiles, _, _ = w4(30, 640, 32, 1)
+    for m in (1, 7, 40):
+        q, xs = quantise(torch.zeros((m, 640), dtype=torch.bfloat16), 640)
+        y = Guarded((m, 30), torch.float32)
+        _pq2().pq2_matmul_w4(q, xs, tiles, y.t, 32)
+        assert bool((y.read() == 0).all())
+
+
+# ---------------------------------------------------------------- gated product
+def ternary_tiles(n, k, seed):
+    pq2 = _pq2()
+    raw = workloads.make_raw_weights(n, k, seed=seed, codes="ternary+3")
+    tiles = torch.empty(pq2.pq2_tiles_bytes(n, k), dtype=torch.uint8, device=DEV)
+    pq2.pq2_prepare_tiles(torch.from_numpy(raw).to(DEV), n, k, tiles)
+    return tiles, raw
+
+
+GATED_SHAPES = [(1, 1, 128), (1, 200, 1024), (2, 40, 384), (4, 33, 5120), (6, 17, 1152), (16, 100, 2176),
+                (13, 24, 17408), (37, 65, 1152), (70, 130, 640), (129, 300, 1024), (4, 20, 16384)]
+
+
+@pytest.mark.parametrize("act", [0, 1])
+@pytest.mark.parametrize("h", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("wg", [0, 128, 64, 32])
+@pytest.mark.parametrize("m,n,k", GATED_SHAPES)
+def test_gated(m, n, k, wg, h, act):
+    announce(f"gated m={m} n={n} k={k} wg={wg} h={h} act={act}")
+    x = activations(m, k, m + n)
+    q, xs = quantise(x, k)
+    codes = ref.quantised(x, k)
+    out = Guarded((m, n), DT[h])
+    if wg:
+        (wa, ca, sa), (wb, cb, sb) = w4(n, k, wg, 11), w4(n, k, wg, 12)
+        _pq2().pq2_gated_matmul_w4(q, xs, wa, wb, out.t, wg, act)
+        ga, gb = ((ref.product(*codes, (c - 8).double(), s, wg)) for c, s in ((ca, sa), (cb, sb)))
+    else:
+        (wa, ra), (wb, rb) = ternary_tiles(n, k, 21), ternary_tiles(n, k, 22)
+        _pq2().pq2_gated_matmul_tiles(q, xs, wa, wb, out.t, act)
+        ga, gb = (ref.product(*codes, *ref.ternary(r, n, k), 128) for r in (ra, rb))
+    want, bound = ref.gated(*ga, *gb, act, DT[h])
+    within(out.read(), want, bound, "h")
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 50, 1024), (4, 33, 5120), (7, 100, 8192), (16, 20, 17408)])
+def test_gated_tiles_has_the_bits_of_the_two_products(m, n, k):
+    """With large positive gates SiLU(g) = g exactly in FP32, so h = fl(yg * yu) of the library's two matmuls."""
+    announce(f"gated bits m={m} n={n} k={k}")
+    pq2 = _pq2()
+    raw = workloads.make_raw_weights(n, k, seed=5, codes="ternary")
+    raw.reshape(n, k // 128, 34)[:, :, 2:] |= 0xAA        # codes 2 and 3: weights +1 and +2
+    x = activations(m, k, 8).abs() + 0.5
+    gate = torch.empty(pq2.pq2_tiles_bytes(n, k), dtype=torch.uint8, device=DEV)
+    pq2.pq2_prepare_tiles(torch.from_numpy(raw).to(DEV), n, k, gate)
+    up, _ = ternary_tiles(n, k, 6)
+    q, xs = quantise(x, k)
+    yg, yu, h = (torch.empty((m, n), device=DEV) for _ in range(3))
+    pq2.pq2_matmul_small_m_tiles(q, xs, gate, yg)
+    pq2.pq2_matmul_small_m_tiles(q, xs, up, yu)
+    pq2.pq2_gated_matmul_tiles(q, xs, gate, up, h, pq2.ACT_SILU)
+    torch.cuda.synchronize()
+    big = yg > 20                                        # exp(-g) < 2^-25: 1 + exp(-g) = 1
+    assert float(big.float().mean()) > 0.9
+    assert torch.equal(h[big], (yg * yu)[big])
+
+
+@pytest.mark.parametrize("m", [2, 12, 80])
+def test_gated_one_matrix_for_both_and_linear(m):
+    announce(f"gated shared matrix m={m}")
+    pq2 = _pq2()
+    n, k = 60, 1152
+    x = activations(m, k, 3, torch.float16, 8).to(DEV)
+    q, xs = quantise(x, k)
+    for wg in (0, 32):
+        w = w4(n, k, wg, 4)[0] if wg else ternary_tiles(n, k, 4)[0]
+        a, b = (torch.empty((m, n), dtype=torch.bfloat16, device=DEV) for _ in range(2))
+        qw, sw = torch.empty_like(q), torch.empty_like(xs)
+        if wg:
+            pq2.pq2_gated_matmul_w4(q, xs, w, w, a, wg, pq2.ACT_GELU_TANH)
+            pq2.pq2_gated_linear_w4(x, w, w, b, wg, qw, sw, pq2.ACT_GELU_TANH)
+        else:
+            pq2.pq2_gated_matmul_tiles(q, xs, w, w, a, pq2.ACT_GELU_TANH)
+            pq2.pq2_gated_linear_tiles(x, w, w, b, qw, sw, pq2.ACT_GELU_TANH)
+        torch.cuda.synchronize()
+        assert torch.equal(a, b) and bool(torch.isfinite(a).all())
+
+
+@pytest.mark.parametrize("act", [0, 1])
+def test_gated_far_ends_of_the_activation(act):
+    """Gates far below and above zero: act(g) goes to 0 and g, never NaN."""
+    announce(f"gated extremes act={act}")
+    pq2 = _pq2()
+    n, k, m = 32, 1024, 4
+    w, _, _ = w4(n, k, 128, 8)
+    x = activations(m, k, 5).float() * torch.tensor([1.0, 1e3, 1e8, 1e16])[:, None]
+    q, xs = quantise(x, k)
+    y, h = torch.empty((m, n), device=DEV), torch.empty((m, n), device=DEV)
+    pq2.pq2_matmul_w4(q, xs, w, y, 128)
+    pq2.pq2_gated_matmul_w4(q, xs, w, w, h, 128, act)
+    torch.cuda.synchronize()
+    assert bool(torch.isfinite(h).all())
+    far = y.abs() > 200
+    assert bool(far.any())
+    assert torch.equal(h[far], torch.where(y > 0, y * y, torch.zeros_like(y))[far].abs())
+
+
+# ---------------------------------------------------------------- block norm
+def rand(shape, seed, dtype, mul=1.0, add=0.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(shape, generator=g) * mul + add).to(dtype)
+
+
+NORM_CASES = [
+    # m, k, r, block, w, x, post, gate, unit_offset, agroup
+    (1, 128, "bf16", "f32", "bf16", "bf16", False, None, False, 128),
+    (3, 5120, "bf16", "f32", "bf16", "bf16", True, "row", False, 128),
+    (2, 1152, "f32", "f32", "f32", "bf16", True, "full", True, 32),
+    (5, 384, "f16", "f16", "f16", "f16", False, "full", False, 64),
+    (4, 8320, "bf16", "bf16", "f32", "f32", True, None, True, 128),
+    (2, 17408, "f32", "bf16", "bf16", "f32", False, "row", False, 64),
+    (1, 65536, "bf16", "f32", "bf16", "bf16", True, "full", False, 32),
+    (3, 20480, "f16", "f32", "bf16", "bf16", True, "row", False, 128),
+    (257, 640, "bf16", "f32", "bf16", "bf16", True, "full", False, 128),
+    (3, 5120, "bf16", None, "bf16", "bf16", False, None, False, 128),
+    (2, 256, "f32", None, "bf16", "f16", False, None, True, 32),
+]
+
+
+def check_norm(case, pad=0, shift=0, in_place=False, seed=1):
+    m, k, r, b, w, x, post, gate, unit, ag = case
+    pq2 = _pq2()
+
+    def rows(t):
+        """The rows of t inside a larger buffer: row stride k + pad, base shifted by `shift` elements."""
+        wide = torch.full((m * (k + pad) + shift + 16,), 7.0, dtype=t.dtype, device=DEV)
+        v = wide[shift:shift + m * (k + pad)].view(m, k + pad)[:, :k]
+        v.copy_(t)
+        return v
+    rr = rand((m, k), seed, DT[r], 1.5)
+    kw = {}
+    if b:
+        kw["block"] = rand((m, k), seed + 1, DT[b], 0.7)
+    mean = 0.0 if unit else 1.0
+    if post:
+        kw["post_w"] = rand((k,), seed + 2, DT[w], 0.1, mean)
+    if gate:
+        kw["gate"] = rand((k,) if gate == "row" else (m, k), seed + 3, DT[w], 0.5)
+    ww = rand((k,), seed + 4, DT[w], 0.1, mean)
+    want_r, want_x = ref.block_norm(rr, ww, 1e-5, alpha=0.37, unit_offset=unit, x_dtype=DT[x], **kw)
+
+    dev = {n: (rows(t) if t.dim() == 2 else t.to(DEV)) for n, t in kw.items()}
+    rd = rows(rr)
+    r_out = rd if in_place else rows(torch.full((m, k), float("nan"), dtype=DT[r]))
+    x_out = rows(torch.full((m, k), float("nan"), dtype=DT[x]))
+    q, xs = Guarded((m, k), torch.int8), Guarded((m, k // ag), torch.float32)
+    pq2.pq2_block_norm(rd, ww.to(DEV), 1e-5, alpha=0.37, unit_offset=unit, r_out=r_out, x_out=x_out, q=q.t, xs=xs.t,
+                       agroup=ag, **dev)
+    torch.cuda.synchronize()
+    assert torch.equal(r_out.cpu(), want_r), "r'"
+    assert torch.equal(x_out.cpu(), want_x), "x"
+    q2 = torch.empty((m, k), dtype=torch.int8, device=DEV)
+    s2 = torch.empty((m, k // ag), dtype=torch.float32, device=DEV)
+    pq2.pq2_quantize_act_i8_g(x_out, q2, s2, ag)
+    assert torch.equal(q.read(), q2.cpu()) and torch.equal(xs.read(), s2.cpu())
+    want_q, want_s = ref.quantised(want_x, k, ag)
+    assert torch.equal(q2.cpu().double().view(m, -1, ag), want_q) and torch.equal(s2.cpu().double(), want_s)
+    if pad:
+        for t in (r_out, x_out):
+            between = t.as_strided((m - 1, pad), (k + pad, 1), t.storage_offset() + k)
+            assert bool((between == 7.0).all()), "wrote between the rows"
+
+
+@pytest.mark.parametrize("case", NORM_CASES, ids=lambda c: "-".join(str(v) for v in c))
+def test_block_norm_bits(case):
+    announce(f"block norm {case}")
+    check_norm(case)
+
+
+@pytest.mark.parametrize("pad,shift", [(8, 0), (16, 8), (3, 1), (0, 1), (5, 0)])
+@pytest.mark.parametrize("case", NORM_CASES[1:4], ids=lambda c: f"{c[0]}-{c[1]}-{c[2]}")
+def test_block_norm_strides(case, pad, shift):
+    announce(f"block norm pad={pad} shift={shift} {case}")
+    check_norm(case, pad, shift)
+
+
+@pytest.mark.parametrize("case", NORM_CASES[:5], ids=lambda c: f"{c[0]}-{c[1]}-{c[2]}")
+def test_block_norm_in_place(case):
+    announce(f"block norm in place {case}")
+    check_norm(case, in_place=True)
+
+
+def test_block_norm_single_outputs():
+    """Each output alone has the bits it has beside the others."""
+    announce("block norm single outputs")
+    pq2 = _pq2()
+    m, k = 5, 1152
+    r, b = rand((m, k), 1, torch.bfloat16).to(DEV), rand((m, k), 2, torch.float32).to(DEV)
+    w = rand((k,), 3, torch.bfloat16, 0.1, 1).to(DEV)
+    new = lambda dt: torch.empty((m, k), dtype=dt, device=DEV)  # noqa: E731
+    ro, xo, q = new(torch.bfloat16), new(torch.bfloat16), new(torch.int8)
+    xs = torch.empty((m, 9), device=DEV)
+    pq2.pq2_block_norm(r, w, 1e-6, block=b, post_w=w, r_out=ro, x_out=xo, q=q, xs=xs)
+    r1, x1, q1, s1 = new(torch.bfloat16), new(torch.bfloat16), new(torch.int8), torch.empty_like(xs)
+    pq2.pq2_block_norm(r, w, 1e-6, block=b, post_w=w, r_out=r1)
+    pq2.pq2_block_norm(r, w, 1e-6, block=b, post_w=w, x_out=x1)
+    pq2.pq2_block_norm(r, w, 1e-6, block=b, post_w=w, q=q1, xs=s1)
+    torch.cuda.synchronize()
+    assert torch.equal(ro, r1) and torch.equal(xo, x1) and torch.equal(q, q1) and torch.equal(xs, s1)
+
+
+def test_block_norm_zero_and_tiny_rows():
+    announce("block norm zero and tiny rows")
+    pq2 = _pq2()
+    k = 384
+    r = torch.zeros((4, k), dtype=torch.float32)
+    r[1] = 2.0 ** -140
+    r[2, 5] = 3e38
+    r[3] = 1e-30
+    w = torch.ones(k, dtype=torch.float32)
+    want_r, want_x = ref.block_norm(r, w, 1e-6)
+    x, q, xs = torch.empty((4, k), device=DEV), torch.empty((4, k), dtype=torch.int8, device=DEV), torch.empty((4, 3), device=DEV)
+    pq2.pq2_block_norm(r.to(DEV), w.to(DEV), 1e-6, x_out=x, q=q, xs=xs)
+    torch.cuda.synchronize()
+    assert torch.equal(x.cpu(), want_x)
+    want_q, want_s = ref.quantised(want_x, k)
+    assert torch.equal(q.cpu().double().view(4, 3, 128), want_q) and torch.equal(xs.cpu().double(), want_s)
+
+
+def test_block_norm_gate_broadcast_by_a_zero_stride():
+    announce("block norm expanded gate")
+    pq2 = _pq2()
+    m, k = 6, 640
+    r, b = rand((m, k), 1, torch.float16).to(DEV), rand((m, k), 2, torch.float32).to(DEV)
+    w, g = rand((k,), 3, torch.float16, 0.1, 1).to(DEV), rand((k,), 4, torch.float16).to(DEV)
+    a, c = torch.empty_like(r), torch.empty_like(r)
+    pq2.pq2_block_norm(r, w, 1e-6, block=b, gate=g, x_out=a)
+    pq2.pq2_block_norm(r, w, 1e-6, block=b, gate=g.expand(m, k), x_out=c)
+    torch.cuda.synchronize()
+    assert torch.equal(a, c)
+
+
+# ---------------------------------------------------------------- together
+class Block:
+    """A feed-forward block between two norms, as a decoder runs it: gated
+    product on ternary weights, down product on 4-bit weights."""
+
+    def __init__(self, m, hidden, inner, wg, seed=1):
+        pq2 = _pq2()
+        self.m, self.wg = m, wg
+        self.gate, self.raw_gate = ternary_tiles(inner, hidden, seed)
+        self.up, self.raw_up = ternary_tiles(inner, hidden, seed + 1)
+        self.down, self.c, self.s = w4(hidden, inner, wg, seed + 2)
+        self.w_in, self.w_out, self.w_post = (rand((hidden,), seed + i, torch.bfloat16, 0.1, 1).to(DEV)
+                                              for i in (3, 4, 5))
+        e = lambda shape, dt: torch.empty(shape, dtype=dt, device=DEV)  # noqa: E731
+        self.q, self.xs = e((m, hidden), torch.int8), e((m, hidden // 128), torch.float32)
+        self.qh, self.xh = e((m, inner), torch.int8), e((m, inner // 128), torch.float32)
+        self.h, self.y = e((m, inner), torch.bfloat16), e((m, hidden), torch.float32)
+        self.r, self.x = e((m, hidden), torch.bfloat16), e((m, hidden), torch.bfloat16)
+
+    def run(self, r, stream=None):
+        pq2 = _pq2()
+        pq2.pq2_block_norm(r, self.w_in, 1e-6, q=self.q, xs=self.xs, stream=stream)
+        pq2.pq2_gated_matmul_tiles(self.q, self.xs, self.gate, self.up, self.h, stream=stream)
+        pq2.pq2_linear_w4(self.h, self.down, self.y, self.wg, self.qh, self.xh, stream=stream)
+        pq2.pq2_block_norm(r, self.w_out, 1e-6, block=self.y, post_w=self.w_post, alpha=0.5, r_out=self.r,
+                           x_out=self.x, stream=stream)
+
+    def check(self, r):
+        """Every step against its reference on the step's own inputs."""
+        torch.cuda.synchronize()
+        hidden, inner = self.q.shape[1], self.qh.shape[1]
+        _, x = ref.block_norm(r.cpu(), self.w_in.cpu(), 1e-6)
+        q, xs = ref.quantised(x, hidden)
+        assert torch.equal(self.q.cpu().double().view(q.shape), q) and torch.equal(self.xs.cpu().double(), xs)
+        parts = [ref.product(q, xs, *ref.ternary(w, inner, hidden), 128) for w in (self.raw_gate, self.raw_up)]
+        within(self.h.cpu(), *ref.gated(*parts[0], *parts[1], 0, torch.bfloat16), "h")
+        within(self.y.cpu(), *ref.product(*ref.quantised(self.h.cpu(), inner), (self.c - 8).double(), self.s, self.wg),
+               "y")
+        want_r, want_x = ref.block_norm(r.cpu(), self.w_out.cpu(), 1e-6, block=self.y.cpu(),
+                                        post_w=self.w_post.cpu(), alpha=0.5)
+        assert torch.equal(self.r.cpu(), want_r) and torch.equal(self.x.cpu(), want_x)
+
+
+@pytest.mark.parametrize("m", [1, 4, 16, 70])
+def test_block_together(m):
+    announce(f"block together m={m}")
+    b = Block(m, 640, 1152, 32)
+    r = rand((m, 640), 9, torch.bfloat16).to(DEV)
+    b.run(r)
+    b.check(r)
+
+
+def test_block_on_another_stream():
+    announce("block on a side stream")
+    b = Block(3, 384, 512, 128)
+    r = rand((3, 384), 9, torch.bfloat16).to(DEV)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    b.run(r, stream=side)
+    side.synchronize()
+    b.check(r)
+    with torch.cuda.stream(side):
+        b.r.zero_()
+        b.run(r)
+    side.synchronize()
+    b.check(r)
+
+
+@pytest.mark.parametrize("m", [2, 9, 40])
+def test_block_captured_and_replayed(m):
+    """Replays with new inputs, eager runs of the same buffers between them."""
+    announce(f"block captured m={m}")
+    b, eager = Block(m, 640, 1152, 64), Block(m, 640, 1152, 64)
+    r = rand((m, 640), 9, torch.bfloat16).to(DEV)
+    b.run(r)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        b.run(r)
+    for i in range(4):
+        r.copy_(rand((m, 640), 20 + i, torch.bfloat16).to(DEV))
+        graph.replay()
+        eager.run(r)
+        torch.cuda.synchronize()
+        for name in ("q", "xs", "h", "y", "r", "x"):
+            assert torch.equal(getattr(b, name), getattr(eager, name)), (i, name)
+    b.check(r)
