@@ -21,7 +21,8 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libpq2.so")
 BUILD_DIR = os.path.join(HERE, "_build")
 SOURCES = ["api.hip", "quantize.hip", "small_m.hip", "small_m_wg.hip", "tiles.hip", "prefill.hip", "probe.hip",
-           "block_api.hip", "w4.hip", "block_small_m.hip", "norm.hip"]
+           "block_api.hip", "w4.hip", "block_small_m.hip", "block_prefill.hip",
+           "norm.hip"]
 ARCH = "gfx950"
 
 COMMON_FLAGS = [
@@ -46,6 +47,7 @@ def _hipcc() -> str:
 # accumulators out of AGPRs and saves one register move per output and group.
 EXTRA_FLAGS = {
     "prefill.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+    "block_prefill.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
 }
 
 

@@ -57,7 +57,8 @@ int check_product(const int8_t* q, const float* xs, const void* w0, const void* 
 
 int launch_product(const pq2::BlockMatmul& p) {
     if (int rc = pq2::api_check_device()) return rc;
-    return pq2::api_launch_status(pq2::launch_block_small_m(p));
+    return pq2::api_launch_status(pq2::block_takes_small_m(p) ? pq2::launch_block_small_m(p)
+                                                              : pq2::launch_block_prefill(p));
 }
 
 int product(const int8_t* q, const float* xs, const void* w0, const void* w1, int64_t m, int64_t n, int64_t k,
