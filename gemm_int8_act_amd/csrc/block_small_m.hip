@@ -1,14 +1,14 @@
 // block_small_m.hip -- decode engine of the block operators: products with
 // 4-bit weights and the gated feed-forward product for few columns.
 //
-// One workgroup per tile of 16 weight rows (gated: the gate tile and the up
-// tile of the same rows); its waves take consecutive slices of k, whole
-// segments of 1024.  A wave loads its segment's activations, scales and codes
-// (every code load one contiguous kilobyte), forms each weight group's exact
-// dot with v_mfma_i32_16x16x64_i8 and adds one FP32 term per activation
-// group; the slices are added in index order by the whole workgroup, which
-// also applies the gate's activation, so the two products of a gated call
-// never reach memory.  The order of a column's sum depends on k only.
+// A workgroup owns whole tiles of 16 weight rows (gated: the gate tile and
+// the up tile of the same rows), one after the other; its waves split k into
+// consecutive slices of whole 1024-weight segments.  Per segment a wave forms
+// each weight group's exact dot with v_mfma_i32_16x16x64_i8 and adds one FP32
+// term per activation group; the slices are added in index order by the
+// whole workgroup, which also applies the gate's activation, so the two
+// products of a gated call never reach memory.  The order of a column's sum
+// depends on k only.
 //
 //  ternary: cls[c] = fma(float(dot) * xs, ws, cls[c]) per group class c and
 //           ((c0+c4)+(c1+c5))+((c2+c6)+(c3+c7)) per slice: the order of
@@ -16,16 +16,23 @@
 //  w4:      acc = fma(t, xs, acc) over the activation groups in k order, t =
 //           the weight groups' float(dot) * ws added in k order.
 //
-// Up to four columns (WIDE false): the four A rows 4c .. 4c+3 of the matrix
+// What bounds it is the weight stream, so the kernel keeps it running: a code
+// register is loaded again, for the wave's next (tile, segment), as soon as
+// its codes are decoded, so a wave holds a segment's loads in flight from its
+// start to its end, through the reduction of one tile and into the next.
+// The activations are staged once per workgroup, not once per tile.
+//
+// Up to four columns (MC 1, 2, 4): the four A rows 4c .. 4c+3 of the matrix
 // core all belong to column c, so a lane owns one output (column lane/16).
 // With S = 2 or 4 weight groups per 128 the rows are told apart by masking:
 // row 4c+r keeps only weight group r, and one pair of MFMAs gives the dots
-// of all S groups in the four result registers.  Activations come through a
-// private LDS region (one load per column).
-// Up to sixteen columns (WIDE): A row = column, read straight from memory in
-// operand order; a lane owns four outputs.
+// of all S groups in the four result registers.  Activations sit in LDS.
+// Up to sixteen columns (MC 16): A row = column, held in registers in operand
+// order (read again per segment where a wave has several); a lane owns four
+// outputs.
 #include "block_internal.h"
-#include "small_m_common.h"
+
+#include <algorithm>
 
 namespace pq2 {
 
@@ -37,18 +44,34 @@ struct SmallArgs {
     const uint8_t* w0;
     const uint8_t* w1;
     void* out;
-    int n, k, groups, s8, nseg, per_wave, mtotal, act, out_dtype, region;
+    int n, k, groups, s8, per_wave, tiles, mtotal, act, out_dtype, part;
 };
 
-constexpr int kColPitch = 1024 + 64;  // four columns' reads fall in distinct banks
+// Waves k is split over at most: registers for three waves per SIMD remain at
+// twelve.  (The ternary kernels keep the split of small_m_tiles_kernel.)
+constexpr int kW4Waves = 12;
 
-template <int FMT, int S, int NB, bool WIDE, int MAXW>
+// Groups of codes a wave holds in flight, and of the activations where they
+// are read per segment (loads complete in order, so both run the same distance
+// ahead).  Eight, a whole segment, is slower: gated ternary at one column 14.3
+// against 12.2 us, and twice the registers.
+constexpr int kRing = 4;
+
+constexpr int kColPitch = 1024 + 64;  // four columns' reads fall in distinct banks
+// LDS per wave and segment: the columns' codes and scales (MC <= 4), or the
+// scales alone, [group][column].
+__host__ __device__ constexpr int seg_bytes(int mc) { return mc <= 4 ? mc * (kColPitch + 32) : 512; }
+
+template <int FMT, int S, int NB, int MC, bool MULTI, int MAXW>
 __global__ __launch_bounds__(64 * MAXW) void block_small_m_kernel(SmallArgs a) {
 #pragma clang fp contract(off)
+    constexpr bool WIDE = MC == 16;
     constexpr int UNIT = block_unit(FMT, S);
     constexpr int CODES = block_code_bytes(FMT);
     constexpr int CB = CODES / 1024;   // code loads per segment
-    constexpr int MC = WIDE ? 16 : 4;
+    constexpr int GPL = 8 / CB;        // groups per code load
+    constexpr int RG = kRing;
+    constexpr int RL = RG / GPL;       // code registers
     constexpr int R = WIDE ? 4 : 1;    // outputs per lane
     constexpr int C = FMT == kFmtTernary ? 8 : 1;  // accumulators per output
     extern __shared__ __align__(16) unsigned char smem[];
@@ -57,19 +80,112 @@ __global__ __launch_bounds__(64 * MAXW) void block_small_m_kernel(SmallArgs a) {
     const int lane = threadIdx.x & 63;
     const int j = lane & 15;
     const int kb = lane >> 4;
-    const int tile = blockIdx.x;
     const int m0 = blockIdx.y * MC;
     const int mcount = min(MC, a.mtotal - m0);
     const int seg_begin = wave * a.per_wave;
-    const int seg_end = min(seg_begin + a.per_wave, a.nseg);
+    const int seg_end = min(seg_begin + a.per_wave, a.s8);
 
-    const size_t tile_off = (size_t)tile * a.s8 * UNIT;
-    const uint32_t tile_bytes = (uint32_t)(a.s8 * UNIT);
-    const __amdgpu_buffer_rsrc_t w_rs[2] = {make_rsrc(a.w0 + tile_off, tile_bytes),
-                                            make_rsrc(NB == 2 ? a.w1 + tile_off : nullptr, NB == 2 ? tile_bytes : 0u)};
     const auto q_rs = make_rsrc(a.q + (size_t)m0 * a.k, (uint32_t)(mcount * a.k));
     const auto xs_rs = make_rsrc(a.xs + (size_t)m0 * a.groups, (uint32_t)(mcount * a.groups * 4));
-    unsigned char* region = smem + (size_t)wave * a.region;
+    // Per wave: its segments' activations; then two sets of slice sums.
+    unsigned char* region = smem + (size_t)wave * a.per_wave * seg_bytes(MC);
+    float* parts = reinterpret_cast<float*>(smem + (size_t)nwaves * a.per_wave * seg_bytes(MC));
+
+    // Loads of one unit (tile, segment); past the last tile they read nothing.
+    uint4 cw[NB][RL], sc[NB][S], sn[NB][S], av[WIDE ? (MULTI ? 2 * RG : 16) : 1];
+    // Codes at `codes` + a scalar offset, scales at `scales`; both are past any
+    // range where there is no such tile.
+    struct Unit {
+        __amdgpu_buffer_rsrc_t rs[2];
+        uint32_t codes, scales;
+    };
+    auto unit_of = [&](int tile, int s) {
+        Unit u;
+        const bool ok = tile < a.tiles;
+        const size_t off = ((size_t)(ok ? tile : 0) * a.s8 + s) * UNIT;
+        u.rs[0] = make_rsrc(a.w0 + off, UNIT);
+        u.rs[1] = make_rsrc(NB == 2 ? a.w1 + off : a.w0, UNIT);
+        u.codes = ok ? 16u * lane : kBufferOOB;
+        u.scales = ok ? (uint32_t)(16 * S * j) : kBufferOOB;
+        return u;
+    };
+    auto load_codes = [&](const Unit& u, int i) {
+#pragma unroll
+        for (int b = 0; b < NB; ++b) cw[b][i % RL] = buf_load16s<kAuxNonTemporal>(u.rs[b], u.codes, 1024u * i);
+    };
+    auto load_scales = [&](const Unit& u, int i, uint4 (&to)[NB][S]) {
+#pragma unroll
+        for (int b = 0; b < NB; ++b) to[b][i] = buf_load16s<kAuxNonTemporal>(u.rs[b], u.scales, CODES + 16u * i);
+    };
+    // WIDE: step i (64 weights, two per group) of segment s.
+    const uint32_t a_off = j < mcount ? (uint32_t)(j * a.k + 16 * kb) : kBufferOOB;
+    auto load_a = [&](int s, int i) {
+        const int off = s * 1024 + 64 * i;
+        av[MULTI ? i % (2 * RG) : i] = buf_load16s(q_rs, off < a.k ? a_off : kBufferOOB, off < a.k ? (uint32_t)off : 0u);
+    };
+
+    // 1. Stage the wave's activations.  The loads of the first PRE segments go
+    //    out first, then the first unit's weights, then the staging writes, so
+    //    the weight stream starts at once.
+    constexpr int PRE = MULTI && !WIDE ? 2 : 1;
+    struct Staged {
+        uint4 v[WIDE ? 1 : MC];
+        uint2 x;
+    };
+    auto stage_load = [&](int s, Staged& t) {
+        const int g0 = 8 * s;
+        if constexpr (WIDE) {
+            // Lane (column j, groups 2 kb and 2 kb + 1).
+            const bool ok = j < mcount && g0 + 2 * kb < a.groups;
+            t.x = buf_load8(xs_rs, ok ? (uint32_t)((j * a.groups + g0 + 2 * kb) * 4) : kBufferOOB);
+        } else {
+            // Lane 8 c + g: the scale of column c, group g.
+            const bool ok = lane < 8 * mcount && g0 + (lane & 7) < a.groups;
+            t.x.x = buf_load4(xs_rs, ok ? (uint32_t)(((lane >> 3) * a.groups + g0 + (lane & 7)) * 4) : kBufferOOB);
+            const int off = s * 1024 + 16 * lane;
+#pragma unroll
+            for (int i = 0; i < MC; ++i)
+                t.v[i] = buf_load16(q_rs, i < mcount && off < a.k ? (uint32_t)(i * a.k + off) : kBufferOOB);
+        }
+    };
+    auto stage_store = [&](int s, const Staged& t) {
+        unsigned char* to = region + (s - seg_begin) * seg_bytes(MC);
+        if constexpr (WIDE) {
+            float* xl = reinterpret_cast<float*>(to);
+            xl[(2 * kb) * 16 + j] = __uint_as_float(t.x.x);
+            xl[(2 * kb + 1) * 16 + j] = 8 * s + 2 * kb + 1 < a.groups ? __uint_as_float(t.x.y) : 0.0f;
+        } else {
+#pragma unroll
+            for (int i = 0; i < MC; ++i) *reinterpret_cast<uint4*>(to + i * kColPitch + 16 * lane) = t.v[i];
+            if (lane < 8 * MC) *reinterpret_cast<uint32_t*>(to + MC * kColPitch + 4 * lane) = t.x.x;
+        }
+    };
+    {
+        Staged t[PRE];
+#pragma unroll
+        for (int i = 0; i < PRE; ++i)
+            if (i == 0 || seg_begin + i < seg_end) stage_load(seg_begin + i, t[i]);
+        const Unit u = unit_of(blockIdx.x, seg_begin);
+        if constexpr (WIDE) {
+#pragma unroll
+            for (int i = 0; i < (MULTI ? 2 * RG : 16); ++i) load_a(seg_begin, i);
+        }
+#pragma unroll
+        for (int i = 0; i < S; ++i) load_scales(u, i, sc);
+#pragma unroll
+        for (int i = 0; i < RL; ++i) load_codes(u, i);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < PRE; ++i)
+            if (i == 0 || seg_begin + i < seg_end) stage_store(seg_begin + i, t[i]);
+        for (int s = seg_begin + PRE; s < seg_end; ++s) {
+            stage_load(s, t[0]);
+            stage_store(s, t[0]);
+        }
+    }
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 
     // Rows of the A operand that keep weight group r = j & 3 of step h.
     uint32_t keep[2] = {~0u, ~0u};
@@ -78,93 +194,53 @@ __global__ __launch_bounds__(64 * MAXW) void block_small_m_kernel(SmallArgs a) {
         for (int h = 0; h < 2; ++h) keep[h] = (j & 3) == (S == 2 ? h : 2 * h + (kb >> 1)) ? ~0u : 0u;
     }
     const uint32_t low_half = kb < 2 ? ~0u : 0u;  // WIDE, S = 4: lanes of the first 32 weights of a step
+    const int a_col = (j >> 2) < mcount ? (j >> 2) : 0;
+    const int x_col = kb < mcount ? kb : 0;
 
     float acc[NB][C][R];
-#pragma unroll
-    for (int b = 0; b < NB; ++b)
-#pragma unroll
-        for (int c = 0; c < C; ++c)
-#pragma unroll
-            for (int r = 0; r < R; ++r) acc[b][c][r] = 0.0f;
-
-    for (int s = seg_begin; s < seg_end; ++s) {
-        // 1. Loads: scales of the activations, activations, then the weights.
-        const int g0 = 8 * s;
-        uint4 xv[2];
-        uint2 xw;
-        uint4 av[WIDE ? 16 : 4];
-        if constexpr (WIDE) {
-            xw = buf_load8(xs_rs, j < mcount && g0 + 2 * kb < a.groups ? (uint32_t)((j * a.groups + g0 + 2 * kb) * 4)
-                                                                       : kBufferOOB);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const int off = s * 1024 + 64 * i + 16 * kb;
-                av[i] = buf_load16(q_rs, j < mcount && off < a.k ? (uint32_t)(j * a.k + off) : kBufferOOB);
-            }
-        } else {
-            const uint32_t xoff = (uint32_t)((min(kb, mcount - 1) * a.groups + g0) * 4);
-            xv[0] = buf_load16(xs_rs, xoff);
-            xv[1] = buf_load16(xs_rs, xoff + 16u);
-            const int off = s * 1024 + 16 * lane;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (i < mcount) av[i] = buf_load16(q_rs, off < a.k ? (uint32_t)(i * a.k + off) : kBufferOOB);
+    // One unit: group dots and terms; the loads of the next unit go out as this
+    // one's registers become free.  (S = 4: eight groups use four scale
+    // registers in turn, so they stream like the codes; else a second set.)
+    auto body = [&](int tile, int s, int next_tile, int next_s) {
+        const unsigned char* from = region + (s - seg_begin) * seg_bytes(MC);
+        const Unit next = unit_of(next_tile, next_s);
+        const Unit cur = RG < 8 ? unit_of(tile, s) : next;
+        float4 xv[2];
+        if constexpr (!WIDE) {
+            const float4* x = reinterpret_cast<const float4*>(from + MC * kColPitch + 32 * x_col);
+            xv[0] = x[0];
+            xv[1] = x[1];
         }
-        uint4 sc[NB][S], cw[NB][CB];
-        const uint32_t unit = (uint32_t)(s * UNIT);
+        if constexpr (S != 4) {
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
-#pragma unroll
-            for (int i = 0; i < S; ++i)
-                sc[b][i] = buf_load16<kAuxNonTemporal>(w_rs[b], unit + CODES + 16 * S * j + 16 * i);
-#pragma unroll
-        for (int i = 0; i < CB; ++i)
-#pragma unroll
-            for (int b = 0; b < NB; ++b)
-                cw[b][i] = buf_load16<kAuxNonTemporal>(w_rs[b], unit + 1024 * i + 16 * lane);
-
-        // 2. Stage.
-        if constexpr (WIDE) {
-            float* xl = reinterpret_cast<float*>(region);
-            xl[(2 * kb) * 16 + j] = __uint_as_float(xw.x);
-            xl[(2 * kb + 1) * 16 + j] = g0 + 2 * kb + 1 < a.groups ? __uint_as_float(xw.y) : 0.0f;
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (i < mcount) *reinterpret_cast<uint4*>(region + i * kColPitch + 16 * lane) = av[i];
+            for (int i = 0; i < S; ++i) load_scales(next, i, sn);
         }
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-
-        // 3. Group dots and terms.
-        const int col = WIDE ? 0 : ((j >> 2) < mcount ? (j >> 2) : 0);
-        const unsigned char* a_base = region + col * kColPitch + 16 * kb;
+        const unsigned char* a_base = from + a_col * kColPitch + 16 * kb;
 #pragma unroll
         for (int g = 0; g < 8; ++g) {
             v4i A[2];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 uint4 v;
-                if constexpr (WIDE) v = av[2 * g + h];
+                if constexpr (WIDE) v = av[MULTI ? (2 * g + h) % (2 * RG) : 2 * g + h];
                 else v = *reinterpret_cast<const uint4*>(a_base + 128 * g + 64 * h);
                 A[h] = v4i{(int)(v.x & keep[h]), (int)(v.y & keep[h]), (int)(v.z & keep[h]), (int)(v.w & keep[h])};
             }
             float xg[R];
             if constexpr (WIDE) {
-                const float4 v = *reinterpret_cast<const float4*>(region + (g * 16 + 4 * kb) * 4);
+                const float4 v = *reinterpret_cast<const float4*>(from + (g * 16 + 4 * kb) * 4);
                 xg[0] = v.x; xg[1] = v.y; xg[2] = v.z; xg[3] = v.w;
             } else {
-                // Past the last group the loads hold the next column's scales.
-                xg[0] = g0 + g < a.groups ? __uint_as_float(word_of(xv[g >> 2], g & 3)) : 0.0f;
+                const float4& v = xv[g >> 2];
+                xg[0] = (g & 3) == 0 ? v.x : (g & 3) == 1 ? v.y : (g & 3) == 2 ? v.z : v.w;
             }
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
                 v4i B[2];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    if constexpr (FMT == kFmtTernary) B[h] = ternary_operand(word_of(cw[b][g >> 1], 2 * (g & 1) + h));
-                    else B[h] = w4_operand(word_of(cw[b][g], 2 * h), word_of(cw[b][g], 2 * h + 1));
+                    if constexpr (FMT == kFmtTernary) B[h] = ternary_operand(word_of(cw[b][(g >> 1) % RL], 2 * (g & 1) + h));
+                    else B[h] = w4_operand(word_of(cw[b][g % RL], 2 * h), word_of(cw[b][g % RL], 2 * h + 1));
                 }
                 float dot[S][R];  // float of the weight groups' dots
                 if constexpr (!WIDE || S == 1) {
@@ -203,73 +279,118 @@ __global__ __launch_bounds__(64 * MAXW) void block_small_m_kernel(SmallArgs a) {
                     }
                 }
             }
-        }
-        // The next segment rewrites the region: LDS operations of one wave
-        // complete in order.
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-    }
-
-    // 4. Slice sums to the wave's own region, then the slices in index order.
-    float* part = reinterpret_cast<float*>(region);
-#pragma unroll
-    for (int b = 0; b < NB; ++b)
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-            float v;
-            if constexpr (FMT == kFmtTernary)
-                v = ((acc[b][0][r] + acc[b][4][r]) + (acc[b][1][r] + acc[b][5][r])) +
-                    ((acc[b][2][r] + acc[b][6][r]) + (acc[b][3][r] + acc[b][7][r]));
-            else
-                v = acc[b][0][r];
-            const int col = WIDE ? 4 * kb + r : kb;
-            if (col < mcount) part[(b * mcount + col) * 16 + j] = v;
-        }
-    __syncthreads();
-    for (int o = threadIdx.x; o < mcount * 16; o += blockDim.x) {
-        float y[NB];
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-            float sum = 0.0f;
-            for (int w = 0; w < nwaves; ++w) {
-                const float v = reinterpret_cast<const float*>(smem + (size_t)w * a.region)[b * mcount * 16 + o];
-                sum = w == 0 ? v : sum + v;
+            if (g % GPL == GPL - 1) {
+                const int i = g / GPL + RL;
+                load_codes(i < CB ? cur : next, i % CB);
             }
-            y[b] = FMT == kFmtW4 ? sum * kW4Scale : sum;
+            if constexpr (S == 4) {
+                if (g % 2 == 1) load_scales(next, g >> 1, sc);
+            }
+            if constexpr (WIDE && MULTI) {
+                const int i = 2 * (g + RG);
+                load_a(i < 16 ? s : next_s, i % 16);
+                load_a(i < 16 ? s : next_s, i % 16 + 1);
+            }
+            __builtin_amdgcn_sched_barrier(0);
         }
-        const int row = tile * 16 + (o & 15);
-        if (row < a.n) {
-            const size_t at = (size_t)(m0 + (o >> 4)) * a.n + row;
-            if constexpr (NB == 2) store_as(a.out, at, gate_activation(y[0], a.act) * y[1], a.out_dtype);
-            else static_cast<float*>(a.out)[at] = y[0];
+        if constexpr (S != 4) {
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int i = 0; i < S; ++i) sc[b][i] = sn[b][i];
+        }
+    };
+
+    // 2. The tiles, with two sets of slice sums in turn: one barrier per tile.
+    int turn = 0;
+    for (int tile = blockIdx.x; tile < a.tiles; tile += gridDim.x, turn ^= 1) {
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+#pragma unroll
+                for (int r = 0; r < R; ++r) acc[b][c][r] = 0.0f;
+        for (int s = seg_begin; s < seg_end; ++s) {
+            const bool last = s + 1 == seg_end;
+            const int nt = last ? tile + (int)gridDim.x : tile, ns = last ? seg_begin : s + 1;
+            body(tile, s, nt, ns);
+        }
+        float* part = parts + turn * a.part;
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                float v;
+                if constexpr (FMT == kFmtTernary)
+                    v = ((acc[b][0][r] + acc[b][4][r]) + (acc[b][1][r] + acc[b][5][r])) +
+                        ((acc[b][2][r] + acc[b][6][r]) + (acc[b][3][r] + acc[b][7][r]));
+                else
+                    v = acc[b][0][r];
+                const int col = WIDE ? 4 * kb + r : kb;
+                if (col < mcount) part[((wave * NB + b) * mcount + col) * 16 + j] = v;
+            }
+        __syncthreads();
+        for (int o = threadIdx.x; o < mcount * 16; o += blockDim.x) {
+            float y[NB];
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                float sum = 0.0f;
+                for (int w = 0; w < nwaves; ++w) {
+                    const float v = part[(w * NB + b) * mcount * 16 + o];
+                    sum = w == 0 ? v : sum + v;
+                }
+                y[b] = FMT == kFmtW4 ? sum * kW4Scale : sum;
+            }
+            const int row = tile * 16 + (o & 15);
+            if (row < a.n) {
+                const size_t at = (size_t)(m0 + (o >> 4)) * a.n + row;
+                if constexpr (NB == 2) store_as(a.out, at, gate_activation(y[0], a.act) * y[1], a.out_dtype);
+                else static_cast<float*>(a.out)[at] = y[0];
+            }
         }
     }
 }
 
-template <int FMT, int S, int NB, bool WIDE>
-hipError_t launch_one(const BlockMatmul& p) {
-    SmallArgs a{p.q, p.xs, p.w0, p.w1, p.out, (int)p.n, (int)p.k, (int)(p.k / 128), (int)((p.k + 1023) / 1024), 0, 0,
-                (int)p.m, p.act, p.out_dtype, 0};
-    a.nseg = a.s8;
-    a.per_wave = (a.nseg + kTilesDefaultWaves - 1) / kTilesDefaultWaves;
-    const int waves = (a.nseg + a.per_wave - 1) / a.per_wave;
-    constexpr int MC = WIDE ? 16 : 4;
+template <int FMT, int S, int NB, int MC, bool MULTI, int MAXW>
+hipError_t launch_one(const BlockMatmul& p, SmallArgs a, int waves) {
+    constexpr int RG = kRing, GPL = FMT == kFmtTernary ? 2 : 1;
     const int mc = (int)(p.m < MC ? p.m : MC);
-    const int partials = NB * mc * 64, staging = WIDE ? 512 : mc * kColPitch;
-    a.region = partials > staging ? partials : staging;
-    const dim3 grid((unsigned)((p.n + 15) / 16), (unsigned)((p.m + MC - 1) / MC));
-    const size_t lds = (size_t)waves * a.region;
+    a.part = waves * NB * mc * 16;
+    const size_t lds = (size_t)waves * a.per_wave * seg_bytes(MC) + (size_t)2 * a.part * 4;
+    const int passes = (int)((p.m + MC - 1) / MC);
+    // Persistent workgroups.  The stream is fastest with about 64 KB in flight
+    // per CU, and more only slows it (FFN up, one column: 4-bit weights 10.7 /
+    // 9.6 / 9.7 / 9.7 us at one / two / three / four workgroups of five waves a
+    // CU; gated ternary 15.4 / 12.4 / 12.1 / 12.6).  With the activations of
+    // sixteen columns to load first, one workgroup of five waves is best
+    // (gated, m = 8: 19.2 / 20.9 / 23.2 us at one / two / three).
+    constexpr int kWaveKB = RG / GPL * NB;
+    const int per_cu = std::max(1, (MC == 16 ? 8 : 64 / kWaveKB) / waves);
+    const dim3 grid((unsigned)std::min(a.tiles, 256 * per_cu), (unsigned)passes);
     clear_stale_error();
-    if (waves <= 8)
-        hipLaunchKernelGGL((block_small_m_kernel<FMT, S, NB, WIDE, 8>), grid, dim3(64 * waves), lds, p.stream, a);
-    else
-        hipLaunchKernelGGL((block_small_m_kernel<FMT, S, NB, WIDE, 16>), grid, dim3(64 * waves), lds, p.stream, a);
+    hipLaunchKernelGGL((block_small_m_kernel<FMT, S, NB, MC, MULTI, MAXW>), grid, dim3(64 * waves), lds, p.stream, a);
     return hipGetLastError();
+}
+
+template <int FMT, int S, int NB, int MC>
+hipError_t launch_split(const BlockMatmul& p) {
+    SmallArgs a{p.q, p.xs, p.w0, p.w1, p.out, (int)p.n, (int)p.k, (int)(p.k / 128), (int)((p.k + 1023) / 1024), 0,
+                (int)((p.n + 15) / 16), (int)p.m, p.act, p.out_dtype, 0};
+    const int max_waves = FMT == kFmtTernary ? kTilesDefaultWaves : kW4Waves;
+    a.per_wave = (a.s8 + max_waves - 1) / max_waves;
+    const int waves = (a.s8 + a.per_wave - 1) / a.per_wave;
+    constexpr int kMany = FMT == kFmtTernary ? 16 : 12;
+    if (a.per_wave > 1) return launch_one<FMT, S, NB, MC, true, kMany>(p, a, waves);
+    if (waves > 8) return launch_one<FMT, S, NB, MC, false, kMany>(p, a, waves);
+    return launch_one<FMT, S, NB, MC, false, 8>(p, a, waves);
 }
 
 template <int FMT, int S, int NB>
 hipError_t launch_cols(const BlockMatmul& p) {
-    return p.m <= 4 ? launch_one<FMT, S, NB, false>(p) : launch_one<FMT, S, NB, true>(p);
+    // LDS holds all of k for the columns of a pass: two at most beyond 32768.
+    if (p.m <= 2 || (p.m <= 4 && p.k > 32768)) return launch_split<FMT, S, NB, 2>(p);
+    if (p.m <= 4) return launch_split<FMT, S, NB, 4>(p);
+    return launch_split<FMT, S, NB, 16>(p);
 }
 
 }  // namespace
