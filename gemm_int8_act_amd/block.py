@@ -8,10 +8,14 @@ torch stream (or ``stream``), whichever device is current.
 from __future__ import annotations
 
 import ctypes
+import functools
+import struct
 
 import torch
 
 from . import PQ2_BF16, PQ2_F16, PQ2_F32, _check, lib, pq2_tiles_bytes
+
+_tiles_bytes = functools.lru_cache(maxsize=256)(pq2_tiles_bytes)
 
 ACT_SILU, ACT_GELU_TANH = 0, 1
 
@@ -30,22 +34,22 @@ BLOCK_EXPORTED = (
 _DTYPE = {torch.bfloat16: PQ2_BF16, torch.float16: PQ2_F16, torch.float32: PQ2_F32}
 
 
-class BlockNormArgs(ctypes.Structure):
-    """pq2_block_norm_args of include/pq2_block.h."""
-    _fields_ = [
-        ("r", ctypes.c_void_p), ("r_stride", ctypes.c_int64),
-        ("block", ctypes.c_void_p), ("block_stride", ctypes.c_int64),
-        ("post_w", ctypes.c_void_p),
-        ("gate", ctypes.c_void_p), ("gate_stride", ctypes.c_int64),
-        ("w", ctypes.c_void_p),
-        ("r_out", ctypes.c_void_p), ("r_out_stride", ctypes.c_int64),
-        ("x_out", ctypes.c_void_p), ("x_out_stride", ctypes.c_int64),
-        ("q", ctypes.c_void_p), ("xs", ctypes.c_void_p),
-        ("m", ctypes.c_int64), ("k", ctypes.c_int64), ("agroup", ctypes.c_int64),
-        ("eps", ctypes.c_double), ("alpha", ctypes.c_float),
-        ("r_dtype", ctypes.c_int), ("block_dtype", ctypes.c_int), ("w_dtype", ctypes.c_int),
-        ("x_dtype", ctypes.c_int), ("unit_offset", ctypes.c_int),
-    ]
+# pq2_block_norm_args of include/pq2_block.h: the fields in order, with their
+# native struct codes.
+NORM_FIELDS = (
+    ("r", "P"), ("r_stride", "q"),
+    ("block", "P"), ("block_stride", "q"),
+    ("post_w", "P"),
+    ("gate", "P"), ("gate_stride", "q"),
+    ("w", "P"),
+    ("r_out", "P"), ("r_out_stride", "q"),
+    ("x_out", "P"), ("x_out_stride", "q"),
+    ("q", "P"), ("xs", "P"),
+    ("m", "q"), ("k", "q"), ("agroup", "q"),
+    ("eps", "d"), ("alpha", "f"),
+    ("r_dtype", "i"), ("block_dtype", "i"), ("w_dtype", "i"), ("x_dtype", "i"), ("unit_offset", "i"),
+)
+_NORM = struct.Struct("@" + "".join(code for _, code in NORM_FIELDS))
 
 
 def _bind():
@@ -60,7 +64,7 @@ def _bind():
         "pq2_gated_matmul_w4": [p, p, p, p, i64, i64, i64, i64, i32, p, i32, p],
         "pq2_gated_linear_tiles": [p, i32, i64, p, p, i64, i64, i64, i32, p, i32, p, p, p],
         "pq2_gated_linear_w4": [p, i32, i64, p, p, i64, i64, i64, i64, i32, p, i32, p, p, p],
-        "pq2_block_norm": [ctypes.POINTER(BlockNormArgs), p],
+        "pq2_block_norm": [ctypes.c_char_p, p],
     }.items():
         fn = getattr(lib, name)
         fn.argtypes = args
@@ -77,13 +81,13 @@ def _dtype(t, name):
     return code
 
 
-def _same_device(first, *rest):
-    """The device of the call's tensors: one GPU for all of them."""
-    dev = first.device
-    if dev.type != "cuda":
+def _device(first, *rest):
+    """Index of the one GPU that holds the call's tensors."""
+    dev = first.get_device()
+    if dev < 0:
         raise ValueError("device tensors expected")
     for t in rest:
-        if t is not None and t.device != dev:
+        if t is not None and t.get_device() != dev:
             raise ValueError("all tensors of a call must be on one device")
     return dev
 
@@ -91,11 +95,11 @@ def _same_device(first, *rest):
 def _call(name, dev, stream, *args):
     """Calls the entry point on device ``dev``: its current stream unless one is given."""
     if stream is None:
-        s = torch.cuda.current_stream(dev).cuda_stream
+        s = torch.cuda.current_stream(dev).cuda_stream if _raw_stream is None else _raw_stream(dev)
     else:
         s = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    fn = getattr(lib, name)
-    if dev.index == torch.cuda.current_device():
+    fn = _FN[name]
+    if dev == torch.cuda.current_device():
         status = fn(*args, s)
     else:
         with torch.cuda.device(dev):
@@ -104,6 +108,13 @@ def _call(name, dev, stream, *args):
         _check(status, name)
 
 
+# The current stream's handle without a Stream object around it (a call's
+# host time is near the decode kernels' own).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_FN = {name: getattr(lib, name) for name in BLOCK_EXPORTED}
+
+
+@functools.lru_cache(maxsize=256)
 def pq2_w4_tiles_bytes(n: int, k: int, wgroup: int) -> int:
     """Bytes of the w4 tile layout of an n x k weight matrix (ValueError on a bad shape or group)."""
     size = lib.pq2_w4_tiles_bytes(n, k, wgroup)
@@ -125,7 +136,7 @@ def pq2_prepare_w4_tiles(codes, scales, wgroup: int, tiles, stream=None) -> None
         raise ValueError("shape mismatch between codes and scales")
     if not tiles.is_contiguous() or tiles.numel() < pq2_w4_tiles_bytes(n, k, wgroup):
         raise ValueError("tiles must be a contiguous uint8 tensor of pq2_w4_tiles_bytes(n, k, wgroup) bytes")
-    _call("pq2_prepare_w4_tiles", _same_device(codes, scales, tiles), stream, codes.data_ptr(),
+    _call("pq2_prepare_w4_tiles", _device(codes, scales, tiles), stream, codes.data_ptr(),
           _row_stride(codes), scales.data_ptr(), _row_stride(scales), n, k, wgroup, tiles.data_ptr())
 
 
@@ -166,7 +177,7 @@ def pq2_matmul_w4(q, xs, tiles, y, wgroup: int, stream=None) -> None:
     m, n = _out(y, "y", (torch.float32,))
     k = _codes(q, xs, m)
     w = _weights(tiles, pq2_w4_tiles_bytes(n, k, wgroup))
-    _call("pq2_matmul_w4", _same_device(q, xs, tiles, y), stream, q.data_ptr(), xs.data_ptr(), w, m, n, k, wgroup,
+    _call("pq2_matmul_w4", _device(q, xs, tiles, y), stream, q.data_ptr(), xs.data_ptr(), w, m, n, k, wgroup,
           y.data_ptr())
 
 
@@ -176,7 +187,7 @@ def pq2_linear_w4(x, tiles, y, wgroup: int, q_work, xs_work, stream=None) -> Non
     m, n = _out(y, "y", (torch.float32,))
     k = _codes(q_work, xs_work, m)
     w = _weights(tiles, pq2_w4_tiles_bytes(n, k, wgroup))
-    _call("pq2_linear_w4", _same_device(x, tiles, y, q_work, xs_work), stream, *_x(x, m, k), w, m, n, k, wgroup,
+    _call("pq2_linear_w4", _device(x, tiles, y, q_work, xs_work), stream, *_x(x, m, k), w, m, n, k, wgroup,
           y.data_ptr(), q_work.data_ptr(), xs_work.data_ptr())
 
 
@@ -185,8 +196,8 @@ def pq2_gated_matmul_tiles(q, xs, gate, up, h, act: int = ACT_SILU, stream=None)
     one shape, q / xs as pq2_matmul_w4."""
     m, n = _out(h, "h", tuple(_DTYPE))
     k = _codes(q, xs, m)
-    need = pq2_tiles_bytes(n, k)
-    _call("pq2_gated_matmul_tiles", _same_device(q, xs, gate, up, h), stream, q.data_ptr(), xs.data_ptr(),
+    need = _tiles_bytes(n, k)
+    _call("pq2_gated_matmul_tiles", _device(q, xs, gate, up, h), stream, q.data_ptr(), xs.data_ptr(),
           _weights(gate, need), _weights(up, need), m, n, k, act, h.data_ptr(), _DTYPE[h.dtype])
 
 
@@ -195,7 +206,7 @@ def pq2_gated_matmul_w4(q, xs, gate, up, h, wgroup: int, act: int = ACT_SILU, st
     m, n = _out(h, "h", tuple(_DTYPE))
     k = _codes(q, xs, m)
     need = pq2_w4_tiles_bytes(n, k, wgroup)
-    _call("pq2_gated_matmul_w4", _same_device(q, xs, gate, up, h), stream, q.data_ptr(), xs.data_ptr(),
+    _call("pq2_gated_matmul_w4", _device(q, xs, gate, up, h), stream, q.data_ptr(), xs.data_ptr(),
           _weights(gate, need), _weights(up, need), m, n, k, wgroup, act, h.data_ptr(), _DTYPE[h.dtype])
 
 
@@ -203,8 +214,8 @@ def pq2_gated_linear_tiles(x, gate, up, h, q_work, xs_work, act: int = ACT_SILU,
     """The complete call of pq2_gated_matmul_tiles: x quantised into the scratch first."""
     m, n = _out(h, "h", tuple(_DTYPE))
     k = _codes(q_work, xs_work, m)
-    need = pq2_tiles_bytes(n, k)
-    _call("pq2_gated_linear_tiles", _same_device(x, gate, up, h, q_work, xs_work), stream, *_x(x, m, k),
+    need = _tiles_bytes(n, k)
+    _call("pq2_gated_linear_tiles", _device(x, gate, up, h, q_work, xs_work), stream, *_x(x, m, k),
           _weights(gate, need), _weights(up, need), m, n, k, act, h.data_ptr(), _DTYPE[h.dtype], q_work.data_ptr(),
           xs_work.data_ptr())
 
@@ -214,7 +225,7 @@ def pq2_gated_linear_w4(x, gate, up, h, wgroup: int, q_work, xs_work, act: int =
     m, n = _out(h, "h", tuple(_DTYPE))
     k = _codes(q_work, xs_work, m)
     need = pq2_w4_tiles_bytes(n, k, wgroup)
-    _call("pq2_gated_linear_w4", _same_device(x, gate, up, h, q_work, xs_work), stream, *_x(x, m, k),
+    _call("pq2_gated_linear_w4", _device(x, gate, up, h, q_work, xs_work), stream, *_x(x, m, k),
           _weights(gate, need), _weights(up, need), m, n, k, wgroup, act, h.data_ptr(), _DTYPE[h.dtype],
           q_work.data_ptr(), xs_work.data_ptr())
 
@@ -244,44 +255,43 @@ def pq2_block_norm(r, w, eps: float, *, block=None, post_w=None, gate=None, alph
     if r.dim() != 2:
         raise ValueError("r must be [m][k]")
     m, k = r.shape
-    a = BlockNormArgs()
-    a.m, a.k, a.agroup = m, k, agroup
-    a.eps, a.alpha, a.unit_offset = eps, alpha, 1 if unit_offset else 0
-    a.r, a.r_stride = _rows(r, "r", m, k)
-    a.r_dtype, a.w_dtype = _dtype(r, "r"), _dtype(w, "w")
-    a.w = _vector(w, "w", k, w.dtype)
+    wt = w.dtype
+    rp, rs = _rows(r, "r", m, k)
+    wp = _vector(w, "w", k, wt)
+    bp = bs = bd = pp = gp = gs = op = os_ = xp = xst = qp = sp = 0
     if block is not None:
-        a.block, a.block_stride = _rows(block, "block", m, k)
-        a.block_dtype = _dtype(block, "block")
+        bp, bs = _rows(block, "block", m, k)
+        bd = _dtype(block, "block")
     if post_w is not None:
-        a.post_w = _vector(post_w, "post_w", k, w.dtype)
+        pp = _vector(post_w, "post_w", k, wt)
     if gate is not None:
         if gate.dim() == 1:
-            a.gate = _vector(gate, "gate", k, w.dtype)
+            gp = _vector(gate, "gate", k, wt)
+        elif gate.dtype != wt:
+            raise ValueError("gate must have the norm weights' dtype")
         else:
-            if gate.dtype != w.dtype:
-                raise ValueError("gate must have the norm weights' dtype")
-            a.gate, a.gate_stride = _rows(gate, "gate", m, k)
+            gp, gs = _rows(gate, "gate", m, k)
     if r_out is not None:
         if r_out.dtype != r.dtype:
             raise ValueError("r_out must have r's dtype")
-        a.r_out, a.r_out_stride = _rows(r_out, "r_out", m, k)
+        op, os_ = _rows(r_out, "r_out", m, k)
     if x_out is not None:
         if x_dtype is not None and x_out.dtype != x_dtype:
             raise ValueError("x_out must have x_dtype")
-        a.x_out, a.x_out_stride = _rows(x_out, "x_out", m, k)
+        xp, xst = _rows(x_out, "x_out", m, k)
         x_dtype = x_out.dtype
-    code = _DTYPE.get(r.dtype if x_dtype is None else x_dtype)
-    if code is None:
+    xd = _DTYPE.get(r.dtype if x_dtype is None else x_dtype)
+    if xd is None:
         raise ValueError(f"unsupported x_dtype {x_dtype}")
-    a.x_dtype = code
     if q is not None:
         if q.dtype != torch.int8 or not q.is_contiguous() or q.shape != (m, k):
             raise ValueError("q must be a contiguous int8 [m][k] tensor")
-        a.q = q.data_ptr()
+        qp = q.data_ptr()
     if xs is not None:
         if xs.dtype != torch.float32 or not xs.is_contiguous() or agroup not in (128, 64, 32) or \
                 xs.numel() != m * (k // agroup):
             raise ValueError("xs must be a contiguous float32 [m][k/agroup] tensor, agroup 128, 64 or 32")
-        a.xs = xs.data_ptr()
-    _call("pq2_block_norm", _same_device(r, w, block, post_w, gate, r_out, x_out, q, xs), stream, ctypes.byref(a))
+        sp = xs.data_ptr()
+    args = _NORM.pack(rp, rs, bp, bs, pp, gp, gs, wp, op, os_, xp, xst, qp, sp, m, k, agroup, eps, alpha,
+                      _dtype(r, "r"), bd, _dtype(w, "w"), xd, 1 if unit_offset else 0)
+    _call("pq2_block_norm", _device(r, w, block, post_w, gate, r_out, x_out, q, xs), stream, args)

@@ -27,6 +27,9 @@ struct BlockMatmul {
     void* out;
     int out_dtype;
     hipStream_t stream;
+    int src = kSrcNatural;      // or the type of x, quantised inside (block_takes_x)
+    const void* x = nullptr;
+    int64_t x_stride = 0;
 };
 
 int64_t w4_tiles_bytes(int64_t n, int64_t k, int64_t wgroup);
@@ -35,6 +38,7 @@ hipError_t launch_prepare_w4(const uint8_t* codes, int64_t codes_stride, const u
 hipError_t launch_block_small_m(const BlockMatmul& a);
 hipError_t launch_block_prefill(const BlockMatmul& a);
 bool block_takes_small_m(const BlockMatmul& a);
+bool block_takes_x(int64_t m);   // whether the decode engine quantises x itself
 hipError_t launch_block_norm(const pq2_block_norm_args& a, hipStream_t stream);
 
 typedef int v4i __attribute__((ext_vector_type(4)));
@@ -67,6 +71,48 @@ __device__ __forceinline__ v4i w4_operand(uint32_t d0, uint32_t d1) {
 }
 
 __device__ __forceinline__ float half_bits(uint32_t h) { return __half2float(__ushort_as_half((unsigned short)h)); }
+
+// The lane's 16 elements v of a 128-element activation group (eight aligned
+// lanes) as INT8 codes in natural order, and the group's scale: the codes of
+// pq2_quantize_act_i8, q = clamp(rint(RN(v / d)), +-127) with d = scale, or 1
+// for an all-zero group.
+//
+// RN(v / d) comes from FP32 operations alone (a double product per element,
+// as in the other quantisers, issues at half their rate and these kernels
+// quantise in every workgroup): with d scaled to [1, 2) by a power of two,
+// y = RN(1 / d) and t0 = RN(v y) within an ulp of the quotient, the residual
+// v - t0 d is exact in one fma and RN(t0 + residual y) is the correctly
+// rounded quotient (Markstein, "Computation of elementary functions on the
+// IBM RISC System/6000 processor", 1990).  Scaling v by the same power is
+// exact for every quotient that does not round to 0: |v / d| >= 1/4 leaves
+// |v| >= 1/4.
+__device__ __forceinline__ uint4 quantize16(const float (&v)[16], float& scale) {
+#pragma clang fp contract(off)
+    float amax = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) amax = fmaxf(amax, fabsf(v[e]));
+    amax = max8_f(amax);
+    scale = amax / 127.0f;
+    const float d = scale > 0.0f ? scale : 1.0f;
+    const int exp = __builtin_amdgcn_frexp_expf(d) - 1;
+    const float dn = __builtin_ldexpf(d, -exp);
+    const float y = 1.0f / dn;
+    constexpr float kRound = 12582912.0f;  // 1.5 * 2^23: adding it rounds to an integer, ties to even
+    uint32_t bits[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+        const float x = __builtin_ldexpf(v[e], -exp);
+        const float t0 = x * y;
+        const float t = __builtin_fmaf(__builtin_fmaf(-t0, dn, x), y, t0);
+        bits[e] = __float_as_uint(__builtin_amdgcn_fmed3f(t, -127.0f, 127.0f) + kRound);
+    }
+    auto low4 = [&](int e) {
+        const uint32_t a = __builtin_amdgcn_perm(bits[e + 1], bits[e], 0x0C0C0400u);
+        const uint32_t b = __builtin_amdgcn_perm(bits[e + 3], bits[e + 2], 0x0C0C0400u);
+        return a | (b << 16);
+    };
+    return make_uint4(low4(0), low4(4), low4(8), low4(12));
+}
 
 // fp16 number i (0..7) of 16 bytes.
 __device__ __forceinline__ float half_at(const uint4& v, int i) {

@@ -22,15 +22,19 @@
 // start to its end, through the reduction of one tile and into the next.
 // The activations are staged once per workgroup, not once per tile.
 //
-// Up to four columns (MC 1, 2, 4): the four A rows 4c .. 4c+3 of the matrix
+// Up to four columns (MC 4): the four A rows 4c .. 4c+3 of the matrix
 // core all belong to column c, so a lane owns one output (column lane/16).
 // With S = 2 or 4 weight groups per 128 the rows are told apart by masking:
 // row 4c+r keeps only weight group r, and one pair of MFMAs gives the dots
-// of all S groups in the four result registers.  Activations sit in LDS.
+// of all S groups in the four result registers.  Activations sit in LDS;
+// they may come unquantised (SRC): each wave then quantises its own slice of
+// k while its first weights are on their way, with the exact in-kernel
+// quantiser, so the codes are those of pq2_quantize_act_i8.
 // Up to sixteen columns (MC 16): A row = column, held in registers in operand
 // order (read again per segment where a wave has several); a lane owns four
 // outputs.
 #include "block_internal.h"
+#include "small_m_common.h"
 
 #include <algorithm>
 
@@ -41,10 +45,12 @@ namespace {
 struct SmallArgs {
     const int8_t* q;
     const float* xs;
+    const void* x;
+    int64_t x_stride;
     const uint8_t* w0;
     const uint8_t* w1;
     void* out;
-    int n, k, groups, s8, per_wave, tiles, mtotal, act, out_dtype, part;
+    int n, k, groups, s8, per_wave, tiles, mtotal, cols, act, out_dtype, part;
 };
 
 // Waves k is split over at most: registers for three waves per SIMD remain at
@@ -58,14 +64,17 @@ constexpr int kW4Waves = 12;
 constexpr int kRing = 4;
 
 constexpr int kColPitch = 1024 + 64;  // four columns' reads fall in distinct banks
-// LDS per wave and segment: the columns' codes and scales (MC <= 4), or the
-// scales alone, [group][column].
-__host__ __device__ constexpr int seg_bytes(int mc) { return mc <= 4 ? mc * (kColPitch + 32) : 512; }
+// LDS per wave and segment: the `cols` columns' codes and scales (MC 4), or
+// the scales alone, [group][column].
+__host__ __device__ constexpr int seg_lds(int mc, int cols) { return mc == 4 ? cols * (kColPitch + 32) : 512; }
 
-template <int FMT, int S, int NB, int MC, bool MULTI, int MAXW>
+template <int FMT, int S, int NB, int MC, int SRC, bool MULTI, int MAXW>
 __global__ __launch_bounds__(64 * MAXW) void block_small_m_kernel(SmallArgs a) {
 #pragma clang fp contract(off)
     constexpr bool WIDE = MC == 16;
+    constexpr bool FUSED = src_fused(SRC);
+    constexpr int XL = src_xloads(SRC);
+    static_assert(!(WIDE && FUSED), "unquantised activations: up to four columns");
     constexpr int UNIT = block_unit(FMT, S);
     constexpr int CODES = block_code_bytes(FMT);
     constexpr int CB = CODES / 1024;   // code loads per segment
@@ -80,16 +89,21 @@ __global__ __launch_bounds__(64 * MAXW) void block_small_m_kernel(SmallArgs a) {
     const int lane = threadIdx.x & 63;
     const int j = lane & 15;
     const int kb = lane >> 4;
-    const int m0 = blockIdx.y * MC;
-    const int mcount = min(MC, a.mtotal - m0);
+    const int m0 = blockIdx.y * a.cols;
+    const int mcount = min(a.cols, a.mtotal - m0);
+    const int seg_bytes = seg_lds(MC, a.cols);
     const int seg_begin = wave * a.per_wave;
     const int seg_end = min(seg_begin + a.per_wave, a.s8);
 
-    const auto q_rs = make_rsrc(a.q + (size_t)m0 * a.k, (uint32_t)(mcount * a.k));
-    const auto xs_rs = make_rsrc(a.xs + (size_t)m0 * a.groups, (uint32_t)(mcount * a.groups * 4));
+    const auto q_rs = make_rsrc(FUSED ? nullptr : a.q + (size_t)m0 * a.k, FUSED ? 0u : (uint32_t)(mcount * a.k));
+    const auto xs_rs = make_rsrc(FUSED ? nullptr : a.xs + (size_t)m0 * a.groups,
+                                 FUSED ? 0u : (uint32_t)(mcount * a.groups * 4));
+    const auto x_rs = make_rsrc(
+        FUSED ? static_cast<const unsigned char*>(a.x) + (size_t)m0 * a.x_stride * src_esize(SRC) : nullptr,
+        FUSED ? (uint32_t)(((int64_t)(mcount - 1) * a.x_stride + a.k) * src_esize(SRC)) : 0u);
     // Per wave: its segments' activations; then two sets of slice sums.
-    unsigned char* region = smem + (size_t)wave * a.per_wave * seg_bytes(MC);
-    float* parts = reinterpret_cast<float*>(smem + (size_t)nwaves * a.per_wave * seg_bytes(MC));
+    unsigned char* region = smem + (size_t)wave * a.per_wave * seg_bytes;
+    float* parts = reinterpret_cast<float*>(smem + (size_t)nwaves * a.per_wave * seg_bytes);
 
     // Loads of one unit (tile, segment); past the last tile they read nothing.
     uint4 cw[NB][RL], sc[NB][S], sn[NB][S], av[WIDE ? (MULTI ? 2 * RG : 16) : 1];
@@ -127,37 +141,59 @@ __global__ __launch_bounds__(64 * MAXW) void block_small_m_kernel(SmallArgs a) {
     // 1. Stage the wave's activations.  The loads of the first PRE segments go
     //    out first, then the first unit's weights, then the staging writes, so
     //    the weight stream starts at once.
-    constexpr int PRE = MULTI && !WIDE ? 2 : 1;
+    constexpr int PRE = !WIDE && !FUSED ? 2 : 1;
     struct Staged {
-        uint4 v[WIDE ? 1 : MC];
+        uint4 v[WIDE ? 1 : MC][FUSED ? XL : 1];
         uint2 x;
     };
     auto stage_load = [&](int s, Staged& t) {
         const int g0 = 8 * s;
+        const int off = s * 1024 + 16 * lane;
         if constexpr (WIDE) {
             // Lane (column j, groups 2 kb and 2 kb + 1).
             const bool ok = j < mcount && g0 + 2 * kb < a.groups;
             t.x = buf_load8(xs_rs, ok ? (uint32_t)((j * a.groups + g0 + 2 * kb) * 4) : kBufferOOB);
+        } else if constexpr (FUSED) {
+#pragma unroll
+            for (int i = 0; i < MC; ++i) {
+                if (i >= mcount) continue;
+                const uint32_t at = (uint32_t)((i * a.x_stride + off) * src_esize(SRC));
+#pragma unroll
+                for (int l = 0; l < XL; ++l) t.v[i][l] = buf_load16(x_rs, off < a.k ? at + 16u * l : kBufferOOB);
+            }
         } else {
             // Lane 8 c + g: the scale of column c, group g.
             const bool ok = lane < 8 * mcount && g0 + (lane & 7) < a.groups;
             t.x.x = buf_load4(xs_rs, ok ? (uint32_t)(((lane >> 3) * a.groups + g0 + (lane & 7)) * 4) : kBufferOOB);
-            const int off = s * 1024 + 16 * lane;
 #pragma unroll
             for (int i = 0; i < MC; ++i)
-                t.v[i] = buf_load16(q_rs, i < mcount && off < a.k ? (uint32_t)(i * a.k + off) : kBufferOOB);
+                if (i < mcount) t.v[i][0] = buf_load16(q_rs, off < a.k ? (uint32_t)(i * a.k + off) : kBufferOOB);
         }
     };
     auto stage_store = [&](int s, const Staged& t) {
-        unsigned char* to = region + (s - seg_begin) * seg_bytes(MC);
+        unsigned char* to = region + (s - seg_begin) * seg_bytes;
+        float* xl = reinterpret_cast<float*>(to + (WIDE ? 0 : a.cols * kColPitch));
         if constexpr (WIDE) {
-            float* xl = reinterpret_cast<float*>(to);
             xl[(2 * kb) * 16 + j] = __uint_as_float(t.x.x);
             xl[(2 * kb + 1) * 16 + j] = 8 * s + 2 * kb + 1 < a.groups ? __uint_as_float(t.x.y) : 0.0f;
         } else {
 #pragma unroll
-            for (int i = 0; i < MC; ++i) *reinterpret_cast<uint4*>(to + i * kColPitch + 16 * lane) = t.v[i];
-            if (lane < 8 * MC) *reinterpret_cast<uint32_t*>(to + MC * kColPitch + 4 * lane) = t.x.x;
+            for (int i = 0; i < MC; ++i) {
+                if (i >= mcount) continue;
+                uint4 v;
+                if constexpr (FUSED) {
+                    float f[16], scale;
+                    x_to_float16<SRC>(t.v[i], f);
+                    v = quantize16(f, scale);  // the eight lanes of a group agree
+                    if ((lane & 7) == 0) xl[8 * i + (lane >> 3)] = scale;
+                } else {
+                    v = t.v[i][0];
+                }
+                *reinterpret_cast<uint4*>(to + i * kColPitch + 16 * lane) = v;
+            }
+            if constexpr (!FUSED) {
+                if (lane < 8 * mcount) xl[lane] = __uint_as_float(t.x.x);
+            }
         }
     };
     {
@@ -202,12 +238,12 @@ __global__ __launch_bounds__(64 * MAXW) void block_small_m_kernel(SmallArgs a) {
     // one's registers become free.  (S = 4: eight groups use four scale
     // registers in turn, so they stream like the codes; else a second set.)
     auto body = [&](int tile, int s, int next_tile, int next_s) {
-        const unsigned char* from = region + (s - seg_begin) * seg_bytes(MC);
+        const unsigned char* from = region + (s - seg_begin) * seg_bytes;
         const Unit next = unit_of(next_tile, next_s);
         const Unit cur = RG < 8 ? unit_of(tile, s) : next;
         float4 xv[2];
         if constexpr (!WIDE) {
-            const float4* x = reinterpret_cast<const float4*>(from + MC * kColPitch + 32 * x_col);
+            const float4* x = reinterpret_cast<const float4*>(from + a.cols * kColPitch + 32 * x_col);
             xv[0] = x[0];
             xv[1] = x[1];
         }
@@ -351,13 +387,12 @@ __global__ __launch_bounds__(64 * MAXW) void block_small_m_kernel(SmallArgs a) {
     }
 }
 
-template <int FMT, int S, int NB, int MC, bool MULTI, int MAXW>
+template <int FMT, int S, int NB, int MC, int SRC, bool MULTI, int MAXW>
 hipError_t launch_one(const BlockMatmul& p, SmallArgs a, int waves) {
     constexpr int RG = kRing, GPL = FMT == kFmtTernary ? 2 : 1;
-    const int mc = (int)(p.m < MC ? p.m : MC);
-    a.part = waves * NB * mc * 16;
-    const size_t lds = (size_t)waves * a.per_wave * seg_bytes(MC) + (size_t)2 * a.part * 4;
-    const int passes = (int)((p.m + MC - 1) / MC);
+    a.part = waves * NB * a.cols * 16;
+    const size_t lds = (size_t)waves * a.per_wave * seg_lds(MC, a.cols) + (size_t)2 * a.part * 4;
+    const int passes = (int)((p.m + a.cols - 1) / a.cols);
     // Persistent workgroups.  The stream is fastest with about 64 KB in flight
     // per CU, and more only slows it (FFN up, one column: 4-bit weights 10.7 /
     // 9.6 / 9.7 / 9.7 us at one / two / three / four workgroups of five waves a
@@ -368,34 +403,46 @@ hipError_t launch_one(const BlockMatmul& p, SmallArgs a, int waves) {
     const int per_cu = std::max(1, (MC == 16 ? 8 : 64 / kWaveKB) / waves);
     const dim3 grid((unsigned)std::min(a.tiles, 256 * per_cu), (unsigned)passes);
     clear_stale_error();
-    hipLaunchKernelGGL((block_small_m_kernel<FMT, S, NB, MC, MULTI, MAXW>), grid, dim3(64 * waves), lds, p.stream, a);
+    hipLaunchKernelGGL((block_small_m_kernel<FMT, S, NB, MC, SRC, MULTI, MAXW>), grid, dim3(64 * waves), lds, p.stream,
+                       a);
     return hipGetLastError();
-}
-
-template <int FMT, int S, int NB, int MC>
-hipError_t launch_split(const BlockMatmul& p) {
-    SmallArgs a{p.q, p.xs, p.w0, p.w1, p.out, (int)p.n, (int)p.k, (int)(p.k / 128), (int)((p.k + 1023) / 1024), 0,
-                (int)((p.n + 15) / 16), (int)p.m, p.act, p.out_dtype, 0};
-    const int max_waves = FMT == kFmtTernary ? kTilesDefaultWaves : kW4Waves;
-    a.per_wave = (a.s8 + max_waves - 1) / max_waves;
-    const int waves = (a.s8 + a.per_wave - 1) / a.per_wave;
-    constexpr int kMany = FMT == kFmtTernary ? 16 : 12;
-    if (a.per_wave > 1) return launch_one<FMT, S, NB, MC, true, kMany>(p, a, waves);
-    if (waves > 8) return launch_one<FMT, S, NB, MC, false, kMany>(p, a, waves);
-    return launch_one<FMT, S, NB, MC, false, 8>(p, a, waves);
 }
 
 template <int FMT, int S, int NB>
 hipError_t launch_cols(const BlockMatmul& p) {
+    SmallArgs a{p.q, p.xs, p.x, p.x_stride, p.w0, p.w1, p.out, (int)p.n, (int)p.k, (int)(p.k / 128),
+                (int)((p.k + 1023) / 1024), 0, (int)((p.n + 15) / 16), (int)p.m, 0, p.act, p.out_dtype, 0};
+    constexpr int kMany = FMT == kFmtTernary ? kTilesDefaultWaves : kW4Waves;
+    a.per_wave = (a.s8 + kMany - 1) / kMany;
+    const int waves = (a.s8 + a.per_wave - 1) / a.per_wave;
+    if (p.m > 4) {
+        a.cols = (int)std::min<int64_t>(p.m, 16);
+        if (a.per_wave > 1) return launch_one<FMT, S, NB, 16, kSrcNatural, true, kMany>(p, a, waves);
+        if (waves > 8) return launch_one<FMT, S, NB, 16, kSrcNatural, false, kMany>(p, a, waves);
+        return launch_one<FMT, S, NB, 16, kSrcNatural, false, 8>(p, a, waves);
+    }
     // LDS holds all of k for the columns of a pass: two at most beyond 32768.
-    if (p.m <= 2 || (p.m <= 4 && p.k > 32768)) return launch_split<FMT, S, NB, 2>(p);
-    if (p.m <= 4) return launch_split<FMT, S, NB, 4>(p);
-    return launch_split<FMT, S, NB, 16>(p);
+    a.cols = (int)(p.k > 32768 ? std::min<int64_t>(p.m, 2) : p.m);
+    switch (p.src) {
+        case kSrcNatural: return launch_one<FMT, S, NB, 4, kSrcNatural, true, kMany>(p, a, waves);
+        case kSrcBf16: return launch_one<FMT, S, NB, 4, kSrcBf16, true, kMany>(p, a, waves);
+        case kSrcF16: return launch_one<FMT, S, NB, 4, kSrcF16, true, kMany>(p, a, waves);
+        case kSrcF32: return launch_one<FMT, S, NB, 4, kSrcF32, true, kMany>(p, a, waves);
+        default: return hipErrorInvalidValue;
+    }
 }
 
 }  // namespace
 
 bool block_takes_small_m(const BlockMatmul& p) { return p.m <= 16; }
+
+// Quantising in the product's launch saves the quantiser's (about 2 us on the
+// GPU, 3 on the host) and costs what the extra columns take to quantise in
+// every workgroup.  Complete calls, one launch against two: QKV 4-bit at
+// m = 1 / 2 / 3 / 4 6.7 / 7.5 / 8.5 / 9.5 against 8.8 / 8.9 / 9.2 / 9.3 us, FFN
+// up gated ternary 12.1 / 12.4 / 13.4 / 15.0 against 13.8 / 14.0 / 14.2 / 14.5,
+// gated 4-bit at m = 4 18.6 against 19.5.
+bool block_takes_x(int64_t m) { return m <= 4; }
 
 hipError_t launch_block_small_m(const BlockMatmul& p) {
     const bool gated = p.act >= 0;

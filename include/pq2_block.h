@@ -78,7 +78,9 @@ int pq2_matmul_w4(const int8_t* q, const float* xs, const void* tiles, int64_t m
                   int64_t wgroup, float* y, void* stream);
 
 /* The complete call: y from bf16 / fp16 / fp32 activations, the bits of
- * pq2_quantize_act_i8 into q_work / xs_work followed by pq2_matmul_w4.
+ * pq2_quantize_act_i8 into q_work / xs_work followed by pq2_matmul_w4.  For
+ * few columns (and 16-byte aligned rows of x) one launch does both and the
+ * scratch is not written.
  *   x       as pq2_quantize_act_i8.
  *   q_work  device int8 [m][k], 16-byte aligned; xs_work device float
  *           [m][k/128], 4-byte aligned: scratch owned by the caller.  Calls

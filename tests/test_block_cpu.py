@@ -10,13 +10,20 @@ import torch
 
 import block_reference as ref
 import gemm_int8_act_amd as pq2
-from gemm_int8_act_amd.block import BlockNormArgs
+from gemm_int8_act_amd.block import NORM_FIELDS, _NORM
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 OK, EINVAL, ESHAPE, EALIGN, EDEVICE = pq2.PQ2_OK, pq2.PQ2_EINVAL, pq2.PQ2_ESHAPE, pq2.PQ2_EALIGN, pq2.PQ2_EDEVICE
 
 # Fake device addresses, never dereferenced: validation fails first.
 A, B, C, D, E, F = (0x7F0000000000 + (i << 36) for i in range(6))
+
+
+
+class BlockNormArgs(ctypes.Structure):
+    _fields_ = [(name, {"P": ctypes.c_void_p, "q": ctypes.c_int64, "d": ctypes.c_double, "f": ctypes.c_float,
+                        "i": ctypes.c_int}[code]) for name, code in NORM_FIELDS]
+
 
 no_gpu = pytest.mark.skipif(torch.cuda.device_count() > 0, reason="the device check passes on a GPU")
 
@@ -41,6 +48,12 @@ def test_args_struct_matches_the_header(tmp_path):
     subprocess.run(["gcc", "-I", os.path.join(ROOT, "include"), str(src), "-o", str(exe)], check=True)
     got = [int(v) for v in subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout.split()]
     assert got == [getattr(BlockNormArgs, f).offset for f in fields] + [ctypes.sizeof(BlockNormArgs)]
+    # What the binding packs is that structure, byte for byte.
+    a = BlockNormArgs()
+    values = [i + 1 if code in "Pq" else (i + 1) / 2 if code in "df" else i + 1 for i, (_, code) in enumerate(NORM_FIELDS)]
+    for (name, _), v in zip(NORM_FIELDS, values):
+        setattr(a, name, v)
+    assert _NORM.pack(*values) == bytes(a)
 
 
 def test_w4_tiles_bytes():
@@ -137,7 +150,7 @@ def norm_args(**kw):
     a.m, a.k, a.agroup, a.eps, a.alpha = 4, 128, 128, 1e-6, 1.0
     for name, v in kw.items():
         setattr(a, name, v)
-    return pq2.lib.pq2_block_norm(ctypes.byref(a), None)
+    return pq2.lib.pq2_block_norm(bytes(a), None)
 
 
 def test_block_norm_validation():

@@ -156,6 +156,47 @@ def test_linear_w4_is_quantise_then_matmul(dtype, m, n, k, pad):
     assert torch.equal(y.read(), want.cpu())
 
 
+def hard_activations(m, k, dtype, seed):
+    """Values at and next to rounding borders of their group's scale, over the exponent range: ties (c + 1/2) * scale
+    and their neighbours, subnormal and huge groups, all-zero groups, single elements."""
+    gen = torch.Generator().manual_seed(seed)
+    x = torch.randint(-127, 128, (m, k // 128, 128), generator=gen).double() + 0.5 * torch.randint(0, 2, (m, k // 128, 128), generator=gen)
+    lo, hi = {"bf16": (-130, 118), "f16": (-22, 6), "f32": (-145, 118)}[dtype]
+    exp = torch.randint(lo, hi, (m, k // 128, 1), generator=gen).double()
+    frac = 1 + torch.rand((m, k // 128, 1), generator=gen).double() * torch.randint(0, 2, (m, k // 128, 1), generator=gen)
+    x[..., 0] = 127
+    x = x * frac * torch.exp2(exp)
+    x[0, 0] = 0
+    if k > 128:
+        x[0, 1] = 0
+        x[0, 1, 77] = x.abs().max()
+    x = x.reshape(m, k).to(DT[dtype])
+    step = torch.randint(-1, 2, (m, k), generator=gen)
+    raw = x.view(torch.int16 if dtype != "f32" else torch.int32)
+    near = (raw + step.to(raw.dtype)).view(DT[dtype])
+    return torch.where(torch.isfinite(near) & (x != 0), near, x)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("m,k", [(1, 1024), (2, 5120), (4, 2176), (3, 17408)])
+def test_linear_w4_codes_at_rounding_borders(m, k, dtype):
+    """The in-kernel quantiser's codes: the same y, bit for bit, as from pq2_quantize_act_i8's q and xs, which are
+    those of the definition, with one weight column standing out per row so that single codes show."""
+    announce(f"linear w4 rounding borders {dtype} m={m} k={k}")
+    n = 256
+    x = hard_activations(m, k, dtype, m + k)
+    want_q, want_s = ref.quantised(x, k)
+    xd = x.to(DEV)
+    q, xs = quantise(xd, k)
+    assert torch.equal(q.cpu().double().view(want_q.shape), want_q) and torch.equal(xs.cpu().double(), want_s)
+    tiles, _, _ = w4(n, k, 32, 77)
+    y, z = torch.empty((m, n), device=DEV), torch.empty((m, n), device=DEV)
+    _pq2().pq2_matmul_w4(q, xs, tiles, y, 32)
+    _pq2().pq2_linear_w4(xd, tiles, z, 32, torch.zeros_like(q), torch.zeros_like(xs))
+    torch.cuda.synchronize()
+    assert torch.equal(y.view(torch.int32), z.view(torch.int32))
+
+
 @pytest.mark.parametrize("m", [4, 16, 64])
 def test_w4_a_bad_row_stays_alone(m):
     """NaN scales in one row of xs reach that row's outputs only (k ends inside a segment)."""
