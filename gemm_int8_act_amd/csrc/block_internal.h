@@ -72,13 +72,13 @@ __device__ __forceinline__ v4i w4_operand(uint32_t d0, uint32_t d1) {
 
 __device__ __forceinline__ float half_bits(uint32_t h) { return __half2float(__ushort_as_half((unsigned short)h)); }
 
-// The lane's 16 elements v of a 128-element activation group (eight aligned
-// lanes) as INT8 codes in natural order, and the group's scale: the codes of
-// pq2_quantize_act_i8, q = clamp(rint(RN(v / d)), +-127) with d = scale, or 1
-// for an all-zero group.
+// INT8 codes of N elements v of an activation group whose largest magnitude
+// is amax: q = clamp(rint(RN(v / d)), +-127), d = scale = RN(amax / 127) or 1
+// for an all-zero group, the steps of pq2_quantize_act_i8.  The low byte of
+// bits[e] is the code.
 //
 // RN(v / d) comes from FP32 operations alone (a double product per element,
-// as in the other quantisers, issues at half their rate and these kernels
+// as in quantize.hip, issues at half their rate and the decode kernels
 // quantise in every workgroup): with d scaled to [1, 2) by a power of two,
 // y = RN(1 / d) and t0 = RN(v y) within an ulp of the quotient, the residual
 // v - t0 d is exact in one fma and RN(t0 + residual y) is the correctly
@@ -86,32 +86,41 @@ __device__ __forceinline__ float half_bits(uint32_t h) { return __half2float(__u
 // IBM RISC System/6000 processor", 1990).  Scaling v by the same power is
 // exact for every quotient that does not round to 0: |v / d| >= 1/4 leaves
 // |v| >= 1/4.
-__device__ __forceinline__ uint4 quantize16(const float (&v)[16], float& scale) {
+template <int N>
+__device__ __forceinline__ void quantise_bits(const float (&v)[N], float amax, float& scale, uint32_t (&bits)[N]) {
 #pragma clang fp contract(off)
-    float amax = 0.0f;
-#pragma unroll
-    for (int e = 0; e < 16; ++e) amax = fmaxf(amax, fabsf(v[e]));
-    amax = max8_f(amax);
     scale = amax / 127.0f;
     const float d = scale > 0.0f ? scale : 1.0f;
     const int exp = __builtin_amdgcn_frexp_expf(d) - 1;
     const float dn = __builtin_ldexpf(d, -exp);
     const float y = 1.0f / dn;
     constexpr float kRound = 12582912.0f;  // 1.5 * 2^23: adding it rounds to an integer, ties to even
-    uint32_t bits[16];
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
+    for (int e = 0; e < N; ++e) {
         const float x = __builtin_ldexpf(v[e], -exp);
         const float t0 = x * y;
         const float t = __builtin_fmaf(__builtin_fmaf(-t0, dn, x), y, t0);
         bits[e] = __float_as_uint(__builtin_amdgcn_fmed3f(t, -127.0f, 127.0f) + kRound);
     }
-    auto low4 = [&](int e) {
-        const uint32_t a = __builtin_amdgcn_perm(bits[e + 1], bits[e], 0x0C0C0400u);
-        const uint32_t b = __builtin_amdgcn_perm(bits[e + 3], bits[e + 2], 0x0C0C0400u);
-        return a | (b << 16);
-    };
-    return make_uint4(low4(0), low4(4), low4(8), low4(12));
+}
+
+// Codes e .. e + 3 in one dword.
+template <int N>
+__device__ __forceinline__ uint32_t code_bytes(const uint32_t (&bits)[N], int e) {
+    const uint32_t a = __builtin_amdgcn_perm(bits[e + 1], bits[e], 0x0C0C0400u);
+    const uint32_t b = __builtin_amdgcn_perm(bits[e + 3], bits[e + 2], 0x0C0C0400u);
+    return a | (b << 16);
+}
+
+// The lane's 16 elements of a 128-element activation group (eight aligned
+// lanes) as codes in natural order, and the group's scale.
+__device__ __forceinline__ uint4 quantize16(const float (&v)[16], float& scale) {
+    float amax = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) amax = fmaxf(amax, fabsf(v[e]));
+    uint32_t bits[16];
+    quantise_bits(v, max8_f(amax), scale, bits);
+    return make_uint4(code_bytes(bits, 0), code_bytes(bits, 4), code_bytes(bits, 8), code_bytes(bits, 12));
 }
 
 // fp16 number i (0..7) of 16 bytes.

@@ -14,6 +14,9 @@
 // load to the codes, so every tensor is read once and written once; chunk
 // t + i * threads, so 16, 8 or 4 neighbouring lanes of a wave hold an
 // activation group and its maximum is a DPP reduction inside a row of 16.
+// All loads, the norm weights' and the gate's among them, go out before the
+// first sum, so a row waits for memory once.  Few rows are bound by that
+// latency and the two reductions, many by memory.
 #include "../../include/pq2_block.h"
 #include "block_internal.h"
 
@@ -32,44 +35,56 @@ struct NormKernelArgs {
     int8_t* q;
     float* xs;
     int64_t r_stride, block_stride, gate_stride, r_out_stride, x_out_stride;
-    double eps;
+    double eps, inv_k;
     float alpha;
-    int k, agroup, block_dtype, w_dtype, x_dtype, unit_offset;
+    int k, agroup, r_dtype, block_dtype, w_dtype, x_dtype, unit_offset;
 };
 
 __device__ __forceinline__ float from16(uint32_t b, bool f16) {
     return f16 ? half_bits(b) : __uint_as_float(b << 16);
 }
 
-// Eight consecutive elements from element i of p; dtype is uniform.
+// Eight consecutive elements as loaded; `hi` for FP32 only.
+struct Raw8 {
+    uint4 lo, hi;
+};
+
+// From element i of p; dtype is uniform.
 template <bool VEC>
-__device__ __forceinline__ void load8(const void* p, int64_t i, int dtype, float (&v)[8]) {
+__device__ __forceinline__ void load8(const void* p, int64_t i, int dtype, Raw8& w) {
     if (dtype == 2) {
-        const float* f = static_cast<const float*>(p) + i;
+        const uint32_t* f = static_cast<const uint32_t*>(p) + i;
         if constexpr (VEC) {
-            const float4 a = *reinterpret_cast<const float4*>(f);
-            const float4 b = *reinterpret_cast<const float4*>(f + 4);
-            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-            v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+            w.lo = *reinterpret_cast<const uint4*>(f);
+            w.hi = *reinterpret_cast<const uint4*>(f + 4);
         } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = f[e];
+            w.lo = make_uint4(f[0], f[1], f[2], f[3]);
+            w.hi = make_uint4(f[4], f[5], f[6], f[7]);
         }
         return;
     }
     const uint16_t* h = static_cast<const uint16_t*>(p) + i;
-    uint32_t w[4];
     if constexpr (VEC) {
-        const uint4 a = *reinterpret_cast<const uint4*>(h);
-        w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+        w.lo = *reinterpret_cast<const uint4*>(h);
     } else {
+        auto two = [&](int e) { return (uint32_t)h[e] | ((uint32_t)h[e + 1] << 16); };
+        w.lo = make_uint4(two(0), two(2), two(4), two(6));
+    }
+}
+
+__device__ __forceinline__ void widen8(const Raw8& w, int dtype, float (&v)[8]) {
+    if (dtype == 2) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) w[e] = (uint32_t)h[2 * e] | ((uint32_t)h[2 * e + 1] << 16);
+        for (int e = 0; e < 4; ++e) {
+            v[e] = __uint_as_float(word_of(w.lo, e));
+            v[4 + e] = __uint_as_float(word_of(w.hi, e));
+        }
+        return;
     }
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        v[2 * e] = from16(w[e] & 0xFFFFu, dtype == 1);
-        v[2 * e + 1] = from16(w[e] >> 16, dtype == 1);
+        v[2 * e] = from16(word_of(w.lo, e) & 0xFFFFu, dtype == 1);
+        v[2 * e + 1] = from16(word_of(w.lo, e) >> 16, dtype == 1);
     }
 }
 
@@ -120,106 +135,156 @@ __device__ __forceinline__ void store8(void* p, int64_t i, int dtype, const floa
     }
 }
 
-// Sum over the workgroup, the same in every thread: lanes by xor steps, then
-// the waves in index order.  `part` holds one double per wave and is not
-// touched again before another barrier.
-__device__ __forceinline__ double block_sum(double v, double* part) {
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d);
-    const int wave = threadIdx.x >> 6;
-    if ((threadIdx.x & 63) == 0) part[wave] = v;
-    __syncthreads();
-    const int waves = blockDim.x >> 6;
-    double s = part[0];
-    for (int i = 1; i < waves; ++i) s += part[i];
-    return s;
+template <int CTRL>
+__device__ __forceinline__ double dpp_d(double v) {
+    const long long b = __double_as_longlong(v);
+    const uint32_t lo = (uint32_t)dpp_i<CTRL>((int)(uint32_t)b), hi = (uint32_t)dpp_i<CTRL>((int)(b >> 32));
+    return __longlong_as_double(((long long)hi << 32) | lo);
 }
 
-// CH chunks per thread; RD the stream's dtype; VEC: every row base is
-// 16-byte aligned.
-template <int CH, int RD, bool VEC>
+__device__ __forceinline__ void add_one(float (&f)[8]) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = 1.0f + f[e];
+}
+
+// Sum over each aligned row of 16 lanes; all lanes agree.
+__device__ __forceinline__ double sum16_d(double v) {
+    v += dpp_d<kDppXor1>(v);
+    v += dpp_d<kDppXor2>(v);
+    v += dpp_d<kDppHalfMirror>(v);
+    v += dpp_d<kDppMirror>(v);
+    return v;
+}
+
+// Sum over the workgroup's (at most 16) waves, the same in every thread: rows
+// of 16 lanes, then the 4 rows of each of the 16 waves from LDS, in a fixed
+// order.  `part` holds 64 doubles, and is not touched again before another
+// barrier.
+__device__ __forceinline__ double block_sum(double v, double* part) {
+    v = sum16_d(v);
+    const int lane = threadIdx.x & 63, rows = blockDim.x >> 4;
+    if ((threadIdx.x & 15) == 0) part[threadIdx.x >> 4] = v;
+    __syncthreads();
+    double s = lane < rows ? part[lane] : 0.0;
+    s = sum16_d(s);
+    // The four rows' sums, read from one lane of each.
+    auto row_sum = [&](int r) {
+        const long long b = __double_as_longlong(s);
+        const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)b, 16 * r);
+        const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(b >> 32), 16 * r);
+        return __longlong_as_double(((long long)hi << 32) | lo);
+    };
+    return (row_sum(0) + row_sum(1)) + (row_sum(2) + row_sum(3));
+}
+
+// CH chunks per thread; VEC: every row base is 16-byte aligned; RD, BD, WD:
+// element types of the stream, the block and the vectors, known at compile
+// time or (-1) from the arguments (the branches per element cost a third of
+// the instructions: m = 4096, K = 5120, 61 us with all of them at run time).
+template <int CH, bool VEC, int RD, int BD, int WD>
 __global__ __launch_bounds__(1024) void block_norm_kernel(NormKernelArgs a) {
 #pragma clang fp contract(off)
-    __shared__ double part[2][16];
+    const int r_dtype = RD >= 0 ? RD : a.r_dtype, b_dtype = BD >= 0 ? BD : a.block_dtype,
+              w_dtype = WD >= 0 ? WD : a.w_dtype;
+    // Longer rows load the vectors where they are used: registers.
+    constexpr bool EARLY = CH <= 2;
+    __shared__ double part[2][64];
     const int64_t row = blockIdx.x;
     const int chunks = a.k >> 3;
     const int t = threadIdx.x, threads = blockDim.x;
+    const bool codes = a.q || a.x_out;
 
-    float v[CH][8];
+    Raw8 rr[CH], rb[CH], rp[EARLY ? CH : 1], rg[EARLY ? CH : 1], rw[EARLY ? CH : 1];
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
         const int ch = t + c * threads;
-        if (ch < chunks) {
-            load8<VEC>(a.r, row * a.r_stride + 8 * ch, RD, v[c]);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[c][e] = 0.0f;
+        rr[c] = rb[c] = Raw8{};
+        if constexpr (EARLY) rp[c] = rg[c] = rw[c] = Raw8{};
+        if (ch >= chunks) continue;
+        if (a.block) load8<VEC>(a.block, row * a.block_stride + 8 * ch, b_dtype, rb[c]);
+        load8<VEC>(a.r, row * a.r_stride + 8 * ch, r_dtype, rr[c]);
+        if constexpr (EARLY) {
+            if (a.post_w) load8<VEC>(a.post_w, 8 * ch, w_dtype, rp[c]);
+            if (a.gate) load8<VEC>(a.gate, row * a.gate_stride + 8 * ch, w_dtype, rg[c]);
+            if (codes) load8<VEC>(a.w, 8 * ch, w_dtype, rw[c]);
         }
     }
+    // The vector of chunk ch, loaded now or before.
+    auto vec8 = [&](const void* p, int64_t off, int ch, const Raw8& early, float (&f)[8]) {
+        if constexpr (EARLY) {
+            widen8(early, w_dtype, f);
+        } else {
+            Raw8 w{};
+            if (ch < chunks) load8<VEC>(p, off + 8 * ch, w_dtype, w);
+            widen8(w, w_dtype, f);
+        }
+    };
+
+    float v[CH][8];
     if (a.block) {
         float b[CH][8];
 #pragma unroll
-        for (int c = 0; c < CH; ++c) {
-            const int ch = t + c * threads;
-            if (ch < chunks) {
-                load8<VEC>(a.block, row * a.block_stride + 8 * ch, a.block_dtype, b[c]);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) b[c][e] = 0.0f;
-            }
-        }
-        float rstd = 1.0f;
+        for (int c = 0; c < CH; ++c) widen8(rb[c], b_dtype, b[c]);
         if (a.post_w) {
             double s = 0.0;
 #pragma unroll
             for (int c = 0; c < CH; ++c)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) s += (double)b[c][e] * (double)b[c][e];
-            rstd = (float)(1.0 / sqrt(block_sum(s, part[0]) / (double)a.k + a.eps));
-        }
+                for (int e = 0; e < 8; ++e) s = __builtin_fma((double)b[c][e], (double)b[c][e], s);
+            const float rstd = (float)rsqrt(block_sum(s, part[0]) * a.inv_k + a.eps);
 #pragma unroll
-        for (int c = 0; c < CH; ++c) {
-            const int ch = t + c * threads;
-            if (ch >= chunks) continue;
-            float f[8];
-            if (a.post_w) {
-                load8<VEC>(a.post_w, 8 * ch, a.w_dtype, f);
+            for (int c = 0; c < CH; ++c) {
+                float f[8];
+                vec8(a.post_w, 0, t + c * threads, rp[EARLY ? c : 0], f);
+                if (a.unit_offset) add_one(f);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) b[c][e] = (b[c][e] * rstd) * (a.unit_offset ? 1.0f + f[e] : f[e]);
+                for (int e = 0; e < 8; ++e) b[c][e] = (b[c][e] * rstd) * f[e];
             }
-            if (a.gate) {
-                load8<VEC>(a.gate, row * a.gate_stride + 8 * ch, a.w_dtype, f);
+        }
+        if (a.gate) {
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+                float f[8];
+                vec8(a.gate, row * a.gate_stride, t + c * threads, rg[EARLY ? c : 0], f);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) b[c][e] *= f[e];
             }
+        }
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            widen8(rr[c], r_dtype, v[c]);
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[c][e] += b[c][e] * a.alpha;
-            round8(v[c], RD);
+            round8(v[c], r_dtype);
         }
+    } else {
+#pragma unroll
+        for (int c = 0; c < CH; ++c) widen8(rr[c], r_dtype, v[c]);
     }
     if (a.r_out) {
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
             const int ch = t + c * threads;
-            if (ch < chunks) store8<VEC>(a.r_out, row * a.r_out_stride + 8 * ch, RD, v[c]);
+            if (ch < chunks) store8<VEC>(a.r_out, row * a.r_out_stride + 8 * ch, r_dtype, v[c]);
         }
     }
-    if (!a.q && !a.x_out) return;
+    if (!codes) return;
 
     double s = 0.0;
 #pragma unroll
     for (int c = 0; c < CH; ++c)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) s += (double)v[c][e] * (double)v[c][e];
-    const float rstd = (float)(1.0 / sqrt(block_sum(s, part[1]) / (double)a.k + a.eps));
+        for (int e = 0; e < 8; ++e) s = __builtin_fma((double)v[c][e], (double)v[c][e], s);
+    const float rstd = (float)rsqrt(block_sum(s, part[1]) * a.inv_k + a.eps);
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
         const int ch = t + c * threads;
         if (ch >= chunks) continue;  // whole groups: a group's chunks are 16, 8 or 4 aligned lanes of one wave
         float f[8];
-        load8<VEC>(a.w, 8 * ch, a.w_dtype, f);
+        vec8(a.w, 0, ch, rw[EARLY ? c : 0], f);
+        if (a.unit_offset) add_one(f);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[c][e] = (v[c][e] * rstd) * (a.unit_offset ? 1.0f + f[e] : f[e]);
+        for (int e = 0; e < 8; ++e) v[c][e] = (v[c][e] * rstd) * f[e];
         round8(v[c], a.x_dtype);
         if (a.x_out) store8<VEC>(a.x_out, row * a.x_out_stride + 8 * ch, a.x_dtype, v[c]);
         if (!a.q) continue;
@@ -230,40 +295,42 @@ __global__ __launch_bounds__(1024) void block_norm_kernel(NormKernelArgs a) {
         amax = fmaxf(amax, dpp_f<kDppXor2>(amax));
         if (a.agroup >= 64) amax = fmaxf(amax, dpp_f<kDppHalfMirror>(amax));
         if (a.agroup == 128) amax = fmaxf(amax, dpp_f<kDppMirror>(amax));
-        // The quantiser's steps (quantize.hip): the IEEE quotient v / d as the
-        // double product v * fl64(1 / d) rounded to fp32.
-        const float scale = amax / 127.0f;
-        const double inv = 1.0 / (double)(scale > 0.0f ? scale : 1.0f);
-        uint32_t packed[2] = {0u, 0u};
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            float r = rintf((float)((double)v[c][e] * inv));
-            r = fminf(127.0f, fmaxf(-127.0f, r));
-            packed[e >> 2] |= ((uint32_t)(int)r & 0xFFu) << (8 * (e & 3));
-        }
-        *reinterpret_cast<uint2*>(a.q + row * a.k + 8 * ch) = make_uint2(packed[0], packed[1]);
+        uint32_t bits[8];
+        float scale;
+        quantise_bits(v[c], amax, scale, bits);
+        *reinterpret_cast<uint2*>(a.q + row * a.k + 8 * ch) = make_uint2(code_bytes(bits, 0), code_bytes(bits, 4));
         const int lanes = a.agroup >> 3;
         if ((ch & (lanes - 1)) == 0) a.xs[row * (a.k / a.agroup) + ch / lanes] = scale;
     }
 }
 
-template <int CH, int RD>
-hipError_t launch_one(const NormKernelArgs& a, int64_t m, int threads, bool vec, hipStream_t stream) {
+template <int CH, bool VEC, int RD, int BD, int WD>
+hipError_t launch_one(const NormKernelArgs& a, int64_t m, int threads, hipStream_t stream) {
     clear_stale_error();
-    if (vec)
-        hipLaunchKernelGGL((block_norm_kernel<CH, RD, true>), dim3((unsigned)m), dim3(threads), 0, stream, a);
-    else
-        hipLaunchKernelGGL((block_norm_kernel<CH, RD, false>), dim3((unsigned)m), dim3(threads), 0, stream, a);
+    hipLaunchKernelGGL((block_norm_kernel<CH, VEC, RD, BD, WD>), dim3((unsigned)m), dim3(threads), 0, stream, a);
     return hipGetLastError();
 }
 
+// Streams of every type with an FP32 or bf16 block and bf16 vectors have
+// kernels of their own, for rows of up to four chunks a thread.
+template <int CH, int RD>
+hipError_t launch_typed(const NormKernelArgs& a, int64_t m, int threads, hipStream_t stream) {
+    if (a.w_dtype == 0 && a.block_dtype == 2) return launch_one<CH, true, RD, 2, 0>(a, m, threads, stream);
+    if (a.w_dtype == 0 && a.block_dtype == 0) return launch_one<CH, true, RD, 0, 0>(a, m, threads, stream);
+    return launch_one<CH, true, -1, -1, -1>(a, m, threads, stream);
+}
+
 template <int CH>
-hipError_t launch_ch(const NormKernelArgs& a, int rd, int64_t m, int threads, bool vec, hipStream_t stream) {
-    switch (rd) {
-        case 0: return launch_one<CH, 0>(a, m, threads, vec, stream);
-        case 1: return launch_one<CH, 1>(a, m, threads, vec, stream);
-        default: return launch_one<CH, 2>(a, m, threads, vec, stream);
+hipError_t launch_ch(const NormKernelArgs& a, int64_t m, int threads, bool vec, hipStream_t stream) {
+    if (!vec) return launch_one<CH, false, -1, -1, -1>(a, m, threads, stream);
+    if constexpr (CH <= 4) {
+        switch (a.r_dtype) {
+            case 0: return launch_typed<CH, 0>(a, m, threads, stream);
+            case 1: return launch_typed<CH, 1>(a, m, threads, stream);
+            default: return launch_typed<CH, 2>(a, m, threads, stream);
+        }
     }
+    return launch_one<CH, true, -1, -1, -1>(a, m, threads, stream);
 }
 
 bool rows_aligned(const void* p, int64_t stride, int dtype) {
@@ -289,9 +356,11 @@ hipError_t launch_block_norm(const pq2_block_norm_args& p, hipStream_t stream) {
     a.r_out_stride = p.r_out_stride;
     a.x_out_stride = p.x_out_stride;
     a.eps = p.eps;
+    a.inv_k = 1.0 / (double)p.k;
     a.alpha = p.alpha;
     a.k = (int)p.k;
     a.agroup = p.q ? (int)p.agroup : 128;
+    a.r_dtype = p.r_dtype;
     a.block_dtype = p.block_dtype;
     a.w_dtype = p.w_dtype;
     a.x_dtype = p.x_dtype;
@@ -303,14 +372,18 @@ hipError_t launch_block_norm(const pq2_block_norm_args& p, hipStream_t stream) {
                      (!p.r_out || rows_aligned(p.r_out, p.r_out_stride, p.r_dtype)) &&
                      (!p.x_out || rows_aligned(p.x_out, p.x_out_stride, p.x_dtype));
     const int chunks = (int)(p.k / 8);
-    int ch = 1;
+    // One chunk a thread while rows are few (their latency counts), two when
+    // there are enough rows to fill the chip with smaller workgroups (K = 5120,
+    // norms on both sides: m = 256 7.1 against 7.4 us, m = 1024 18.2 against
+    // 16.5, m = 4096 58.7 against 51.6; K = 640, m = 4096 11.3 against 11.5).
+    int ch = p.m >= 768 && chunks > 128 ? 2 : 1;
     while ((chunks + ch - 1) / ch > 1024) ch *= 2;  // k <= 65536: at most 8
     const int threads = ((chunks + ch - 1) / ch + 63) / 64 * 64;
     switch (ch) {
-        case 1: return launch_ch<1>(a, p.r_dtype, p.m, threads, vec, stream);
-        case 2: return launch_ch<2>(a, p.r_dtype, p.m, threads, vec, stream);
-        case 4: return launch_ch<4>(a, p.r_dtype, p.m, threads, vec, stream);
-        default: return launch_ch<8>(a, p.r_dtype, p.m, threads, vec, stream);
+        case 1: return launch_ch<1>(a, p.m, threads, vec, stream);
+        case 2: return launch_ch<2>(a, p.m, threads, vec, stream);
+        case 4: return launch_ch<4>(a, p.m, threads, vec, stream);
+        default: return launch_ch<8>(a, p.m, threads, vec, stream);
     }
 }
 
