@@ -140,41 +140,52 @@ def pq2_prepare_w4_tiles(codes, scales, wgroup: int, tiles, stream=None) -> None
           _row_stride(codes), scales.data_ptr(), _row_stride(scales), n, k, wgroup, tiles.data_ptr())
 
 
+# The checks below run on every call of a decode step and are written for few
+# attribute reads (a tensor attribute costs about 0.1 us of host time).
+_F32, _I8, _U8 = torch.float32, torch.int8, torch.uint8
+_Y = (_F32,)
+_H = tuple(_DTYPE)
+
+
 def _row_stride(t):
     """Row stride in elements; a single row's is its length, whatever the tensor says."""
     return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
 
 
 def _weights(tiles, need):
-    if tiles.dtype != torch.uint8 or not tiles.is_contiguous() or tiles.numel() < need:
+    if tiles.dtype is not _U8 or tiles.numel() < need or not tiles.is_contiguous():
         raise ValueError("weights: contiguous uint8 tensor of the prepared layout's size expected")
     return tiles.data_ptr()
 
 
 def _codes(q, xs, m):
-    if q.dtype != torch.int8 or xs.dtype != torch.float32 or not q.is_contiguous() or not xs.is_contiguous():
+    if q.dtype is not _I8 or xs.dtype is not _F32 or not q.is_contiguous() or not xs.is_contiguous():
         raise ValueError("q contiguous int8 and xs contiguous float32 expected")
-    if q.dim() != 2 or q.shape[0] != m or xs.numel() != m * (q.shape[1] // 128):
+    rows, k = q.shape
+    if rows != m or xs.numel() * 128 != m * k:
         raise ValueError("shape mismatch: q [m][k], xs [m][k/128] expected")
-    return q.shape[1]
+    return k
 
 
 def _out(t, name, dtypes):
-    if t.dtype not in dtypes or t.dim() != 2 or not t.is_contiguous():
+    if t.dtype not in dtypes or not t.is_contiguous():
         raise ValueError(f"{name}: contiguous 2-D tensor of {', '.join(str(d) for d in dtypes)} expected")
-    return t.shape
+    m, n = t.shape
+    return m, n
 
 
 def _x(x, m, k):
-    if x.dim() != 2 or x.stride(1) != 1 or x.shape[0] != m or x.shape[1] < k:
+    rows, width = x.shape
+    stride, unit = x.stride()
+    if unit != 1 or rows != m or width < k:
         raise ValueError("x must be [m][>= k] with unit column stride")
-    return x.data_ptr(), _dtype(x, "x"), _row_stride(x)
+    return x.data_ptr(), _dtype(x, "x"), stride if m > 1 else max(stride, width)
 
 
 def pq2_matmul_w4(q, xs, tiles, y, wgroup: int, stream=None) -> None:
     """y [m][n] (float32) = 4-bit weights x INT8 activations, any m >= 1; q int8 [m][k] and xs float32 [m][k/128]
     from pq2_quantize_act_i8 or pq2_block_norm."""
-    m, n = _out(y, "y", (torch.float32,))
+    m, n = _out(y, "y", _Y)
     k = _codes(q, xs, m)
     w = _weights(tiles, pq2_w4_tiles_bytes(n, k, wgroup))
     _call("pq2_matmul_w4", _device(q, xs, tiles, y), stream, q.data_ptr(), xs.data_ptr(), w, m, n, k, wgroup,
@@ -184,7 +195,7 @@ def pq2_matmul_w4(q, xs, tiles, y, wgroup: int, stream=None) -> None:
 def pq2_linear_w4(x, tiles, y, wgroup: int, q_work, xs_work, stream=None) -> None:
     """The complete call: x [m][>= k] bf16/f16/f32 quantised into q_work / xs_work (scratch, int8 [m][k] and float32
     [m][k/128]), then pq2_matmul_w4."""
-    m, n = _out(y, "y", (torch.float32,))
+    m, n = _out(y, "y", _Y)
     k = _codes(q_work, xs_work, m)
     w = _weights(tiles, pq2_w4_tiles_bytes(n, k, wgroup))
     _call("pq2_linear_w4", _device(x, tiles, y, q_work, xs_work), stream, *_x(x, m, k), w, m, n, k, wgroup,
@@ -194,7 +205,7 @@ def pq2_linear_w4(x, tiles, y, wgroup: int, q_work, xs_work, stream=None) -> Non
 def pq2_gated_matmul_tiles(q, xs, gate, up, h, act: int = ACT_SILU, stream=None) -> None:
     """h [m][n] (bf16/f16/f32) = act(gate product) * up product in one kernel; gate and up are ternary tile layouts of
     one shape, q / xs as pq2_matmul_w4."""
-    m, n = _out(h, "h", tuple(_DTYPE))
+    m, n = _out(h, "h", _H)
     k = _codes(q, xs, m)
     need = _tiles_bytes(n, k)
     _call("pq2_gated_matmul_tiles", _device(q, xs, gate, up, h), stream, q.data_ptr(), xs.data_ptr(),
@@ -203,7 +214,7 @@ def pq2_gated_matmul_tiles(q, xs, gate, up, h, act: int = ACT_SILU, stream=None)
 
 def pq2_gated_matmul_w4(q, xs, gate, up, h, wgroup: int, act: int = ACT_SILU, stream=None) -> None:
     """pq2_gated_matmul_tiles with 4-bit weights in the w4 tile layout."""
-    m, n = _out(h, "h", tuple(_DTYPE))
+    m, n = _out(h, "h", _H)
     k = _codes(q, xs, m)
     need = pq2_w4_tiles_bytes(n, k, wgroup)
     _call("pq2_gated_matmul_w4", _device(q, xs, gate, up, h), stream, q.data_ptr(), xs.data_ptr(),
@@ -212,7 +223,7 @@ def pq2_gated_matmul_w4(q, xs, gate, up, h, wgroup: int, act: int = ACT_SILU, st
 
 def pq2_gated_linear_tiles(x, gate, up, h, q_work, xs_work, act: int = ACT_SILU, stream=None) -> None:
     """The complete call of pq2_gated_matmul_tiles: x quantised into the scratch first."""
-    m, n = _out(h, "h", tuple(_DTYPE))
+    m, n = _out(h, "h", _H)
     k = _codes(q_work, xs_work, m)
     need = _tiles_bytes(n, k)
     _call("pq2_gated_linear_tiles", _device(x, gate, up, h, q_work, xs_work), stream, *_x(x, m, k),
@@ -222,7 +233,7 @@ def pq2_gated_linear_tiles(x, gate, up, h, q_work, xs_work, act: int = ACT_SILU,
 
 def pq2_gated_linear_w4(x, gate, up, h, wgroup: int, q_work, xs_work, act: int = ACT_SILU, stream=None) -> None:
     """The complete call of pq2_gated_matmul_w4: x quantised into the scratch first."""
-    m, n = _out(h, "h", tuple(_DTYPE))
+    m, n = _out(h, "h", _H)
     k = _codes(q_work, xs_work, m)
     need = pq2_w4_tiles_bytes(n, k, wgroup)
     _call("pq2_gated_linear_w4", _device(x, gate, up, h, q_work, xs_work), stream, *_x(x, m, k),
@@ -230,14 +241,15 @@ def pq2_gated_linear_w4(x, gate, up, h, wgroup: int, q_work, xs_work, act: int =
           q_work.data_ptr(), xs_work.data_ptr())
 
 
-def _rows(t, name, m, k):
-    if t.dim() != 2 or t.shape != (m, k) or t.stride(1) != 1:
+def _rows(t, name, shape):
+    st = t.stride()
+    if t.shape != shape or st[1] != 1:
         raise ValueError(f"{name} must be [m][k] with unit column stride")
-    return t.data_ptr(), _row_stride(t)
+    return t.data_ptr(), st[0] if shape[0] > 1 else max(st[0], shape[1])
 
 
 def _vector(t, name, k, dtype):
-    if t.dim() != 1 or t.shape[0] != k or t.stride(0) != 1 or t.dtype != dtype:
+    if t.shape != (k,) or t.dtype is not dtype or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous [k] tensor of the norm weights' dtype")
     return t.data_ptr()
 
@@ -252,44 +264,43 @@ def pq2_block_norm(r, w, eps: float, *, block=None, post_w=None, gate=None, alph
     dtype; may be r itself), x_out (x_dtype), and q int8 [m][k] with xs float32 [m][k/agroup].  x is rounded to
     x_dtype (x_out's dtype if not given, else r's) before it is quantised, so q and xs are those of
     pq2_quantize_act_i8_g on x_out.  post_w and gate have w's dtype."""
-    if r.dim() != 2:
-        raise ValueError("r must be [m][k]")
-    m, k = r.shape
-    wt = w.dtype
-    rp, rs = _rows(r, "r", m, k)
+    shape = r.shape
+    m, k = shape
+    rt, wt = r.dtype, w.dtype
+    rp, rs = _rows(r, "r", shape)
     wp = _vector(w, "w", k, wt)
     bp = bs = bd = pp = gp = gs = op = os_ = xp = xst = qp = sp = 0
     if block is not None:
-        bp, bs = _rows(block, "block", m, k)
+        bp, bs = _rows(block, "block", shape)
         bd = _dtype(block, "block")
     if post_w is not None:
         pp = _vector(post_w, "post_w", k, wt)
     if gate is not None:
-        if gate.dim() == 1:
+        if len(gate.shape) == 1:
             gp = _vector(gate, "gate", k, wt)
-        elif gate.dtype != wt:
+        elif gate.dtype is not wt:
             raise ValueError("gate must have the norm weights' dtype")
         else:
-            gp, gs = _rows(gate, "gate", m, k)
+            gp, gs = _rows(gate, "gate", shape)
     if r_out is not None:
-        if r_out.dtype != r.dtype:
+        if r_out.dtype is not rt:
             raise ValueError("r_out must have r's dtype")
-        op, os_ = _rows(r_out, "r_out", m, k)
+        op, os_ = _rows(r_out, "r_out", shape)
     if x_out is not None:
-        if x_dtype is not None and x_out.dtype != x_dtype:
+        if x_dtype is not None and x_out.dtype is not x_dtype:
             raise ValueError("x_out must have x_dtype")
-        xp, xst = _rows(x_out, "x_out", m, k)
+        xp, xst = _rows(x_out, "x_out", shape)
         x_dtype = x_out.dtype
-    xd = _DTYPE.get(r.dtype if x_dtype is None else x_dtype)
+    xd = _DTYPE.get(rt if x_dtype is None else x_dtype)
     if xd is None:
         raise ValueError(f"unsupported x_dtype {x_dtype}")
     if q is not None:
-        if q.dtype != torch.int8 or not q.is_contiguous() or q.shape != (m, k):
+        if q.dtype is not _I8 or q.shape != shape or not q.is_contiguous():
             raise ValueError("q must be a contiguous int8 [m][k] tensor")
         qp = q.data_ptr()
     if xs is not None:
-        if xs.dtype != torch.float32 or not xs.is_contiguous() or agroup not in (128, 64, 32) or \
-                xs.numel() != m * (k // agroup):
+        if xs.dtype is not _F32 or agroup not in (128, 64, 32) or xs.numel() * agroup != m * k or \
+                not xs.is_contiguous():
             raise ValueError("xs must be a contiguous float32 [m][k/agroup] tensor, agroup 128, 64 or 32")
         sp = xs.data_ptr()
     args = _NORM.pack(rp, rs, bp, bs, pp, gp, gs, wp, op, os_, xp, xst, qp, sp, m, k, agroup, eps, alpha,
