@@ -87,7 +87,7 @@ int linear(const void* x, int dtype, int64_t stride, const void* w0, const void*
     // Few columns: one launch, which reads x with 16-byte loads and 32-bit
     // offsets (the same bits, the scratch untouched).
     const int es = esize(dtype);
-    if (pq2::block_takes_x(m) && aligned(x, 16) && (stride * es) % 16 == 0 && xspan.bytes < ((size_t)1 << 31)) {
+    if (pq2::block_takes_x(m, k) && aligned(x, 16) && (stride * es) % 16 == 0 && xspan.bytes < ((size_t)1 << 31)) {
         p.src = pq2::src_of_dtype(dtype);
         p.x = x;
         p.x_stride = stride;

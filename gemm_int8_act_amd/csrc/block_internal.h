@@ -38,7 +38,7 @@ hipError_t launch_prepare_w4(const uint8_t* codes, int64_t codes_stride, const u
 hipError_t launch_block_small_m(const BlockMatmul& a);
 hipError_t launch_block_prefill(const BlockMatmul& a);
 bool block_takes_small_m(const BlockMatmul& a);
-bool block_takes_x(int64_t m);   // whether the decode engine quantises x itself
+bool block_takes_x(int64_t m, int64_t k);   // whether the decode engine quantises x itself
 hipError_t launch_block_norm(const pq2_block_norm_args& a, hipStream_t stream);
 
 typedef int v4i __attribute__((ext_vector_type(4)));

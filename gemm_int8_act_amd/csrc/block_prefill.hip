@@ -7,7 +7,8 @@
 // with it: both tile layouts hold the INT8 matrix core's B operand order, so
 // codes go from memory to registers and, decoded there, to
 // v_mfma_i32_16x16x64_i8 without passing through LDS.  The activations are
-// shared by the waves and go through LDS, double-buffered by group of 128,
+// shared by the waves and go through LDS, double-buffered by group of 128
+// (loads run D groups ahead, in registers),
 // quads XOR-swizzled so that the 16 rows of an operand read fall in distinct
 // banks.  Gate and up tiles of the same rows sit in one wave's registers, so
 // the gated epilogue needs no exchange.
@@ -36,7 +37,7 @@ struct PrefillArgs {
 // Slot (16-byte quads) of quad t of row i of an A buffer.
 __device__ __forceinline__ int a_slot(int i, int t) { return i * 8 + (t ^ ((i >> 1) & 7)); }
 
-template <int FMT, int S, int NB, int MT, int NT>
+template <int FMT, int S, int NB, int MT, int NT, int D>
 __global__ __launch_bounds__(256) void block_prefill_kernel(PrefillArgs a) {
 #pragma clang fp contract(off)
     constexpr int UNIT = block_unit(FMT, S);
@@ -95,17 +96,20 @@ __global__ __launch_bounds__(256) void block_prefill_kernel(PrefillArgs a) {
         q_off[p] = (uint32_t)(min(it >> 3, rows - 1) * a.k + 16 * (it & 7));
         q_slot[p] = a_slot(it >> 3, it & 7);
     }
-    uint4 areg[AQ];
+    // D groups ahead: activations on their way to LDS, and packed codes
+    // (ternary: pairs of groups), each loaded again as soon as it is used.
+    // Weight scales: RS sets of 16 bytes, 8 / S groups each.
+    constexpr int DC = FMT == kFmtTernary ? (D + 1) / 2 : D;
+    constexpr int RS = D > 1 && S == 4 ? 4 : 2;
+    constexpr int SG = 8 / S;
+    uint4 areg[D][AQ];
     uint32_t xreg[XQ];
-    // Packed codes: this group's (ternary: this pair's), loaded again as soon
-    // as they are decoded.  Weight scales: this pair's (S = 1) or group's and
-    // the next one's.
-    uint4 cw[NB][NT];
-    uint2 sc[2][NB][NT];
+    uint4 cw[DC][NB][NT];
+    uint4 sc[RS][NB][NT];
 
-    auto load_a = [&](int g) {
+    auto load_a = [&](int g, int set) {
 #pragma unroll
-        for (int p = 0; p < AQ; ++p) areg[p] = buf_load16(q_rs, q_off[p] + 128u * g);
+        for (int p = 0; p < AQ; ++p) areg[set][p] = buf_load16(q_rs, q_off[p] + 128u * g);
     };
     auto load_xs = [&](int seg) {
 #pragma unroll
@@ -115,26 +119,24 @@ __global__ __launch_bounds__(256) void block_prefill_kernel(PrefillArgs a) {
             xreg[p] = buf_load4(x_rs, g < a.groups ? (uint32_t)((min(it >> 3, rows - 1) * a.groups + g) * 4) : kBufferOOB);
         }
     };
-    auto load_codes = [&](int g) {
+    auto load_codes = [&](int g, int set) {
         const uint32_t off = (uint32_t)((g >> 3) * UNIT + (FMT == kFmtTernary ? ((g & 7) >> 1) : (g & 7)) * 1024 + 16 * lane);
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
-            for (int t = 0; t < NT; ++t) cw[b][t] = buf_load16(w_rs[b], off + t_off[t]);
+            for (int t = 0; t < NT; ++t) cw[set][b][t] = buf_load16(w_rs[b], off + t_off[t]);
     };
-    auto load_scales = [&](int g, uint2 (&to)[NB][NT]) {
-        const uint32_t off = (uint32_t)((g >> 3) * UNIT + CODES + 16 * S * j + (S == 1 ? 2 * (g & 6) : 2 * S * (g & 7)));
+    // The scales of groups g .. g + SG - 1 (g a multiple of SG).
+    auto load_scales = [&](int g, int set) {
+        const uint32_t off = (uint32_t)((g >> 3) * UNIT + CODES + 16 * S * j + 16 * ((g & 7) / SG));
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                if constexpr (S == 4) to[b][t] = buf_load8(w_rs[b], off + t_off[t]);
-                else to[b][t].x = buf_load4(w_rs[b], off + t_off[t]);
-            }
+            for (int t = 0; t < NT; ++t) sc[set][b][t] = buf_load16(w_rs[b], off + t_off[t]);
     };
-    auto store_a = [&](int buf) {
+    auto store_a = [&](int buf, int set) {
 #pragma unroll
-        for (int p = 0; p < AQ; ++p) As[buf][q_slot[p]] = areg[p];
+        for (int p = 0; p < AQ; ++p) As[buf][q_slot[p]] = areg[set][p];
     };
     auto store_xs = [&](int buf) {
 #pragma unroll
@@ -153,22 +155,32 @@ __global__ __launch_bounds__(256) void block_prefill_kernel(PrefillArgs a) {
             for (int i = 0; i < MT; ++i) acc[b][t][i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
     const int low_half = kb < 2 ? -1 : 0;
 
-    load_a(0);
+    load_a(0, 0);
     load_xs(0);
-    load_codes(0);
-    load_scales(0, sc[0]);
-    store_a(0);
+    load_codes(0, 0);
+    load_scales(0, 0);
+#pragma unroll
+    for (int i = 1; i < D; ++i)
+        if (i < a.groups) {
+            load_a(i, i);
+            if (FMT == kFmtW4 || i % 2 == 0) load_codes(i, FMT == kFmtW4 ? i : i / 2);
+        }
+#pragma unroll
+    for (int i = 1; i < RS; ++i)
+        if (i * SG < a.groups) load_scales(i * SG, i);
+    store_a(0, 0);
     store_xs(0);
     __syncthreads();
 
-    // One group; u = g modulo 4 (a constant).  Group g + 1 is loaded while g
-    // is multiplied and staged into the other buffer after it.
+    // One group; u = g modulo 8 (a constant).  Group g + D is loaded while g
+    // is multiplied, and g + 1 staged into the other buffer after it.
     auto step = [&](int g, auto uc) {
         constexpr int u = decltype(uc)::value;
         constexpr int buf = u & 1;
-        constexpr int sb = S == 1 ? u >> 1 : u & 1;   // scale set of this group
-        const bool more = g + 1 < a.groups;
-        if (more) load_a(g + 1);
+        constexpr int cs = (FMT == kFmtTernary ? u / 2 : u) % DC;   // code set of this group
+        constexpr int ss = u / SG % RS;                             // scale set
+        const bool more = g + 1 < a.groups, ahead = g + D < a.groups;
+        if (ahead) load_a(g + D, u % D);
         v4i B[NB][NT][2];
 #pragma unroll
         for (int b = 0; b < NB; ++b)
@@ -176,13 +188,29 @@ __global__ __launch_bounds__(256) void block_prefill_kernel(PrefillArgs a) {
             for (int t = 0; t < NT; ++t)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    if constexpr (FMT == kFmtTernary) B[b][t][h] = ternary_operand(word_of(cw[b][t], 2 * (u & 1) + h));
-                    else B[b][t][h] = w4_operand(word_of(cw[b][t], 2 * h), word_of(cw[b][t], 2 * h + 1));
+                    if constexpr (FMT == kFmtTernary) B[b][t][h] = ternary_operand(word_of(cw[cs][b][t], 2 * (u & 1) + h));
+                    else B[b][t][h] = w4_operand(word_of(cw[cs][b][t], 2 * h), word_of(cw[cs][b][t], 2 * h + 1));
                 }
-        if (more) {
-            if constexpr (FMT == kFmtW4 || u % 2 == 1) load_codes(g + 1);
-            if constexpr (S != 1 || u % 2 == 1) load_scales(g + 1, sc[S == 1 ? (u >> 1) ^ 1 : (u & 1) ^ 1]);
-            if ((g & 7) == 7) load_xs((g + 1) >> 3);
+        if constexpr (FMT == kFmtW4) {
+            if (ahead) load_codes(g + D, cs);
+        } else if constexpr (u % 2 == 1) {
+            if (g - 1 + 2 * DC < a.groups) load_codes(g - 1 + 2 * DC, cs);
+        }
+        // The set before this one is free from its last group on.  (S = 1: a
+        // set lasts the whole unroll, so the next one moves down.)
+        if constexpr (S == 1 && u == 0) {
+            if (g > 0) {
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) sc[0][b][t] = sc[1][b][t];
+                if (g + 8 < a.groups) load_scales(g + 8, 1);
+            }
+        } else if constexpr (u % SG == 0) {
+            if (g > 0 && g + (RS - 1) * SG < a.groups) load_scales(g + (RS - 1) * SG, (ss + RS - 1) % RS);
+        }
+        if constexpr (u == 0) {
+            if (g + 8 < a.groups) load_xs((g >> 3) + 1);
         }
         const float* xrow = &Xs[(g >> 3) & 1][g & 7][0];
 #pragma unroll
@@ -200,14 +228,14 @@ __global__ __launch_bounds__(256) void block_prefill_kernel(PrefillArgs a) {
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
                     if constexpr (S == 1) {
-                        v4i D = __builtin_amdgcn_mfma_i32_16x16x64_i8(A[0], B[b][t][0], v4i{}, 0, 0, 0);
-                        D = __builtin_amdgcn_mfma_i32_16x16x64_i8(A[1], B[b][t][1], D, 0, 0, 0);
-                        const float ws = half_bits((u & 1) ? sc[sb][b][t].x >> 16 : sc[sb][b][t].x & 0xFFFFu);
+                        v4i dot = __builtin_amdgcn_mfma_i32_16x16x64_i8(A[0], B[b][t][0], v4i{}, 0, 0, 0);
+                        dot = __builtin_amdgcn_mfma_i32_16x16x64_i8(A[1], B[b][t][1], dot, 0, 0, 0);
+                        const float ws = half_at(sc[ss][b][t], u);
 #pragma unroll
                         for (int r = 0; r < 4; ++r)
                             acc[b][t][i][r] = FMT == kFmtTernary
-                                                  ? __builtin_fmaf((float)D[r] * x[r], ws, acc[b][t][i][r])
-                                                  : __builtin_fmaf((float)D[r] * ws, x[r], acc[b][t][i][r]);
+                                                  ? __builtin_fmaf((float)dot[r] * x[r], ws, acc[b][t][i][r])
+                                                  : __builtin_fmaf((float)dot[r] * ws, x[r], acc[b][t][i][r]);
                     } else {
                         float sum[4];
 #pragma unroll
@@ -218,32 +246,32 @@ __global__ __launch_bounds__(256) void block_prefill_kernel(PrefillArgs a) {
                                 const int mask = (s & 1) ? ~low_half : low_half;
                                 Am = v4i{Am[0] & mask, Am[1] & mask, Am[2] & mask, Am[3] & mask};
                             }
-                            const v4i D = __builtin_amdgcn_mfma_i32_16x16x64_i8(Am, B[b][t][h], v4i{}, 0, 0, 0);
-                            const uint32_t pair = s < 2 ? sc[sb][b][t].x : sc[sb][b][t].y;
-                            const float ws = half_bits((s & 1) ? pair >> 16 : pair & 0xFFFFu);
+                            const v4i dot = __builtin_amdgcn_mfma_i32_16x16x64_i8(Am, B[b][t][h], v4i{}, 0, 0, 0);
+                            const float ws = half_at(sc[ss][b][t], u % SG * S + s);
 #pragma unroll
                             for (int r = 0; r < 4; ++r)
-                                sum[r] = s == 0 ? (float)D[r] * ws : __builtin_fmaf((float)D[r], ws, sum[r]);
+                                sum[r] = s == 0 ? (float)dot[r] * ws : __builtin_fmaf((float)dot[r], ws, sum[r]);
                         }
 #pragma unroll
                         for (int r = 0; r < 4; ++r) acc[b][t][i][r] = __builtin_fmaf(sum[r], x[r], acc[b][t][i][r]);
                     }
                 }
-            // S = 2: rows in turn, which keeps three waves per SIMD (FFN up,
-            // m = 1024: 189 against 221 us).
-            if constexpr (S == 2) __builtin_amdgcn_sched_barrier(0);
         }
-        if (more) {
-            store_a(buf ^ 1);
-            if ((g & 7) == 7) store_xs(((g + 1) >> 3) & 1);
+        if (more) store_a(buf ^ 1, (u + 1) % D);
+        if constexpr (u == 7) {
+            if (more) store_xs(((g >> 3) + 1) & 1);
         }
         __syncthreads();
     };
-    for (int g = 0; g < a.groups; g += 4) {
+    for (int g = 0; g < a.groups; g += 8) {
         step(g, std::integral_constant<int, 0>{});
         if (g + 1 < a.groups) step(g + 1, std::integral_constant<int, 1>{});
         if (g + 2 < a.groups) step(g + 2, std::integral_constant<int, 2>{});
         if (g + 3 < a.groups) step(g + 3, std::integral_constant<int, 3>{});
+        if (g + 4 < a.groups) step(g + 4, std::integral_constant<int, 4>{});
+        if (g + 5 < a.groups) step(g + 5, std::integral_constant<int, 5>{});
+        if (g + 6 < a.groups) step(g + 6, std::integral_constant<int, 6>{});
+        if (g + 7 < a.groups) step(g + 7, std::integral_constant<int, 7>{});
     }
 
 #pragma unroll
@@ -266,7 +294,7 @@ __global__ __launch_bounds__(256) void block_prefill_kernel(PrefillArgs a) {
     }
 }
 
-template <int FMT, int S, int NB, int MT, int NT>
+template <int FMT, int S, int NB, int MT, int NT, int D>
 hipError_t launch_one(const BlockMatmul& p) {
     PrefillArgs a{p.q, p.xs, p.w0, p.w1, p.out, (int)p.m, (int)p.n, (int)p.k, (int)(p.k / 128), (int)((p.k + 1023) / 1024),
                   (int)((p.n + 15) / 16), 0, 0, p.act, p.out_dtype};
@@ -274,21 +302,28 @@ hipError_t launch_one(const BlockMatmul& p) {
     a.mblk = (int)((p.m + 16 * MT - 1) / (16 * MT));
     const int64_t grid = a.nblk >= 8 ? (int64_t)8 * ((a.nblk + 7) / 8) * a.mblk : (int64_t)a.nblk * a.mblk;
     clear_stale_error();
-    hipLaunchKernelGGL((block_prefill_kernel<FMT, S, NB, MT, NT>), dim3((unsigned)grid), dim3(256), 0, p.stream, a);
+    hipLaunchKernelGGL((block_prefill_kernel<FMT, S, NB, MT, NT, D>), dim3((unsigned)grid), dim3(256), 0, p.stream, a);
     return hipGetLastError();
 }
 
-// Two 16-row tiles per wave (gated: one of each matrix).  64 rows per
-// workgroup while that gives three workgroups a CU, else 32: FFN up gated
-// m = 1024 / 256 / 64, 328 / 98 / 46 us against 381 / 94 / 41; gate (n = 6144)
-// m = 512, 35.5 against 33.3.  Four tiles per wave or 128 rows measured no
-// faster (two waves per SIMD): 327 and 341 us at m = 1024.
+// Tile choice by the number of workgroups, against the 256 CUs.
+//  * Up to three 32-row workgroups a CU: what counts is a group's latency, so
+//    loads run four groups ahead, and plain products take one 16-row weight
+//    tile per wave.  (K = 5120, N = 6144: m = 64 15.8 us against 28.4 with
+//    loads one group ahead and two tiles a wave; FFN down, m = 256 56 / 89;
+//    FFN up gated, m = 64 41.2 / 42.5.)  Above that, fewer registers are
+//    better: gated m = 96 46 us against 53, N = 6144 m = 512 32.9 against 36.4.
+//  * From three 64-row workgroups a CU on, 64 rows (FFN up gated m = 1024, 335
+//    against 384 us; 4-bit 155 / 169), except with smaller weight groups, whose
+//    64-row kernels hold two waves per SIMD (wgroup 64: 223 against 200).
+// Four tiles per wave or 128 rows measured no faster (327 and 341 us).
 template <int FMT, int S, int NB>
 hipError_t launch_variant(const BlockMatmul& p) {
     constexpr int NT = 2 / NB;
-    const int64_t wgs = ((p.n + 127) / 128 * NB) * ((p.m + 63) / 64);
-    if (wgs >= 768) return launch_one<FMT, S, NB, 4, NT>(p);
-    return launch_one<FMT, S, NB, 2, NT>(p);
+    const int64_t cols = (p.n + 64 * NT - 1) / (64 * NT);
+    if (((p.n + 63) / 64) * ((p.m + 31) / 32) <= 768) return launch_one<FMT, S, NB, 2, 1, 4>(p);
+    if (S == 1 && cols * ((p.m + 63) / 64) >= 768) return launch_one<FMT, S, NB, S == 1 ? 4 : 2, NT, 1>(p);
+    return launch_one<FMT, S, NB, 2, NT, 1>(p);
 }
 
 }  // namespace

@@ -31,12 +31,13 @@
 // k while its first weights are on their way, with the exact in-kernel
 // quantiser, so the codes are those of pq2_quantize_act_i8.
 // Up to sixteen columns (MC 16): A row = column, held in registers in operand
-// order (read again per segment where a wave has several); a lane owns four
-// outputs.
+// order (a wave's second segment in LDS; read again per segment where those
+// are more, or do not fit); a lane owns four outputs.
 #include "block_internal.h"
 #include "small_m_common.h"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace pq2 {
 
@@ -64,14 +65,23 @@ constexpr int kW4Waves = 12;
 constexpr int kRing = 4;
 
 constexpr int kColPitch = 1024 + 64;  // four columns' reads fall in distinct banks
+constexpr int kRowPitch = 1024 + 16;  // sixteen columns' reads fall in distinct banks
+constexpr int kLdsBytes = 160 * 1024;
+
+// Where the activations of up to sixteen columns sit: in registers (a wave
+// with one segment), read again per segment, or the first segment in
+// registers and the second in LDS (waves with up to two).
+enum : int { kARegisters = 0, kAStream = 1, kABoth = 2 };
+
 // LDS per wave and segment: the `cols` columns' codes and scales (MC 4), or
 // the scales alone, [group][column].
 __host__ __device__ constexpr int seg_lds(int mc, int cols) { return mc == 4 ? cols * (kColPitch + 32) : 512; }
 
-template <int FMT, int S, int NB, int MC, int SRC, bool MULTI, int MAXW>
+template <int FMT, int S, int NB, int MC, int SRC, int AMODE, int MAXW>
 __global__ __launch_bounds__(64 * MAXW) void block_small_m_kernel(SmallArgs a) {
 #pragma clang fp contract(off)
     constexpr bool WIDE = MC == 16;
+    constexpr bool STREAM = WIDE && AMODE == kAStream, BOTH = WIDE && AMODE == kABoth;
     constexpr bool FUSED = src_fused(SRC);
     constexpr int XL = src_xloads(SRC);
     static_assert(!(WIDE && FUSED), "unquantised activations: up to four columns");
@@ -104,9 +114,11 @@ __global__ __launch_bounds__(64 * MAXW) void block_small_m_kernel(SmallArgs a) {
     // Per wave: its segments' activations; then two sets of slice sums.
     unsigned char* region = smem + (size_t)wave * a.per_wave * seg_bytes;
     float* parts = reinterpret_cast<float*>(smem + (size_t)nwaves * a.per_wave * seg_bytes);
+    // BOTH: the second segment's activations of the waves that have one.
+    unsigned char* a_lds = reinterpret_cast<unsigned char*>(parts + 2 * a.part) + (size_t)wave * a.cols * kRowPitch;
 
     // Loads of one unit (tile, segment); past the last tile they read nothing.
-    uint4 cw[NB][RL], sc[NB][S], sn[NB][S], av[WIDE ? (MULTI ? 2 * RG : 16) : 1];
+    uint4 cw[NB][RL], sc[NB][S], sn[NB][S == 1 ? 1 : S], av[WIDE ? (STREAM ? 2 * RG : 16) : 1];
     // Codes at `codes` + a scalar offset, scales at `scales`; both are past any
     // range where there is no such tile.
     struct Unit {
@@ -135,7 +147,7 @@ __global__ __launch_bounds__(64 * MAXW) void block_small_m_kernel(SmallArgs a) {
     const uint32_t a_off = j < mcount ? (uint32_t)(j * a.k + 16 * kb) : kBufferOOB;
     auto load_a = [&](int s, int i) {
         const int off = s * 1024 + 64 * i;
-        av[MULTI ? i % (2 * RG) : i] = buf_load16s(q_rs, off < a.k ? a_off : kBufferOOB, off < a.k ? (uint32_t)off : 0u);
+        av[STREAM ? i % (2 * RG) : i] = buf_load16s(q_rs, off < a.k ? a_off : kBufferOOB, off < a.k ? (uint32_t)off : 0u);
     };
 
     // 1. Stage the wave's activations.  The loads of the first PRE segments go
@@ -203,8 +215,10 @@ __global__ __launch_bounds__(64 * MAXW) void block_small_m_kernel(SmallArgs a) {
             if (i == 0 || seg_begin + i < seg_end) stage_load(seg_begin + i, t[i]);
         const Unit u = unit_of(blockIdx.x, seg_begin);
         if constexpr (WIDE) {
+            // (BOTH: the second segment's first, on their way to LDS.)
+            const int s = BOTH ? min(seg_begin + 1, a.s8 - 1) : seg_begin;
 #pragma unroll
-            for (int i = 0; i < (MULTI ? 2 * RG : 16); ++i) load_a(seg_begin, i);
+            for (int i = 0; i < (STREAM ? 2 * RG : 16); ++i) load_a(s, i);
         }
 #pragma unroll
         for (int i = 0; i < S; ++i) load_scales(u, i, sc);
@@ -214,6 +228,15 @@ __global__ __launch_bounds__(64 * MAXW) void block_small_m_kernel(SmallArgs a) {
 #pragma unroll
         for (int i = 0; i < PRE; ++i)
             if (i == 0 || seg_begin + i < seg_end) stage_store(seg_begin + i, t[i]);
+        if constexpr (BOTH) {
+            if (seg_begin + 1 < seg_end) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (j < mcount) *reinterpret_cast<uint4*>(a_lds + j * kRowPitch + 64 * i + 16 * kb) = av[i];
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) load_a(seg_begin, i);
+        }
         for (int s = seg_begin + PRE; s < seg_end; ++s) {
             stage_load(s, t[0]);
             stage_store(s, t[0]);
@@ -235,9 +258,10 @@ __global__ __launch_bounds__(64 * MAXW) void block_small_m_kernel(SmallArgs a) {
 
     float acc[NB][C][R];
     // One unit: group dots and terms; the loads of the next unit go out as this
-    // one's registers become free.  (S = 4: eight groups use four scale
-    // registers in turn, so they stream like the codes; else a second set.)
-    auto body = [&](int tile, int s, int next_tile, int next_s) {
+    // one's registers become free.  (Two or four scale registers a unit are
+    // used in turn and stream like the codes; a single one has a second set.)
+    auto body = [&](int tile, int s, int next_tile, int next_s, auto lds_c) {
+        constexpr bool LDS_A = BOTH && decltype(lds_c)::value;
         const unsigned char* from = region + (s - seg_begin) * seg_bytes;
         const Unit next = unit_of(next_tile, next_s);
         const Unit cur = RG < 8 ? unit_of(tile, s) : next;
@@ -247,18 +271,17 @@ __global__ __launch_bounds__(64 * MAXW) void block_small_m_kernel(SmallArgs a) {
             xv[0] = x[0];
             xv[1] = x[1];
         }
-        if constexpr (S != 4) {
-#pragma unroll
-            for (int i = 0; i < S; ++i) load_scales(next, i, sn);
-        }
+        if constexpr (S == 1) load_scales(next, 0, sn);
         const unsigned char* a_base = from + a_col * kColPitch + 16 * kb;
+        const unsigned char* wide_base = a_lds + (j < mcount ? j : 0) * kRowPitch + 16 * kb;
 #pragma unroll
         for (int g = 0; g < 8; ++g) {
             v4i A[2];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 uint4 v;
-                if constexpr (WIDE) v = av[MULTI ? (2 * g + h) % (2 * RG) : 2 * g + h];
+                if constexpr (LDS_A) v = *reinterpret_cast<const uint4*>(wide_base + 128 * g + 64 * h);
+                else if constexpr (WIDE) v = av[STREAM ? (2 * g + h) % (2 * RG) : 2 * g + h];
                 else v = *reinterpret_cast<const uint4*>(a_base + 128 * g + 64 * h);
                 A[h] = v4i{(int)(v.x & keep[h]), (int)(v.y & keep[h]), (int)(v.z & keep[h]), (int)(v.w & keep[h])};
             }
@@ -319,21 +342,20 @@ __global__ __launch_bounds__(64 * MAXW) void block_small_m_kernel(SmallArgs a) {
                 const int i = g / GPL + RL;
                 load_codes(i < CB ? cur : next, i % CB);
             }
-            if constexpr (S == 4) {
-                if (g % 2 == 1) load_scales(next, g >> 1, sc);
+            if constexpr (S != 1) {
+                constexpr int kPer = 8 / S;  // groups of one scale register
+                if (g % kPer == kPer - 1) load_scales(next, g / kPer, sc);
             }
-            if constexpr (WIDE && MULTI) {
+            if constexpr (STREAM) {
                 const int i = 2 * (g + RG);
                 load_a(i < 16 ? s : next_s, i % 16);
                 load_a(i < 16 ? s : next_s, i % 16 + 1);
             }
             __builtin_amdgcn_sched_barrier(0);
         }
-        if constexpr (S != 4) {
+        if constexpr (S == 1) {
 #pragma unroll
-            for (int b = 0; b < NB; ++b)
-#pragma unroll
-                for (int i = 0; i < S; ++i) sc[b][i] = sn[b][i];
+            for (int b = 0; b < NB; ++b) sc[b][0] = sn[b][0];
         }
     };
 
@@ -349,7 +371,12 @@ __global__ __launch_bounds__(64 * MAXW) void block_small_m_kernel(SmallArgs a) {
         for (int s = seg_begin; s < seg_end; ++s) {
             const bool last = s + 1 == seg_end;
             const int nt = last ? tile + (int)gridDim.x : tile, ns = last ? seg_begin : s + 1;
-            body(tile, s, nt, ns);
+            if constexpr (BOTH) {
+                if (s == seg_begin) body(tile, s, nt, ns, std::false_type{});
+                else body(tile, s, nt, ns, std::true_type{});
+            } else {
+                body(tile, s, nt, ns, std::false_type{});
+            }
         }
         float* part = parts + turn * a.part;
 #pragma unroll
@@ -387,11 +414,18 @@ __global__ __launch_bounds__(64 * MAXW) void block_small_m_kernel(SmallArgs a) {
     }
 }
 
-template <int FMT, int S, int NB, int MC, int SRC, bool MULTI, int MAXW>
+// LDS of a launch; `second`: waves whose second segment's activations it holds.
+template <int NB, int MC>
+size_t lds_bytes(const SmallArgs& a, int waves, int second) {
+    return (size_t)waves * a.per_wave * seg_lds(MC, a.cols) + (size_t)2 * waves * NB * a.cols * 64 +
+           (size_t)second * a.cols * kRowPitch;
+}
+
+template <int FMT, int S, int NB, int MC, int SRC, int AMODE, int MAXW>
 hipError_t launch_one(const BlockMatmul& p, SmallArgs a, int waves) {
     constexpr int RG = kRing, GPL = FMT == kFmtTernary ? 2 : 1;
     a.part = waves * NB * a.cols * 16;
-    const size_t lds = (size_t)waves * a.per_wave * seg_lds(MC, a.cols) + (size_t)2 * a.part * 4;
+    const size_t lds = lds_bytes<NB, MC>(a, waves, AMODE == kABoth ? a.s8 - waves : 0);
     const int passes = (int)((p.m + a.cols - 1) / a.cols);
     // Persistent workgroups.  The stream is fastest with about 64 KB in flight
     // per CU, and more only slows it (FFN up, one column: 4-bit weights 10.7 /
@@ -403,7 +437,7 @@ hipError_t launch_one(const BlockMatmul& p, SmallArgs a, int waves) {
     const int per_cu = std::max(1, (MC == 16 ? 8 : 64 / kWaveKB) / waves);
     const dim3 grid((unsigned)std::min(a.tiles, 256 * per_cu), (unsigned)passes);
     clear_stale_error();
-    hipLaunchKernelGGL((block_small_m_kernel<FMT, S, NB, MC, SRC, MULTI, MAXW>), grid, dim3(64 * waves), lds, p.stream,
+    hipLaunchKernelGGL((block_small_m_kernel<FMT, S, NB, MC, SRC, AMODE, MAXW>), grid, dim3(64 * waves), lds, p.stream,
                        a);
     return hipGetLastError();
 }
@@ -417,24 +451,38 @@ hipError_t launch_cols(const BlockMatmul& p) {
     const int waves = (a.s8 + a.per_wave - 1) / a.per_wave;
     if (p.m > 4) {
         a.cols = (int)std::min<int64_t>(p.m, 16);
-        if (a.per_wave > 1) return launch_one<FMT, S, NB, 16, kSrcNatural, true, kMany>(p, a, waves);
-        if (waves > 8) return launch_one<FMT, S, NB, 16, kSrcNatural, false, kMany>(p, a, waves);
-        return launch_one<FMT, S, NB, 16, kSrcNatural, false, 8>(p, a, waves);
+        if constexpr (NB == 1 && S <= 2) {
+            // K = 17408, N = 5120, m = 16: 18.9 against 23.7 us streamed; with
+            // four scales a group, or two matrices, the registers spill.
+            if (a.per_wave == 2 && lds_bytes<NB, 16>(a, waves, a.s8 - waves) <= kLdsBytes)
+                return launch_one<FMT, S, NB, 16, kSrcNatural, kABoth, kMany>(p, a, waves);
+        }
+        if (a.per_wave > 1) return launch_one<FMT, S, NB, 16, kSrcNatural, kAStream, kMany>(p, a, waves);
+        if (waves > 8) return launch_one<FMT, S, NB, 16, kSrcNatural, kARegisters, kMany>(p, a, waves);
+        return launch_one<FMT, S, NB, 16, kSrcNatural, kARegisters, 8>(p, a, waves);
     }
     // LDS holds all of k for the columns of a pass: two at most beyond 32768.
     a.cols = (int)(p.k > 32768 ? std::min<int64_t>(p.m, 2) : p.m);
     switch (p.src) {
-        case kSrcNatural: return launch_one<FMT, S, NB, 4, kSrcNatural, true, kMany>(p, a, waves);
-        case kSrcBf16: return launch_one<FMT, S, NB, 4, kSrcBf16, true, kMany>(p, a, waves);
-        case kSrcF16: return launch_one<FMT, S, NB, 4, kSrcF16, true, kMany>(p, a, waves);
-        case kSrcF32: return launch_one<FMT, S, NB, 4, kSrcF32, true, kMany>(p, a, waves);
+        case kSrcNatural: return launch_one<FMT, S, NB, 4, kSrcNatural, kARegisters, kMany>(p, a, waves);
+        case kSrcBf16: return launch_one<FMT, S, NB, 4, kSrcBf16, kARegisters, kMany>(p, a, waves);
+        case kSrcF16: return launch_one<FMT, S, NB, 4, kSrcF16, kARegisters, kMany>(p, a, waves);
+        case kSrcF32: return launch_one<FMT, S, NB, 4, kSrcF32, kARegisters, kMany>(p, a, waves);
         default: return hipErrorInvalidValue;
     }
 }
 
 }  // namespace
 
-bool block_takes_small_m(const BlockMatmul& p) { return p.m <= 16; }
+// Passes of sixteen columns read the weights again, from the Infinity Cache.
+// Two passes, or all passes in one workgroup a CU, are faster than the prefill
+// engine: N = 6144, K = 5120 m = 17 / 37 / 64 9.3 / 14.1 / 22.7 us against 15.5
+// / 15.5 / 15.8, FFN down m = 17 / 64 29 / 63 against 50 / 50, N = 1000, K =
+// 1152 gated m = 64 / 128 6.4 / 9.9 against 10.9 / 12.0.
+bool block_takes_small_m(const BlockMatmul& p) {
+    const int64_t passes = (p.m + 15) / 16, tiles = (p.n + 15) / 16;
+    return passes <= 2 || passes * tiles <= 256;
+}
 
 // Quantising in the product's launch saves the quantiser's (about 2 us on the
 // GPU, 3 on the host) and costs what the extra columns take to quantise in
@@ -442,7 +490,9 @@ bool block_takes_small_m(const BlockMatmul& p) { return p.m <= 16; }
 // m = 1 / 2 / 3 / 4 6.7 / 7.5 / 8.5 / 9.5 against 8.8 / 8.9 / 9.2 / 9.3 us, FFN
 // up gated ternary 12.1 / 12.4 / 13.4 / 15.0 against 13.8 / 14.0 / 14.2 / 14.5,
 // gated 4-bit at m = 4 18.6 against 19.5.
-bool block_takes_x(int64_t m) { return m <= 4; }
+// A wave's second segment of k is quantised behind the first: FFN down 4-bit at
+// m = 2 / 4 12.5 / 16.3 against 13.5 / 16.0, from FP32 18.7 against 14.8.
+bool block_takes_x(int64_t m, int64_t k) { return m * ((k + 1024 * kW4Waves - 1) / (1024 * kW4Waves)) <= 4; }
 
 hipError_t launch_block_small_m(const BlockMatmul& p) {
     const bool gated = p.act >= 0;
