@@ -68,10 +68,11 @@ constexpr int kColPitch = 1024 + 64;  // four columns' reads fall in distinct ba
 constexpr int kRowPitch = 1024 + 16;  // sixteen columns' reads fall in distinct banks
 constexpr int kLdsBytes = 160 * 1024;
 
-// Where the activations of up to sixteen columns sit: in registers (a wave
-// with one segment), read again per segment, or the first segment in
-// registers and the second in LDS (waves with up to two).
-enum : int { kARegisters = 0, kAStream = 1, kABoth = 2 };
+// Where the activations of up to sixteen columns sit: in LDS, whole; where
+// they do not fit there, in registers in operand order (a wave with one
+// segment), the first segment in registers and the second in LDS (waves with
+// two), or read again per segment.
+enum : int { kALds = 0, kARegisters = 1, kABoth = 2, kAStream = 3 };
 
 // LDS per wave and segment: the `cols` columns' codes and scales (MC 4), or
 // the scales alone, [group][column].
@@ -81,7 +82,8 @@ template <int FMT, int S, int NB, int MC, int SRC, int AMODE, int MAXW>
 __global__ __launch_bounds__(64 * MAXW) void block_small_m_kernel(SmallArgs a) {
 #pragma clang fp contract(off)
     constexpr bool WIDE = MC == 16;
-    constexpr bool STREAM = WIDE && AMODE == kAStream, BOTH = WIDE && AMODE == kABoth;
+    constexpr bool STREAM = WIDE && AMODE == kAStream, BOTH = WIDE && AMODE == kABoth,
+                   ALDS = WIDE && AMODE == kALds;
     constexpr bool FUSED = src_fused(SRC);
     constexpr int XL = src_xloads(SRC);
     static_assert(!(WIDE && FUSED), "unquantised activations: up to four columns");
@@ -114,11 +116,13 @@ __global__ __launch_bounds__(64 * MAXW) void block_small_m_kernel(SmallArgs a) {
     // Per wave: its segments' activations; then two sets of slice sums.
     unsigned char* region = smem + (size_t)wave * a.per_wave * seg_bytes;
     float* parts = reinterpret_cast<float*>(smem + (size_t)nwaves * a.per_wave * seg_bytes);
-    // BOTH: the second segment's activations of the waves that have one.
-    unsigned char* a_lds = reinterpret_cast<unsigned char*>(parts + 2 * a.part) + (size_t)wave * a.cols * kRowPitch;
+    // ALDS: the wave's activations; BOTH: its second segment's, if it has one.
+    const int a_seg = a.cols * kRowPitch;
+    unsigned char* a_lds = reinterpret_cast<unsigned char*>(parts + 2 * a.part) +
+                           (size_t)(ALDS ? seg_begin : wave) * a_seg;
 
     // Loads of one unit (tile, segment); past the last tile they read nothing.
-    uint4 cw[NB][RL], sc[NB][S], sn[NB][S == 1 ? 1 : S], av[WIDE ? (STREAM ? 2 * RG : 16) : 1];
+    uint4 cw[NB][RL], sc[NB][S], sn[NB][S == 1 ? 1 : S], av[WIDE && !ALDS ? (STREAM ? 2 * RG : 16) : 1];
     // Codes at `codes` + a scalar offset, scales at `scales`; both are past any
     // range where there is no such tile.
     struct Unit {
@@ -155,7 +159,7 @@ __global__ __launch_bounds__(64 * MAXW) void block_small_m_kernel(SmallArgs a) {
     //    the weight stream starts at once.
     constexpr int PRE = !WIDE && !FUSED ? 2 : 1;
     struct Staged {
-        uint4 v[WIDE ? 1 : MC][FUSED ? XL : 1];
+        uint4 v[WIDE && !ALDS ? 1 : MC][FUSED ? XL : 1];
         uint2 x;
     };
     auto stage_load = [&](int s, Staged& t) {
@@ -165,6 +169,11 @@ __global__ __launch_bounds__(64 * MAXW) void block_small_m_kernel(SmallArgs a) {
             // Lane (column j, groups 2 kb and 2 kb + 1).
             const bool ok = j < mcount && g0 + 2 * kb < a.groups;
             t.x = buf_load8(xs_rs, ok ? (uint32_t)((j * a.groups + g0 + 2 * kb) * 4) : kBufferOOB);
+            if constexpr (ALDS) {
+#pragma unroll
+                for (int i = 0; i < MC; ++i)
+                    if (i < mcount) t.v[i][0] = buf_load16(q_rs, off < a.k ? (uint32_t)(i * a.k + off) : kBufferOOB);
+            }
         } else if constexpr (FUSED) {
 #pragma unroll
             for (int i = 0; i < MC; ++i) {
@@ -188,6 +197,12 @@ __global__ __launch_bounds__(64 * MAXW) void block_small_m_kernel(SmallArgs a) {
         if constexpr (WIDE) {
             xl[(2 * kb) * 16 + j] = __uint_as_float(t.x.x);
             xl[(2 * kb + 1) * 16 + j] = 8 * s + 2 * kb + 1 < a.groups ? __uint_as_float(t.x.y) : 0.0f;
+            if constexpr (ALDS) {
+#pragma unroll
+                for (int i = 0; i < MC; ++i)
+                    if (i < mcount)
+                        *reinterpret_cast<uint4*>(a_lds + (s - seg_begin) * a_seg + i * kRowPitch + 16 * lane) = t.v[i][0];
+            }
         } else {
 #pragma unroll
             for (int i = 0; i < MC; ++i) {
@@ -214,7 +229,7 @@ __global__ __launch_bounds__(64 * MAXW) void block_small_m_kernel(SmallArgs a) {
         for (int i = 0; i < PRE; ++i)
             if (i == 0 || seg_begin + i < seg_end) stage_load(seg_begin + i, t[i]);
         const Unit u = unit_of(blockIdx.x, seg_begin);
-        if constexpr (WIDE) {
+        if constexpr (WIDE && !ALDS) {
             // (BOTH: the second segment's first, on their way to LDS.)
             const int s = BOTH ? min(seg_begin + 1, a.s8 - 1) : seg_begin;
 #pragma unroll
@@ -261,7 +276,7 @@ __global__ __launch_bounds__(64 * MAXW) void block_small_m_kernel(SmallArgs a) {
     // one's registers become free.  (Two or four scale registers a unit are
     // used in turn and stream like the codes; a single one has a second set.)
     auto body = [&](int tile, int s, int next_tile, int next_s, auto lds_c) {
-        constexpr bool LDS_A = BOTH && decltype(lds_c)::value;
+        constexpr bool LDS_A = ALDS || (BOTH && decltype(lds_c)::value);
         const unsigned char* from = region + (s - seg_begin) * seg_bytes;
         const Unit next = unit_of(next_tile, next_s);
         const Unit cur = RG < 8 ? unit_of(tile, s) : next;
@@ -273,7 +288,8 @@ __global__ __launch_bounds__(64 * MAXW) void block_small_m_kernel(SmallArgs a) {
         }
         if constexpr (S == 1) load_scales(next, 0, sn);
         const unsigned char* a_base = from + a_col * kColPitch + 16 * kb;
-        const unsigned char* wide_base = a_lds + (j < mcount ? j : 0) * kRowPitch + 16 * kb;
+        const unsigned char* wide_base = a_lds + (ALDS ? (s - seg_begin) * a_seg : 0) +
+                                         (j < mcount ? j : 0) * kRowPitch + 16 * kb;
 #pragma unroll
         for (int g = 0; g < 8; ++g) {
             v4i A[2];
@@ -414,27 +430,28 @@ __global__ __launch_bounds__(64 * MAXW) void block_small_m_kernel(SmallArgs a) {
     }
 }
 
-// LDS of a launch; `second`: waves whose second segment's activations it holds.
-template <int NB, int MC>
-size_t lds_bytes(const SmallArgs& a, int waves, int second) {
+// LDS of a launch.
+template <int NB, int MC, int AMODE>
+size_t lds_bytes(const SmallArgs& a, int waves) {
+    const int held = MC == 4 ? 0 : AMODE == kALds ? a.s8 : AMODE == kABoth ? a.s8 - waves : 0;
     return (size_t)waves * a.per_wave * seg_lds(MC, a.cols) + (size_t)2 * waves * NB * a.cols * 64 +
-           (size_t)second * a.cols * kRowPitch;
+           (size_t)held * a.cols * kRowPitch;
 }
 
 template <int FMT, int S, int NB, int MC, int SRC, int AMODE, int MAXW>
 hipError_t launch_one(const BlockMatmul& p, SmallArgs a, int waves) {
     constexpr int RG = kRing, GPL = FMT == kFmtTernary ? 2 : 1;
     a.part = waves * NB * a.cols * 16;
-    const size_t lds = lds_bytes<NB, MC>(a, waves, AMODE == kABoth ? a.s8 - waves : 0);
+    const size_t lds = lds_bytes<NB, MC, AMODE>(a, waves);
     const int passes = (int)((p.m + a.cols - 1) / a.cols);
     // Persistent workgroups.  The stream is fastest with about 64 KB in flight
     // per CU, and more only slows it (FFN up, one column: 4-bit weights 10.7 /
     // 9.6 / 9.7 / 9.7 us at one / two / three / four workgroups of five waves a
-    // CU; gated ternary 15.4 / 12.4 / 12.1 / 12.6).  With the activations of
-    // sixteen columns to load first, one workgroup of five waves is best
-    // (gated, m = 8: 19.2 / 20.9 / 23.2 us at one / two / three).
+    // CU; gated ternary 15.4 / 12.4 / 12.1 / 12.6).  Wide kernels have more to
+    // load first: gated 4-bit m = 8 18.0 / 17.5 / 19.7 us at one / two / three,
+    // m = 16 18.9 / 20.4 / 22.7.
     constexpr int kWaveKB = RG / GPL * NB;
-    const int per_cu = std::max(1, (MC == 16 ? 8 : 64 / kWaveKB) / waves);
+    const int per_cu = std::max(1, (MC == 16 ? (a.cols > 8 ? 8 : 12) : 64 / kWaveKB) / waves);
     const dim3 grid((unsigned)std::min(a.tiles, 256 * per_cu), (unsigned)passes);
     clear_stale_error();
     hipLaunchKernelGGL((block_small_m_kernel<FMT, S, NB, MC, SRC, AMODE, MAXW>), grid, dim3(64 * waves), lds, p.stream,
@@ -451,23 +468,26 @@ hipError_t launch_cols(const BlockMatmul& p) {
     const int waves = (a.s8 + a.per_wave - 1) / a.per_wave;
     if (p.m > 4) {
         a.cols = (int)std::min<int64_t>(p.m, 16);
+        if (lds_bytes<NB, 16, kALds>(a, waves) <= kLdsBytes) {
+            if (waves <= 8) return launch_one<FMT, S, NB, 16, kSrcNatural, kALds, 8>(p, a, waves);
+            return launch_one<FMT, S, NB, 16, kSrcNatural, kALds, kMany>(p, a, waves);
+        }
         if constexpr (NB == 1 && S <= 2) {
             // K = 17408, N = 5120, m = 16: 18.9 against 23.7 us streamed; with
             // four scales a group, or two matrices, the registers spill.
-            if (a.per_wave == 2 && lds_bytes<NB, 16>(a, waves, a.s8 - waves) <= kLdsBytes)
+            if (a.per_wave == 2 && lds_bytes<NB, 16, kABoth>(a, waves) <= kLdsBytes)
                 return launch_one<FMT, S, NB, 16, kSrcNatural, kABoth, kMany>(p, a, waves);
         }
         if (a.per_wave > 1) return launch_one<FMT, S, NB, 16, kSrcNatural, kAStream, kMany>(p, a, waves);
-        if (waves > 8) return launch_one<FMT, S, NB, 16, kSrcNatural, kARegisters, kMany>(p, a, waves);
-        return launch_one<FMT, S, NB, 16, kSrcNatural, kARegisters, 8>(p, a, waves);
+        return launch_one<FMT, S, NB, 16, kSrcNatural, kARegisters, kMany>(p, a, waves);
     }
     // LDS holds all of k for the columns of a pass: two at most beyond 32768.
     a.cols = (int)(p.k > 32768 ? std::min<int64_t>(p.m, 2) : p.m);
     switch (p.src) {
-        case kSrcNatural: return launch_one<FMT, S, NB, 4, kSrcNatural, kARegisters, kMany>(p, a, waves);
-        case kSrcBf16: return launch_one<FMT, S, NB, 4, kSrcBf16, kARegisters, kMany>(p, a, waves);
-        case kSrcF16: return launch_one<FMT, S, NB, 4, kSrcF16, kARegisters, kMany>(p, a, waves);
-        case kSrcF32: return launch_one<FMT, S, NB, 4, kSrcF32, kARegisters, kMany>(p, a, waves);
+        case kSrcNatural: return launch_one<FMT, S, NB, 4, kSrcNatural, kALds, kMany>(p, a, waves);
+        case kSrcBf16: return launch_one<FMT, S, NB, 4, kSrcBf16, kALds, kMany>(p, a, waves);
+        case kSrcF16: return launch_one<FMT, S, NB, 4, kSrcF16, kALds, kMany>(p, a, waves);
+        case kSrcF32: return launch_one<FMT, S, NB, 4, kSrcF32, kALds, kMany>(p, a, waves);
         default: return hipErrorInvalidValue;
     }
 }
