@@ -313,16 +313,22 @@ hipError_t launch_one(const BlockMatmul& p) {
 //    loads one group ahead and two tiles a wave; FFN down, m = 256 56 / 89;
 //    FFN up gated, m = 64 41.2 / 42.5.)  Above that, fewer registers are
 //    better: gated m = 96 46 us against 53, N = 6144 m = 512 32.9 against 36.4.
-//  * From three 64-row workgroups a CU on, 64 rows (FFN up gated m = 1024, 335
-//    against 384 us; 4-bit 155 / 169), except with smaller weight groups, whose
-//    64-row kernels hold two waves per SIMD (wgroup 64: 223 against 200).
+//  * From two 64-row workgroups a CU on, 64 rows (FFN up gated m = 1024, 335
+//    against 384 us; 4-bit m = 1024 / 256 153 / 49.7 against 169 / 56.0; N =
+//    6144, m = 512, one and a half a CU, 41.0 against 32.9), except with
+//    smaller weight groups, whose 64-row kernels hold two waves per SIMD
+//    (wgroup 64: 223 against 200).  The 4-bit kernels have the registers to
+//    load two groups ahead (gated m = 1024 294 against 302 us); the ternary one
+//    would drop to two waves per SIMD (382 against 330).
 // Four tiles per wave or 128 rows measured no faster (327 and 341 us).
 template <int FMT, int S, int NB>
 hipError_t launch_variant(const BlockMatmul& p) {
     constexpr int NT = 2 / NB;
     const int64_t cols = (p.n + 64 * NT - 1) / (64 * NT);
     if (((p.n + 63) / 64) * ((p.m + 31) / 32) <= 768) return launch_one<FMT, S, NB, 2, 1, 4>(p);
-    if (S == 1 && cols * ((p.m + 63) / 64) >= 768) return launch_one<FMT, S, NB, S == 1 ? 4 : 2, NT, 1>(p);
+    if constexpr (S == 1) {
+        if (cols * ((p.m + 63) / 64) >= 512) return launch_one<FMT, S, NB, 4, NT, FMT == kFmtW4 ? 2 : 1>(p);
+    }
     return launch_one<FMT, S, NB, 2, NT, 1>(p);
 }
 
