@@ -307,9 +307,10 @@ hipError_t launch_one(const BlockMatmul& p) {
 }
 
 // Tile choice by the number of workgroups, against the 256 CUs.
-//  * Up to three 32-row workgroups a CU: what counts is a group's latency, so
-//    loads run four groups ahead, and plain products take one 16-row weight
-//    tile per wave.  (K = 5120, N = 6144: m = 64 15.8 us against 28.4 with
+//  * While all 32-row workgroups are resident at once (four a CU; gated, which
+//    needs more registers, three or two): what counts is a group's latency,
+//    so loads run four groups ahead, and plain products take one 16-row
+//    weight tile per wave.  (K = 5120, N = 6144: m = 64 15.8 us against 28.4 with
 //    loads one group ahead and two tiles a wave; FFN down, m = 256 56 / 89;
 //    FFN up gated, m = 64 41.2 / 42.5.)  Above that, fewer registers are
 //    better: gated m = 96 46 us against 53, N = 6144 m = 512 32.9 against 36.4.
@@ -325,7 +326,8 @@ template <int FMT, int S, int NB>
 hipError_t launch_variant(const BlockMatmul& p) {
     constexpr int NT = 2 / NB;
     const int64_t cols = (p.n + 64 * NT - 1) / (64 * NT);
-    if (((p.n + 63) / 64) * ((p.m + 31) / 32) <= 768) return launch_one<FMT, S, NB, 2, 1, 4>(p);
+    constexpr int kResident = 256 * (NB == 1 ? 4 : S == 4 ? 2 : 3);
+    if (((p.n + 63) / 64) * ((p.m + 31) / 32) <= kResident) return launch_one<FMT, S, NB, 2, 1, 4>(p);
     if constexpr (S == 1) {
         if (cols * ((p.m + 63) / 64) >= 512) return launch_one<FMT, S, NB, 4, NT, FMT == kFmtW4 ? 2 : 1>(p);
     }
