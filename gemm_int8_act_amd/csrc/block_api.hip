@@ -11,6 +11,7 @@
 namespace {
 
 constexpr int64_t kMaxN = (int64_t)1 << 30;
+constexpr double kMinEps = 1e-70;
 
 bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p % a) == 0; }
 
@@ -171,7 +172,8 @@ int pq2_block_norm(const pq2_block_norm_args* a, void* stream) {
         (a->block && !dtype_ok(a->block_dtype)))
         return PQ2_EINVAL;
     if (a->q && !group_ok(a->agroup)) return PQ2_EINVAL;
-    if (!(a->eps > 0) || !isfinite(a->eps) || !isfinite(a->alpha)) return PQ2_EINVAL;
+    // (Below kMinEps a zero row's rstd would not be a finite float.)
+    if (!(a->eps >= kMinEps) || !isfinite(a->eps) || !isfinite(a->alpha)) return PQ2_EINVAL;
     if (a->unit_offset != 0 && a->unit_offset != 1) return PQ2_EINVAL;
     const int64_t m = a->m, k = a->k;
     if (m < 1 || m > INT32_MAX || !k_ok(k)) return PQ2_ESHAPE;

@@ -301,6 +301,7 @@ hipError_t launch_one(const BlockMatmul& p) {
     a.nblk = (a.tiles + 4 * NT - 1) / (4 * NT);
     a.mblk = (int)((p.m + 16 * MT - 1) / (16 * MT));
     const int64_t grid = a.nblk >= 8 ? (int64_t)8 * ((a.nblk + 7) / 8) * a.mblk : (int64_t)a.nblk * a.mblk;
+    if (grid > INT32_MAX) return hipErrorInvalidValue;
     clear_stale_error();
     hipLaunchKernelGGL((block_prefill_kernel<FMT, S, NB, MT, NT, D>), dim3((unsigned)grid), dim3(256), 0, p.stream, a);
     return hipGetLastError();

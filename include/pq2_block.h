@@ -157,7 +157,7 @@ typedef struct pq2_block_norm_args {
     float* xs;                /* float [m][k/agroup]                                        */
     int64_t m, k;             /* k as pq2_quantize_act_i8                                   */
     int64_t agroup;           /* 128, 64 or 32; read with q only                            */
-    double eps;               /* > 0, finite                                                */
+    double eps;               /* >= 1e-70, finite                                           */
     float alpha;              /* residual scale                                             */
     int r_dtype, block_dtype; /* PQ2_BF16 / PQ2_F16 / PQ2_F32                               */
     int w_dtype;              /* of w, post_w and gate                                      */

@@ -162,7 +162,7 @@ def test_block_norm_validation():
     assert f(r_dtype=3) == EINVAL and f(w_dtype=-1) == EINVAL and f(x_dtype=9) == EINVAL
     assert f(block=D, block_stride=128, block_dtype=4) == EINVAL
     assert f(q=D, xs=E, agroup=16) == EINVAL
-    for eps in (0.0, -1e-6, float("inf"), float("nan")):
+    for eps in (0.0, -1e-6, 1e-71, float("inf"), float("nan")):
         assert f(eps=eps) == EINVAL
     assert f(alpha=float("nan")) == EINVAL and f(alpha=float("inf")) == EINVAL and f(unit_offset=2) == EINVAL
     assert f(m=0) == ESHAPE and f(m=1 << 31) == ESHAPE and f(k=64) == ESHAPE and f(k=1 << 17) == ESHAPE

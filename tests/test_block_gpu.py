@@ -88,7 +88,11 @@ def test_prepare_w4_byte_exact(n, k, pad, wg):
 # ---------------------------------------------------------------- 4-bit products
 W4_SHAPES = [(1, 1, 128), (1, 200, 512), (2, 17, 384), (3, 33, 1024), (4, 300, 1152), (5, 16, 128), (4, 40, 16384),
              (9, 150, 2176), (16, 64, 5120), (16, 31, 17408), (17, 100, 640), (33, 70, 5120), (64, 128, 1024),
-             (100, 257, 1152), (131, 40, 3200), (1, 24, 65536), (300, 600, 1280)]
+             (100, 257, 1152), (131, 40, 3200), (1, 24, 65536), (300, 600, 1280),
+             # decode: LDS full of activations, several segments a wave, each place the activations of a wide pass sit in
+             (4, 33, 32768), (3, 20, 65536), (8, 40, 17408), (13, 24, 12288), (16, 20, 24576), (7, 18, 65536),
+             # prefill: low-latency, 32-row and 64-row kernels, ragged rows and columns, groups behind the last segment
+             (33, 1400, 384), (257, 300, 1152), (500, 130, 2176), (1000, 1001, 256), (2100, 1100, 384), (2201, 2083, 128)]
 
 
 @pytest.mark.parametrize("wg", [128, 64, 32])
@@ -197,11 +201,11 @@ def test_linear_w4_codes_at_rounding_borders(m, k, dtype):
     assert torch.equal(y.view(torch.int32), z.view(torch.int32))
 
 
-@pytest.mark.parametrize("m", [4, 16, 64])
-def test_w4_a_bad_row_stays_alone(m):
+@pytest.mark.parametrize("m,n", [(4, 40), (16, 40), (64, 40), (60, 1200), (2200, 2100)])
+def test_w4_a_bad_row_stays_alone(m, n):
     """NaN scales in one row of xs reach that row's outputs only (k ends inside a segment)."""
-    announce(f"w4 one bad row m={m}")
-    n, k = 40, 1152
+    announce(f"w4 one bad row m={m} n={n}")
+    k = 1152
     tiles, _, _ = w4(n, k, 128, 2)
     q, xs = quantise(activations(m, k, 3), k)
     y = torch.empty((m, n), device=DEV)
@@ -233,7 +237,7 @@ def ternary_tiles(n, k, seed):
     return tiles, raw
 
 
-GATED_SHAPES = [(1, 1, 128), (1, 200, 1024), (2, 40, 384), (4, 33, 5120), (6, 17, 1152), (16, 100, 2176),
+GATED_SHAPES = [(1500, 1999, 128), (600, 2100, 256), (40, 1500, 1152), (4, 33, 32768), (8, 17, 17408), (1, 1, 128), (1, 200, 1024), (2, 40, 384), (4, 33, 5120), (6, 17, 1152), (16, 100, 2176),
                 (13, 24, 17408), (37, 65, 1152), (70, 130, 640), (129, 300, 1024), (4, 20, 16384)]
 
 
@@ -425,6 +429,13 @@ def test_block_norm_single_outputs():
     assert torch.equal(ro, r1) and torch.equal(xo, x1) and torch.equal(q, q1) and torch.equal(xs, s1)
 
 
+@pytest.mark.parametrize("m,k", [(767, 2048), (768, 2048), (800, 1152), (770, 9216), (769, 128), (9, 33024)])
+def test_block_norm_many_rows(m, k):
+    """Both sides of the workgroup shape's rule, and rows of two to eight chunks a thread."""
+    announce(f"block norm many rows m={m} k={k}")
+    check_norm((m, k, "bf16", "f32", "bf16", "bf16", True, "row", False, 64))
+
+
 def test_block_norm_zero_and_tiny_rows():
     announce("block norm zero and tiny rows")
     pq2 = _pq2()
@@ -499,7 +510,7 @@ class Block:
         assert torch.equal(self.r.cpu(), want_r) and torch.equal(self.x.cpu(), want_x)
 
 
-@pytest.mark.parametrize("m", [1, 4, 16, 70])
+@pytest.mark.parametrize("m", [1, 4, 16, 70, 300])
 def test_block_together(m):
     announce(f"block together m={m}")
     b = Block(m, 640, 1152, 32)
@@ -524,7 +535,7 @@ def test_block_on_another_stream():
     b.check(r)
 
 
-@pytest.mark.parametrize("m", [2, 9, 40])
+@pytest.mark.parametrize("m", [2, 9, 40, 300])
 def test_block_captured_and_replayed(m):
     """Replays with new inputs, eager runs of the same buffers between them."""
     announce(f"block captured m={m}")
