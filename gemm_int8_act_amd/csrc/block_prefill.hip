@@ -109,7 +109,7 @@ __global__ __launch_bounds__(256) void block_prefill_kernel(PrefillArgs a) {
 
     auto load_a = [&](int g, int set) {
 #pragma unroll
-        for (int p = 0; p < AQ; ++p) areg[set][p] = buf_load16(q_rs, q_off[p] + 128u * g);
+        for (int p = 0; p < AQ; ++p) areg[set][p] = buf_load16s(q_rs, q_off[p], 128u * g);
     };
     auto load_xs = [&](int seg) {
 #pragma unroll
@@ -120,19 +120,19 @@ __global__ __launch_bounds__(256) void block_prefill_kernel(PrefillArgs a) {
         }
     };
     auto load_codes = [&](int g, int set) {
-        const uint32_t off = (uint32_t)((g >> 3) * UNIT + (FMT == kFmtTernary ? ((g & 7) >> 1) : (g & 7)) * 1024 + 16 * lane);
+        const uint32_t off = (uint32_t)((g >> 3) * UNIT + (FMT == kFmtTernary ? ((g & 7) >> 1) : (g & 7)) * 1024);
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
-            for (int t = 0; t < NT; ++t) cw[set][b][t] = buf_load16(w_rs[b], off + t_off[t]);
+            for (int t = 0; t < NT; ++t) cw[set][b][t] = buf_load16s(w_rs[b], 16 * lane, off + t_off[t]);
     };
     // The scales of groups g .. g + SG - 1 (g a multiple of SG).
     auto load_scales = [&](int g, int set) {
-        const uint32_t off = (uint32_t)((g >> 3) * UNIT + CODES + 16 * S * j + 16 * ((g & 7) / SG));
+        const uint32_t off = (uint32_t)((g >> 3) * UNIT + CODES + 16 * ((g & 7) / SG));
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
-            for (int t = 0; t < NT; ++t) sc[set][b][t] = buf_load16(w_rs[b], off + t_off[t]);
+            for (int t = 0; t < NT; ++t) sc[set][b][t] = buf_load16s(w_rs[b], 16 * S * j, off + t_off[t]);
     };
     auto store_a = [&](int buf, int set) {
 #pragma unroll
@@ -155,19 +155,24 @@ __global__ __launch_bounds__(256) void block_prefill_kernel(PrefillArgs a) {
             for (int i = 0; i < MT; ++i) acc[b][t][i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
     const int low_half = kb < 2 ? -1 : 0;
 
+    // Loads behind the last group: a branch around them costs copies of every
+    // register they write and ends the scheduler's region, so the kernels of
+    // full grids (D < 4) read the last group again instead.  The latency kernel
+    // (D = 4) has no VALU to spare but a short k to end: it skips them.
+    const int last = a.groups - 1;
+    auto wanted = [&](int g) { return D < 4 || g <= last; };
     load_a(0, 0);
     load_xs(0);
     load_codes(0, 0);
     load_scales(0, 0);
 #pragma unroll
     for (int i = 1; i < D; ++i)
-        if (i < a.groups) {
-            load_a(i, i);
-            if (FMT == kFmtW4 || i % 2 == 0) load_codes(i, FMT == kFmtW4 ? i : i / 2);
+        if (wanted(i)) {
+            load_a(min(i, last), i);
+            if (FMT == kFmtW4 || i % 2 == 0) load_codes(min(i, last), FMT == kFmtW4 ? i : i / 2);
         }
 #pragma unroll
-    for (int i = 1; i < RS; ++i)
-        if (i * SG < a.groups) load_scales(i * SG, i);
+    for (int i = 1; i < RS; ++i) load_scales(min(i * SG, last), i);
     store_a(0, 0);
     store_xs(0);
     __syncthreads();
@@ -179,8 +184,7 @@ __global__ __launch_bounds__(256) void block_prefill_kernel(PrefillArgs a) {
         constexpr int buf = u & 1;
         constexpr int cs = (FMT == kFmtTernary ? u / 2 : u) % DC;   // code set of this group
         constexpr int ss = u / SG % RS;                             // scale set
-        const bool more = g + 1 < a.groups, ahead = g + D < a.groups;
-        if (ahead) load_a(g + D, u % D);
+        if (wanted(g + D)) load_a(min(g + D, last), u % D);
         v4i B[NB][NT][2];
 #pragma unroll
         for (int b = 0; b < NB; ++b)
@@ -192,25 +196,25 @@ __global__ __launch_bounds__(256) void block_prefill_kernel(PrefillArgs a) {
                     else B[b][t][h] = w4_operand(word_of(cw[cs][b][t], 2 * h), word_of(cw[cs][b][t], 2 * h + 1));
                 }
         if constexpr (FMT == kFmtW4) {
-            if (ahead) load_codes(g + D, cs);
+            if (wanted(g + D)) load_codes(min(g + D, last), cs);
         } else if constexpr (u % 2 == 1) {
-            if (g - 1 + 2 * DC < a.groups) load_codes(g - 1 + 2 * DC, cs);
+            if (wanted(g - 1 + 2 * DC)) load_codes(min(g - 1 + 2 * DC, last), cs);
         }
-        // The set before this one is free from its last group on.  (S = 1: a
-        // set lasts the whole unroll, so the next one moves down.)
+        // The scale set before this one is free from its last group on.  (S = 1:
+        // a set lasts the whole unroll, so the next one moves down.)
         if constexpr (S == 1 && u == 0) {
             if (g > 0) {
 #pragma unroll
                 for (int b = 0; b < NB; ++b)
 #pragma unroll
                     for (int t = 0; t < NT; ++t) sc[0][b][t] = sc[1][b][t];
-                if (g + 8 < a.groups) load_scales(g + 8, 1);
             }
+            if (wanted(g + 8)) load_scales(min(g + 8, last), 1);
         } else if constexpr (u % SG == 0) {
-            if (g > 0 && g + (RS - 1) * SG < a.groups) load_scales(g + (RS - 1) * SG, (ss + RS - 1) % RS);
+            if (wanted(g + (RS - 1) * SG)) load_scales(min(g + (RS - 1) * SG, last), (ss + RS - 1) % RS);
         }
         if constexpr (u == 0) {
-            if (g + 8 < a.groups) load_xs((g >> 3) + 1);
+            if (wanted(g + 8)) load_xs((g >> 3) + 1);
         }
         const float* xrow = &Xs[(g >> 3) & 1][g & 7][0];
 #pragma unroll
@@ -257,10 +261,8 @@ __global__ __launch_bounds__(256) void block_prefill_kernel(PrefillArgs a) {
                     }
                 }
         }
-        if (more) store_a(buf ^ 1, (u + 1) % D);
-        if constexpr (u == 7) {
-            if (more) store_xs(((g >> 3) + 1) & 1);
-        }
+        if (wanted(g + 1)) store_a(buf ^ 1, (u + 1) % D);
+        if constexpr (u == 7) store_xs(((g >> 3) + 1) & 1);
         __syncthreads();
     };
     for (int g = 0; g < a.groups; g += 8) {
