@@ -478,8 +478,14 @@ hipError_t launch_cols(const BlockMatmul& p) {
             if (a.per_wave == 2 && lds_bytes<NB, 16, kABoth>(a, waves) <= kLdsBytes)
                 return launch_one<FMT, S, NB, 16, kSrcNatural, kABoth, kMany>(p, a, waves);
         }
-        if (a.per_wave > 1) return launch_one<FMT, S, NB, 16, kSrcNatural, kAStream, kMany>(p, a, waves);
-        return launch_one<FMT, S, NB, 16, kSrcNatural, kARegisters, kMany>(p, a, waves);
+        // K = 10240, N = 8192 gated, m = 16: wgroup 128 in registers 18.9 us,
+        // streamed 24.6; but with four scales a group (67.9 against 30.0) or the
+        // ternary kernel's eight sums and sixteen waves (41.5 against 31.8) the
+        // registers spill.
+        if constexpr (FMT == kFmtW4 && S <= 2) {
+            if (a.per_wave == 1) return launch_one<FMT, S, NB, 16, kSrcNatural, kARegisters, kMany>(p, a, waves);
+        }
+        return launch_one<FMT, S, NB, 16, kSrcNatural, kAStream, kMany>(p, a, waves);
     }
     // LDS holds all of k for the columns of a pass: two at most beyond 32768.
     a.cols = (int)(p.k > 32768 ? std::min<int64_t>(p.m, 2) : p.m);
