@@ -176,7 +176,7 @@ int pq2_block_norm(const pq2_block_norm_args* a, void* stream) {
     if (!(a->eps >= kMinEps) || !isfinite(a->eps) || !isfinite(a->alpha)) return PQ2_EINVAL;
     if (a->unit_offset != 0 && a->unit_offset != 1) return PQ2_EINVAL;
     const int64_t m = a->m, k = a->k;
-    if (m < 1 || m > INT32_MAX || !k_ok(k)) return PQ2_ESHAPE;
+    if (m < 1 || m > PQ2_MAX_BLOCK_M || !k_ok(k)) return PQ2_ESHAPE;
     if (a->r_stride < k || (a->block && a->block_stride < k) || (a->r_out && a->r_out_stride < k) ||
         (a->x_out && a->x_out_stride < k) || (a->gate && a->gate_stride != 0 && a->gate_stride < k))
         return PQ2_ESHAPE;

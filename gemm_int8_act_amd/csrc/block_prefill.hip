@@ -19,6 +19,7 @@
 // matrix core for the group's 128 multiply-adds) bounds the kernel.
 #include "block_internal.h"
 
+#include <algorithm>
 #include <type_traits>
 
 namespace pq2 {
@@ -301,12 +302,25 @@ hipError_t launch_one(const BlockMatmul& p) {
     PrefillArgs a{p.q, p.xs, p.w0, p.w1, p.out, (int)p.m, (int)p.n, (int)p.k, (int)(p.k / 128), (int)((p.k + 1023) / 1024),
                   (int)((p.n + 15) / 16), 0, 0, p.act, p.out_dtype};
     a.nblk = (a.tiles + 4 * NT - 1) / (4 * NT);
-    a.mblk = (int)((p.m + 16 * MT - 1) / (16 * MT));
-    const int64_t grid = a.nblk >= 8 ? (int64_t)8 * ((a.nblk + 7) / 8) * a.mblk : (int64_t)a.nblk * a.mblk;
-    if (grid > INT32_MAX) return hipErrorInvalidValue;
-    clear_stale_error();
-    hipLaunchKernelGGL((block_prefill_kernel<FMT, S, NB, MT, NT, D>), dim3((unsigned)grid), dim3(256), 0, p.stream, a);
-    return hipGetLastError();
+    // A launch holds fewer than 2^32 threads: outputs of some 10^10 elements
+    // take several, each of whole workgroup rows.
+    const int64_t per_row = a.nblk >= 8 ? (int64_t)8 * ((a.nblk + 7) / 8) : a.nblk;
+    const int64_t most = ((int64_t)UINT32_MAX / 256) / per_row * (16 * MT);
+    if (most < 1) return hipErrorInvalidValue;
+    for (int64_t m0 = 0; m0 < p.m; m0 += most) {
+        a.m = (int)std::min(p.m - m0, most);
+        a.mblk = (a.m + 16 * MT - 1) / (16 * MT);
+        a.q = p.q + m0 * p.k;
+        a.xs = p.xs + m0 * (p.k / 128);
+        const int size = NB == 2 && p.out_dtype != 2 ? 2 : 4;
+        a.out = static_cast<unsigned char*>(p.out) + m0 * p.n * size;
+        clear_stale_error();
+        hipLaunchKernelGGL((block_prefill_kernel<FMT, S, NB, MT, NT, D>), dim3((unsigned)(per_row * a.mblk)), dim3(256),
+                           0, p.stream, a);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 // Tile choice by the number of workgroups, against the 256 CUs.

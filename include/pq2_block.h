@@ -23,7 +23,7 @@ extern "C" {
  * SiLU g / (1 + exp(-g)); GELU 0.5 g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))). */
 enum { PQ2_ACT_SILU = 0, PQ2_ACT_GELU_TANH = 1 };
 
-/* Largest m of the matmul entry points below. */
+/* Largest m of the entry points below. */
 #define PQ2_MAX_BLOCK_M (65535 * 16)
 
 /* ---- 4-bit weights.
@@ -167,7 +167,7 @@ typedef struct pq2_block_norm_args {
 
 /* Errors: EINVAL (null args, r or w; no output; q without xs or xs without
  *         q; post_w or gate without block; dtype; agroup; eps; alpha not
- *         finite; unit_offset; overlap), ESHAPE (m < 1 or > 2^31 - 1, k, a
+ *         finite; unit_offset; overlap), ESHAPE (m < 1 or > PQ2_MAX_BLOCK_M, k, a
  *         stride below k), EALIGN (a pointer not aligned to its element, q
  *         not to 8 bytes), ELAUNCH, EDEVICE. */
 int pq2_block_norm(const pq2_block_norm_args* args, void* stream);

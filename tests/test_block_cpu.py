@@ -165,7 +165,7 @@ def test_block_norm_validation():
     for eps in (0.0, -1e-6, 1e-71, float("inf"), float("nan")):
         assert f(eps=eps) == EINVAL
     assert f(alpha=float("nan")) == EINVAL and f(alpha=float("inf")) == EINVAL and f(unit_offset=2) == EINVAL
-    assert f(m=0) == ESHAPE and f(m=1 << 31) == ESHAPE and f(k=64) == ESHAPE and f(k=1 << 17) == ESHAPE
+    assert f(m=0) == ESHAPE and f(m=65535 * 16 + 1) == ESHAPE and f(m=1 << 31) == ESHAPE and f(k=64) == ESHAPE and f(k=1 << 17) == ESHAPE
     assert f(r_stride=127) == ESHAPE and f(r_out_stride=1) == ESHAPE
     assert f(block=D, block_stride=0) == ESHAPE
     assert f(block=D, block_stride=128, gate=E, gate_stride=5) == ESHAPE

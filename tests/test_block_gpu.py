@@ -306,6 +306,27 @@ def test_gated_one_matrix_for_both_and_linear(m):
         assert torch.equal(a, b) and bool(torch.isfinite(a).all())
 
 
+def test_gated_more_rows_than_one_launch_takes():
+    """2^24 workgroups of 256 threads and more: the rows of several launches have the bits of a small call's."""
+    m, n, k, wg = 65535 * 16, 32768, 128, 32
+    part = m // 257
+    if torch.cuda.mem_get_info()[0] < 100e9:
+        pytest.skip("needs 70 GB for the output")
+    announce(f"gated m={m} n={n} k={k} wg={wg}")
+    pq2 = _pq2()
+    w = w4(n, k, wg, 5)[0]
+    q, xs = quantise(activations(part, k, 6), k)
+    want = torch.empty((part, n), dtype=torch.bfloat16, device=DEV)
+    pq2.pq2_gated_matmul_w4(q, xs, w, w, want, wg)
+    h = torch.full((m, n), float("nan"), dtype=torch.bfloat16, device=DEV)
+    pq2.pq2_gated_matmul_w4(q.repeat(257, 1), xs.repeat(257, 1), w, w, h, wg)
+    torch.cuda.synchronize()
+    for i in range(257):
+        assert torch.equal(h[i * part:(i + 1) * part], want), f"rows of part {i}"
+    del h
+    torch.cuda.empty_cache()
+
+
 @pytest.mark.parametrize("act", [0, 1])
 def test_gated_far_ends_of_the_activation(act):
     """Gates far below and above zero: act(g) goes to 0 and g, never NaN."""
