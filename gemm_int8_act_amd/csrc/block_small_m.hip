@@ -2,13 +2,13 @@
 // 4-bit weights and the gated feed-forward product for few columns.
 //
 // A workgroup owns whole tiles of 16 weight rows (gated: the gate tile and
-// the up tile of the same rows), one after the other; its waves split k into
-// consecutive slices of whole 1024-weight segments.  Per segment a wave forms
-// each weight group's exact dot with v_mfma_i32_16x16x64_i8 and adds one FP32
-// term per activation group; the slices are added in index order by the
-// whole workgroup, which also applies the gate's activation, so the two
-// products of a gated call never reach memory.  The order of a column's sum
-// depends on k only.
+// the up tile of the same rows; some plain products: two tiles at a time),
+// one after the other; its waves split k into consecutive slices of whole
+// 1024-weight segments.  Per segment a wave forms each weight group's exact
+// dot with v_mfma_i32_16x16x64_i8 and adds one FP32 term per activation
+// group; the slices are added in index order by the whole workgroup, which
+// also applies the gate's activation, so the two products of a gated call
+// never reach memory.  The order of a column's sum depends on k only.
 //
 //  ternary: cls[c] = fma(float(dot) * xs, ws, cls[c]) per group class c and
 //           ((c0+c4)+(c1+c5))+((c2+c6)+(c3+c7)) per slice: the order of
@@ -51,7 +51,7 @@ struct SmallArgs {
     const uint8_t* w0;
     const uint8_t* w1;
     void* out;
-    int n, k, groups, s8, per_wave, tiles, mtotal, cols, act, out_dtype, part;
+    int n, k, groups, s8, per_wave, tiles, mtotal, cols, act, out_dtype, part, last_tile;
 };
 
 // Waves k is split over at most: registers for three waves per SIMD remain at
@@ -102,6 +102,7 @@ __global__ __launch_bounds__(64 * MAXW) void block_small_m_kernel(SmallArgs a) {
     const int j = lane & 15;
     const int kb = lane >> 4;
     const int m0 = blockIdx.y * a.cols;
+    const bool pair = FMT == kFmtW4 && NB == 2 && a.act < 0;  // two neighbouring tiles of one matrix
     const int mcount = min(a.cols, a.mtotal - m0);
     const int seg_bytes = seg_lds(MC, a.cols);
     const int seg_begin = wave * a.per_wave;
@@ -132,9 +133,10 @@ __global__ __launch_bounds__(64 * MAXW) void block_small_m_kernel(SmallArgs a) {
     auto unit_of = [&](int tile, int s) {
         Unit u;
         const bool ok = tile < a.tiles;
-        const size_t off = ((size_t)(ok ? tile : 0) * a.s8 + s) * UNIT;
+        const size_t off = ((size_t)(ok ? (pair ? 2 * tile : tile) : 0) * a.s8 + s) * UNIT;
         u.rs[0] = make_rsrc(a.w0 + off, UNIT);
-        u.rs[1] = make_rsrc(NB == 2 ? a.w1 + off : a.w0, UNIT);
+        const size_t next = pair && 2 * tile < a.last_tile ? (size_t)a.s8 * UNIT : 0;
+        u.rs[1] = make_rsrc(NB == 2 ? a.w1 + off + next : a.w0, UNIT);
         u.codes = ok ? 16u * lane : kBufferOOB;
         u.scales = ok ? (uint32_t)(16 * S * j) : kBufferOOB;
         return u;
@@ -420,11 +422,14 @@ __global__ __launch_bounds__(64 * MAXW) void block_small_m_kernel(SmallArgs a) {
                 }
                 y[b] = FMT == kFmtW4 ? sum * kW4Scale : sum;
             }
-            const int row = tile * 16 + (o & 15);
-            if (row < a.n) {
-                const size_t at = (size_t)(m0 + (o >> 4)) * a.n + row;
-                if constexpr (NB == 2) store_as(a.out, at, gate_activation(y[0], a.act) * y[1], a.out_dtype);
-                else static_cast<float*>(a.out)[at] = y[0];
+            const int row = (pair ? 2 * tile : tile) * 16 + (o & 15);
+            const size_t at = (size_t)(m0 + (o >> 4)) * a.n + row;
+            if (NB == 2 && !pair) {
+                if (row < a.n) store_as(a.out, at, gate_activation(y[0], a.act) * y[NB - 1], a.out_dtype);
+            } else {
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+                    if (row + 16 * b < a.n) static_cast<float*>(a.out)[at + 16 * b] = y[b];
             }
         }
     }
@@ -461,8 +466,11 @@ hipError_t launch_one(const BlockMatmul& p, SmallArgs a, int waves) {
 
 template <int FMT, int S, int NB>
 hipError_t launch_cols(const BlockMatmul& p) {
-    SmallArgs a{p.q, p.xs, p.x, p.x_stride, p.w0, p.w1, p.out, (int)p.n, (int)p.k, (int)(p.k / 128),
-                (int)((p.k + 1023) / 1024), 0, (int)((p.n + 15) / 16), (int)p.m, 0, p.act, p.out_dtype, 0};
+    const int tiles = (int)((p.n + 15) / 16);
+    const bool pair = NB == 2 && p.act < 0;
+    SmallArgs a{p.q, p.xs, p.x, p.x_stride, p.w0, pair ? p.w0 : p.w1, p.out, (int)p.n, (int)p.k, (int)(p.k / 128),
+                (int)((p.k + 1023) / 1024), 0, pair ? (tiles + 1) / 2 : tiles, (int)p.m, 0, p.act, p.out_dtype, 0,
+                tiles - 1};
     constexpr int kMany = FMT == kFmtTernary ? kTilesDefaultWaves : kW4Waves;
     a.per_wave = (a.s8 + kMany - 1) / kMany;
     const int waves = (a.s8 + a.per_wave - 1) / a.per_wave;
@@ -472,11 +480,22 @@ hipError_t launch_cols(const BlockMatmul& p) {
             if (waves <= 8) return launch_one<FMT, S, NB, 16, kSrcNatural, kALds, 8>(p, a, waves);
             return launch_one<FMT, S, NB, 16, kSrcNatural, kALds, kMany>(p, a, waves);
         }
-        if constexpr (NB == 1 && S <= 2) {
-            // K = 17408, N = 5120, m = 16: 18.9 against 23.7 us streamed; with
+        if constexpr (NB == 1) {
+            // K = 17408, N = 5120, m = 16: kABoth 18.9 against 23.7 us streamed; with
             // four scales a group, or two matrices, the registers spill.
-            if (a.per_wave == 2 && lds_bytes<NB, 16, kABoth>(a, waves) <= kLdsBytes)
-                return launch_one<FMT, S, NB, 16, kSrcNatural, kABoth, kMany>(p, a, waves);
+            const bool both = S <= 2 && a.per_wave == 2 && lds_bytes<NB, 16, kABoth>(a, waves) <= kLdsBytes;
+            const bool registers = S <= 2 && a.per_wave == 1;
+            // Two tiles at a time: twice the weights in flight and half the
+            // activations streamed.  Wins where these are streamed anyway (m = 16,
+            // K = 17408, wgroup 32, N = 5120 / 8192 / 17408 26.3 / 30.6 / 63.4 us
+            // against 21.5 / 25.2 / 55.9) and where one round of pairs replaces two of
+            // tiles (wgroup 64, N = 5120 / 8192 20.2 / 22.8 against 18.5 / 22.1; N =
+            // 10240 27.6 against 34.6); loses where half the CUs would idle (wgroup
+            // 32, N = 4096 17.7 against 21.1).
+            if (tiles > 256 && (both ? tiles <= 512 : !registers)) return launch_cols<FMT, S, 2>(p);
+            if constexpr (S <= 2) {
+                if (both) return launch_one<FMT, S, NB, 16, kSrcNatural, kABoth, kMany>(p, a, waves);
+            }
         }
         // K = 10240, N = 8192 gated, m = 16: wgroup 128 in registers 18.9 us,
         // streamed 24.6; but with four scales a group (67.9 against 30.0) or the

@@ -124,6 +124,32 @@ def test_matmul_w4_columns_do_not_depend_on_the_batch(k, wg):
         assert torch.equal(y, whole[16 - m:]), m
 
 
+@pytest.mark.parametrize("wg", [128, 64, 32])
+@pytest.mark.parametrize("m,n,k", [(16, 4100, 17408), (9, 8192, 17408), (16, 8300, 12288), (12, 4128, 26624), (5, 4200, 65536),
+                                   (16, 4097, 9728)])
+def test_matmul_w4_rows_do_not_depend_on_the_matrix(m, n, k, wg):
+    """A row's bits in a matrix of more than 256 tiles (in pairs, for some of these) and in a slice of it."""
+    announce(f"w4 slices m={m} n={n} k={k} wg={wg}")
+    pq2 = _pq2()
+    gen = torch.Generator(device=DEV).manual_seed(n + k + wg)
+    w = torch.empty(pq2.pq2_w4_tiles_bytes(n, k, wg), dtype=torch.uint8, device=DEV)
+    codes = torch.randint(0, 256, (n, k // 2), dtype=torch.uint8, generator=gen, device=DEV)
+    pq2.pq2_prepare_w4_tiles(codes, (torch.rand((n, k // wg), generator=gen, device=DEV) * 0.05).half(), wg, w)
+    q, xs = quantise(activations(m, k, 5), k)
+    y = Guarded((m, n), torch.float32)
+    pq2.pq2_matmul_w4(q, xs, w, y.t, wg)
+    got = y.read()
+    assert bool(torch.isfinite(got).all())
+    for first in (0, 2000, n // 16 * 16 - 48):      # whole tiles; the last slice ends with the matrix
+        rows = min(2000, n - first)
+        size = pq2.pq2_w4_tiles_bytes(rows, k, wg)
+        start = pq2.pq2_w4_tiles_bytes(first, k, wg) if first else 0
+        part = torch.empty((m, rows), device=DEV)
+        pq2.pq2_matmul_w4(q, xs, w[start:start + size], part, wg)
+        torch.cuda.synchronize()
+        assert torch.equal(got[:, first:first + rows], part.cpu()), f"rows from {first}"
+
+
 @pytest.mark.parametrize("m", [3, 16, 150])
 def test_w4_extreme_codes(m):
     """All weights -8 or 7 against codes of +-127: the largest dots, exact as floats."""
