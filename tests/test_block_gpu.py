@@ -92,7 +92,7 @@ W4_SHAPES = [(1, 1, 128), (1, 200, 512), (2, 17, 384), (3, 33, 1024), (4, 300, 1
              # decode: LDS full of activations, several segments a wave, each place the activations of a wide pass sit in
              (4, 33, 32768), (3, 20, 65536), (8, 40, 17408), (13, 24, 12288), (16, 20, 24576), (7, 18, 65536),
              # prefill: low-latency, 32-row and 64-row kernels, ragged rows and columns, groups behind the last segment
-             (33, 1400, 384), (257, 300, 1152), (500, 130, 2176), (1000, 1001, 256), (2100, 1100, 384), (2201, 2083, 128)]
+             (90, 1400, 384), (600, 300, 1152), (1100, 130, 2176), (33, 1400, 384), (257, 300, 1152), (500, 130, 2176), (1000, 1001, 256), (2100, 1100, 384), (2201, 2083, 128)]
 
 
 @pytest.mark.parametrize("wg", [128, 64, 32])
@@ -264,7 +264,8 @@ def ternary_tiles(n, k, seed):
 
 
 GATED_SHAPES = [(1500, 1999, 128), (600, 2100, 256), (40, 1500, 1152), (4, 33, 32768), (8, 17, 17408), (1, 1, 128), (1, 200, 1024), (2, 40, 384), (4, 33, 5120), (6, 17, 1152), (16, 100, 2176),
-                (13, 24, 17408), (37, 65, 1152), (70, 130, 640), (129, 300, 1024), (4, 20, 16384)]
+                (13, 24, 17408), (37, 65, 1152), (70, 130, 640), (129, 300, 1024), (4, 20, 16384),
+                (250, 700, 640), (200, 400, 8192)]
 
 
 @pytest.mark.parametrize("act", [0, 1])
