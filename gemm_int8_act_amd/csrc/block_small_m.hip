@@ -520,18 +520,20 @@ hipError_t launch_cols(const BlockMatmul& p) {
 }  // namespace
 
 // Passes of sixteen columns read the weights again, from the Infinity Cache.
-// Up to two passes, or two workgroups a CU in all, are faster than the prefill
-// engine, whose workgroups walk k alone: N = 6144, K = 5120 m = 17 9.3 us
-// against 15.5, FFN down m = 17 29 / 50; K = 11264, N = 109 m = 200 / 800 12.3 /
-// 21.2 against 25.7 / 26.0 (m = 1600, 700 workgroups, 31.3 / 30.7); K = 5120,
-// N = 300 m = 400 / 800 10.7 / 19.9 against 13.9 / 16.1, gated wgroup 64 14.9 /
-// 28.0 against 24.7 / 26.8; K = 1152, N = 1000 gated m = 128 9.9 against 12.0.
-// The ternary kernels stream the activations from K = 8192 on, slowly: one
-// workgroup a CU there (K = 11264, N = 109, m = 400 / 800 27.8 / 47.7 against
-// 41.2 / 41.9).
+// Up to two passes, or about three workgroups a CU in all, are faster than the
+// prefill engine, whose workgroups each walk k alone.  Decode / prefill: N =
+// 6144, K = 5120 m = 17 9.3 / 15.5 us, FFN down m = 17 29 / 50; K = 11264, N = 109
+// m = 200 / 800 (350 workgroups) 12.3 / 25.7, 21.2 / 26.0; K = 4096, N = 2700,
+// wgroup 32 m = 64 (676) 10.2 / 17.8, gated ternary 13.9 / 20.5, m = 96 (1014) 14.2
+// / 17.6 and 19.6 / 18.3; K = 5120, N = 300 m = 800 (950) 19.9 / 16.1.  Three
+// passes hold out to 1152: N = 6144, K = 5120, m = 48 15.2 / 15.8, FFN down m =
+// 40 34.2 / 44.4.  The ternary kernels stream the activations from K = 8192 on,
+// slowly: one workgroup a CU there (K = 11264, N = 109 m = 400 / 800 27.8 / 41.2,
+// 47.7 / 41.9).
 bool block_takes_small_m(const BlockMatmul& p) {
     const int64_t passes = (p.m + 15) / 16, tiles = (p.n + 15) / 16;
-    return passes <= 2 || passes * tiles <= (p.fmt == kFmtTernary && p.k > 7168 ? 256 : 512);
+    const int64_t most = p.fmt == kFmtTernary && p.k > 7168 ? 256 : passes == 3 ? 1152 : 768;
+    return passes <= 2 || passes * tiles <= most;
 }
 
 // Quantising in the product's launch saves the quantiser's (about 2 us on the

@@ -92,7 +92,7 @@ W4_SHAPES = [(1, 1, 128), (1, 200, 512), (2, 17, 384), (3, 33, 1024), (4, 300, 1
              # decode: LDS full of activations, several segments a wave, each place the activations of a wide pass sit in
              (4, 33, 32768), (3, 20, 65536), (8, 40, 17408), (13, 24, 12288), (16, 20, 24576), (7, 18, 65536),
              # prefill: low-latency, 32-row and 64-row kernels, ragged rows and columns, groups behind the last segment
-             (90, 1400, 384), (600, 300, 1152), (1100, 130, 2176), (33, 1400, 384), (257, 300, 1152), (500, 130, 2176), (1000, 1001, 256), (2100, 1100, 384), (2201, 2083, 128)]
+             (130, 1400, 384), (700, 300, 1152), (1400, 130, 2176), (33, 1400, 384), (257, 300, 1152), (500, 130, 2176), (1000, 1001, 256), (2100, 1100, 384), (2201, 2083, 128)]
 
 
 @pytest.mark.parametrize("wg", [128, 64, 32])
@@ -227,7 +227,7 @@ def test_linear_w4_codes_at_rounding_borders(m, k, dtype):
     assert torch.equal(y.view(torch.int32), z.view(torch.int32))
 
 
-@pytest.mark.parametrize("m,n", [(4, 40), (16, 40), (64, 40), (60, 1200), (2200, 2100)])
+@pytest.mark.parametrize("m,n", [(4, 40), (16, 40), (64, 40), (60, 1200), (200, 1200), (2200, 2100)])
 def test_w4_a_bad_row_stays_alone(m, n):
     """NaN scales in one row of xs reach that row's outputs only (k ends inside a segment)."""
     announce(f"w4 one bad row m={m} n={n}")
@@ -265,7 +265,7 @@ def ternary_tiles(n, k, seed):
 
 GATED_SHAPES = [(1500, 1999, 128), (600, 2100, 256), (40, 1500, 1152), (4, 33, 32768), (8, 17, 17408), (1, 1, 128), (1, 200, 1024), (2, 40, 384), (4, 33, 5120), (6, 17, 1152), (16, 100, 2176),
                 (13, 24, 17408), (37, 65, 1152), (70, 130, 640), (129, 300, 1024), (4, 20, 16384),
-                (250, 700, 640), (200, 400, 8192)]
+                (300, 700, 640), (200, 400, 8192), (70, 1100, 8192)]
 
 
 @pytest.mark.parametrize("act", [0, 1])
@@ -558,7 +558,7 @@ class Block:
         assert torch.equal(self.r.cpu(), want_r) and torch.equal(self.x.cpu(), want_x)
 
 
-@pytest.mark.parametrize("m", [1, 4, 16, 70, 300])
+@pytest.mark.parametrize("m", [1, 4, 16, 70, 300, 400])
 def test_block_together(m):
     announce(f"block together m={m}")
     b = Block(m, 640, 1152, 32)
@@ -583,7 +583,7 @@ def test_block_on_another_stream():
     b.check(r)
 
 
-@pytest.mark.parametrize("m", [2, 9, 40, 300])
+@pytest.mark.parametrize("m", [2, 9, 40, 300, 400])
 def test_block_captured_and_replayed(m):
     """Replays with new inputs, eager runs of the same buffers between them."""
     announce(f"block captured m={m}")
