@@ -11,6 +11,8 @@
 namespace {
 
 constexpr int64_t kMaxN = (int64_t)1 << 30;
+constexpr int64_t kMaxStride = (int64_t)1 << 31;  // elements: spans stay within 64 bits
+constexpr int64_t kMaxQuantised = (int64_t)1 << 34;  // elements of x: the quantiser's grid
 constexpr double kMinEps = 1e-70;
 
 bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p % a) == 0; }
@@ -73,9 +75,10 @@ int product(const int8_t* q, const float* xs, const void* w0, const void* w1, in
 int linear(const void* x, int dtype, int64_t stride, const void* w0, const void* w1, int64_t m, int64_t n, int64_t k,
            int64_t wgroup, bool gated, int act, void* out, int out_dtype, int8_t* q, float* xs, void* stream) {
     if (!x || !dtype_ok(dtype)) return PQ2_EINVAL;
+    if (m >= 1 && m <= PQ2_MAX_BLOCK_M && k_ok(k) && m * k > kMaxQuantised) return PQ2_ESHAPE;
     pq2::BlockMatmul p;
     if (int rc = check_product(q, xs, w0, w1, m, n, k, wgroup, gated, act, out, out_dtype, stream, &p)) return rc;
-    if (stride < k) return PQ2_ESHAPE;
+    if (stride < k || stride > kMaxStride) return PQ2_ESHAPE;
     if (!aligned(x, esize(dtype))) return PQ2_EALIGN;
     const size_t wbytes = (size_t)(wgroup ? pq2::w4_tiles_bytes(n, k, wgroup) : pq2::tiles_bytes(n, k));
     const Span xspan{x, row_span(m, stride, k, esize(dtype))}, qs{q, (size_t)m * k},
@@ -114,6 +117,7 @@ int pq2_prepare_w4_tiles(const uint8_t* codes, int64_t codes_row_stride_bytes, c
     if (!codes || !scales || !tiles || !group_ok(wgroup)) return PQ2_EINVAL;
     if (n < 1 || n > kMaxN || !k_ok(k)) return PQ2_ESHAPE;
     if (codes_row_stride_bytes < k / 2 || scales_row_stride_elems < k / wgroup) return PQ2_ESHAPE;
+    if (codes_row_stride_bytes > kMaxStride || scales_row_stride_elems > kMaxStride) return PQ2_ESHAPE;
     if (!aligned(tiles, 16) || !aligned(scales, 2)) return PQ2_EALIGN;
     const Span o{tiles, (size_t)pq2::w4_tiles_bytes(n, k, wgroup)};
     if (overlap(o, {codes, row_span(n, codes_row_stride_bytes, k / 2, 1)}) ||
@@ -179,6 +183,10 @@ int pq2_block_norm(const pq2_block_norm_args* a, void* stream) {
     if (m < 1 || m > PQ2_MAX_BLOCK_M || !k_ok(k)) return PQ2_ESHAPE;
     if (a->r_stride < k || (a->block && a->block_stride < k) || (a->r_out && a->r_out_stride < k) ||
         (a->x_out && a->x_out_stride < k) || (a->gate && a->gate_stride != 0 && a->gate_stride < k))
+        return PQ2_ESHAPE;
+    if (a->r_stride > kMaxStride || (a->block && a->block_stride > kMaxStride) ||
+        (a->r_out && a->r_out_stride > kMaxStride) || (a->x_out && a->x_out_stride > kMaxStride) ||
+        (a->gate && a->gate_stride > kMaxStride))
         return PQ2_ESHAPE;
     const int rs = esize(a->r_dtype), ws = esize(a->w_dtype), xs = esize(a->x_dtype), bs = esize(a->block_dtype);
     if (!aligned(a->r, rs) || !aligned(a->r_out, rs) || !aligned(a->w, ws) || !aligned(a->post_w, ws) ||

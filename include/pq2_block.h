@@ -8,7 +8,8 @@
  * on `stream`, nothing allocated, nothing kept after the call).
  *
  * q and xs are the outputs of pq2_quantize_act_i8 (groups of 128) throughout,
- * unless an entry point takes `agroup`.
+ * unless an entry point takes `agroup`.  A row stride above 2^31 elements (or
+ * bytes of codes) is PQ2_ESHAPE.
  */
 #ifndef PQ2_BLOCK_H
 #define PQ2_BLOCK_H
@@ -80,7 +81,8 @@ int pq2_matmul_w4(const int8_t* q, const float* xs, const void* tiles, int64_t m
 /* The complete call: y from bf16 / fp16 / fp32 activations, the bits of
  * pq2_quantize_act_i8 into q_work / xs_work followed by pq2_matmul_w4.  For
  * few columns (and 16-byte aligned rows of x) one launch does both and the
- * scratch is not written.
+ * scratch is not written.  m * k above 2^34 is PQ2_ESHAPE, here and in the
+ * gated complete calls.
  *   x       as pq2_quantize_act_i8.
  *   q_work  device int8 [m][k], 16-byte aligned; xs_work device float
  *           [m][k/128], 4-byte aligned: scratch owned by the caller.  Calls

@@ -92,6 +92,7 @@ def test_prepare_w4_validation():
     assert f(A, 64, B, 1, 4, 192, 128, C, None) == ESHAPE
     assert f(A, 63, B, 1, 4, 128, 128, C, None) == ESHAPE
     assert f(A, 64, B, 3, 4, 128, 32, C, None) == ESHAPE
+    assert f(A, 1 << 40, B, 1, 4, 128, 128, C, None) == ESHAPE and f(A, 64, B, 1 << 40, 4, 128, 128, C, None) == ESHAPE
     assert f(A, 64, B, 1, 4, 128, 128, C + 8, None) == EALIGN
     assert f(A, 64, B + 1, 1, 4, 128, 128, C, None) == EALIGN
     assert f(A, 64, B, 1, 4, 128, 128, A + 128, None) == EINVAL
@@ -134,6 +135,8 @@ def test_linear_validation(kind):
     for name in ("x", "q", "xs", "w", "y"):
         assert f(**{name: None}) == EINVAL
     assert f(dt=3) == EINVAL and f(stride=127) == ESHAPE and f(m=0) == ESHAPE and f(k=64) == ESHAPE
+    assert f(stride=(1 << 31) + 1) == ESHAPE and f(stride=(1 << 62) + 64) == ESHAPE
+    assert f(m=65535 * 16, k=32768, stride=32768) == ESHAPE
     assert f(x=F + 1) == EALIGN and f(dt=2, x=F + 2) == EALIGN and f(q=A + 8) == EALIGN
     assert f(q=F) == EINVAL and f(xs=F) == EINVAL and f(y=F) == EINVAL    # x overlapped
     assert f(q=C) == EINVAL and f(xs=C + 64) == EINVAL                    # the weights overlapped
@@ -167,6 +170,9 @@ def test_block_norm_validation():
     assert f(alpha=float("nan")) == EINVAL and f(alpha=float("inf")) == EINVAL and f(unit_offset=2) == EINVAL
     assert f(m=0) == ESHAPE and f(m=65535 * 16 + 1) == ESHAPE and f(m=1 << 31) == ESHAPE and f(k=64) == ESHAPE and f(k=1 << 17) == ESHAPE
     assert f(r_stride=127) == ESHAPE and f(r_out_stride=1) == ESHAPE
+    assert f(r_stride=(1 << 31) + 1) == ESHAPE and f(r_out_stride=1 << 62) == ESHAPE
+    assert f(block=D, block_stride=1 << 61) == ESHAPE and f(x_out=D, x_out_stride=1 << 40) == ESHAPE
+    assert f(block=D, block_stride=128, gate=E, gate_stride=1 << 60) == ESHAPE
     assert f(block=D, block_stride=0) == ESHAPE
     assert f(block=D, block_stride=128, gate=E, gate_stride=5) == ESHAPE
     assert f(x_out=D, x_out_stride=100) == ESHAPE
