@@ -61,10 +61,9 @@ __device__ __forceinline__ v4i ternary_operand(uint32_t d) {
 
 // The same of two w4 code dwords.  A four-bit two's complement value in the
 // high half of a byte is that value times 16 as an INT8, so no offset or sign
-// extension is needed; every dot is 16 times too large and kW4Scale undoes
-// it on the finished sum (a power of two: exact).  |16 dot| <= 16*8*127*128 <
-// 2^24 stays exact as a float.
-constexpr float kW4Scale = 0.0625f;
+// extension is needed; every dot is 16 times too large and the weight scales
+// take the factor back (weight_scale_at).  |16 dot| <= 16*8*127*128 < 2^24
+// stays exact as a float.
 __device__ __forceinline__ v4i w4_operand(uint32_t d0, uint32_t d1) {
     return v4i{(int)((d0 << 4) & 0xF0F0F0F0u), (int)(d0 & 0xF0F0F0F0u), (int)((d1 << 4) & 0xF0F0F0F0u),
                (int)(d1 & 0xF0F0F0F0u)};
@@ -127,6 +126,18 @@ __device__ __forceinline__ uint4 quantize16(const float (&v)[16], float& scale) 
 __device__ __forceinline__ float half_at(const uint4& v, int i) {
     const uint32_t w = word_of(v, i >> 1);
     return half_bits((i & 1) ? (w >> 16) : (w & 0xFFFFu));
+}
+
+// The scale of a weight group as its dot is multiplied with it: fp16 number i
+// (0..7) of 16 bytes, for 4-bit weights a sixteenth of it.  Every fp16 scale
+// has an exact sixteenth in FP32, so each term has the bits it has with a dot
+// of the weights themselves.  (Taken off the finished sum instead, the factor
+// makes sums from 2^124 on overflow on their way.)  As a fused multiply-add it
+// is one mixed-precision instruction together with the conversion from fp16.
+template <int FMT>
+__device__ __forceinline__ float weight_scale_at(const uint4& v, int i) {
+    if constexpr (FMT == kFmtW4) return __builtin_fmaf(half_at(v, i), 0.0625f, 0.0f);
+    return half_at(v, i);
 }
 
 // The gate's activation on an fp32 sum (PQ2_ACT_SILU = 0, PQ2_ACT_GELU_TANH = 1).

@@ -235,7 +235,7 @@ __global__ __launch_bounds__(256) void block_prefill_kernel(PrefillArgs a) {
                     if constexpr (S == 1) {
                         v4i dot = __builtin_amdgcn_mfma_i32_16x16x64_i8(A[0], B[b][t][0], v4i{}, 0, 0, 0);
                         dot = __builtin_amdgcn_mfma_i32_16x16x64_i8(A[1], B[b][t][1], dot, 0, 0, 0);
-                        const float ws = half_at(sc[ss][b][t], u);
+                        const float ws = weight_scale_at<FMT>(sc[ss][b][t], u);
 #pragma unroll
                         for (int r = 0; r < 4; ++r)
                             acc[b][t][i][r] = FMT == kFmtTernary
@@ -252,7 +252,7 @@ __global__ __launch_bounds__(256) void block_prefill_kernel(PrefillArgs a) {
                                 Am = v4i{Am[0] & mask, Am[1] & mask, Am[2] & mask, Am[3] & mask};
                             }
                             const v4i dot = __builtin_amdgcn_mfma_i32_16x16x64_i8(Am, B[b][t][h], v4i{}, 0, 0, 0);
-                            const float ws = half_at(sc[ss][b][t], u % SG * S + s);
+                            const float ws = weight_scale_at<FMT>(sc[ss][b][t], u % SG * S + s);
 #pragma unroll
                             for (int r = 0; r < 4; ++r)
                                 sum[r] = s == 0 ? (float)dot[r] * ws : __builtin_fmaf((float)dot[r], ws, sum[r]);
@@ -288,11 +288,10 @@ __global__ __launch_bounds__(256) void block_prefill_kernel(PrefillArgs a) {
                 const int row = row0 + 16 * i + 4 * kb + r;
                 if (row >= a.m) continue;
                 const size_t at = (size_t)row * a.n + col;
-                constexpr float fix = FMT == kFmtW4 ? kW4Scale : 1.0f;
                 if constexpr (NB == 2)
-                    store_as(a.out, at, gate_activation(acc[0][t][i][r] * fix, a.act) * (acc[1][t][i][r] * fix), a.out_dtype);
+                    store_as(a.out, at, gate_activation(acc[0][t][i][r], a.act) * acc[1][t][i][r], a.out_dtype);
                 else
-                    static_cast<float*>(a.out)[at] = acc[0][t][i][r] * fix;
+                    static_cast<float*>(a.out)[at] = acc[0][t][i][r];
             }
     }
 }

@@ -3,6 +3,7 @@ with 4-bit weights, the gated feed-forward product, the block norms.  Bounds
 are those of tests/block_reference.py; outputs are poisoned before a call and
 followed by guard elements that must not change."""
 import functools
+import math
 
 import pytest
 import torch
@@ -242,6 +243,67 @@ def test_w4_a_bad_row_stays_alone(m, n):
     torch.cuda.synchronize()
     rows = [i for i in range(m) if i != 2]
     assert torch.equal(y[rows], z[rows]) and bool(torch.isnan(z[2]).all())
+
+
+# m, n, k: decode of up to four and of more columns, each prefill kernel.
+HUGE_SHAPES = [(1, 40, 1152), (4, 40, 17408), (7, 40, 1152), (16, 40, 17408), (12, 4130, 17408), (60, 1200, 384), (200, 1200, 1152),
+               (2100, 1100, 256), (2201, 2083, 256)]
+
+
+def huge_weights(n, k, wg, seed):
+    """(tiles, c, scales) with, by row modulo three, positive weights, negative ones, and positive ones in the first half
+    of k against negative ones in the second."""
+    gen = torch.Generator().manual_seed(seed)
+    c = torch.randint(9, 16, (n, k), generator=gen, dtype=torch.uint8)
+    c[1::3] = 16 - c[1::3]
+    c[2::3, k // 2:] = 16 - c[2::3, k // 2:]
+    scales = (torch.rand((n, k // wg), generator=gen) * 0.5 + 0.5).half()
+    tiles = torch.empty(_pq2().pq2_w4_tiles_bytes(n, k, wg), dtype=torch.uint8, device=DEV)
+    _pq2().pq2_prepare_w4_tiles((c[:, 0::2] | (c[:, 1::2] << 4)).contiguous().to(DEV), scales.to(DEV), wg, tiles)
+    return tiles, c.long(), scales
+
+
+def huge_activations(m, k, wg, c, scales):
+    """Positive FP32 activations whose sums of magnitudes end between 2^126 and 2^127, so that no order of adding the
+    terms passes the largest float."""
+    x = workloads.make_activations(m, k, 3, "normal+outliers").float().abs() + 0.25
+    q, xs = ref.quantised(x, k)
+    per_group = (q.reshape(m, k // wg, wg).sum(2) * xs.repeat_interleave(128 // wg, 1))
+    most = float((per_group.abs() @ (scales.double() * (c - 8).abs().amax(1, keepdim=True)).t()).max())
+    return x * 2.0 ** (126 - math.floor(math.log2(most)))
+
+
+@pytest.mark.parametrize("wg", [128, 64, 32])
+@pytest.mark.parametrize("m,n,k", HUGE_SHAPES)
+def test_w4_sums_near_the_largest_float(m, n, k, wg):
+    """y, and every sum on the way, stays below the largest float: the result is finite and within the bound."""
+    announce(f"w4 huge m={m} n={n} k={k} wg={wg}")
+    tiles, c, scales = huge_weights(n, k, wg, n + k)
+    x = huge_activations(m, k, wg, c, scales)
+    q, xs = quantise(x, k)
+    y, z = Guarded((m, n), torch.float32), Guarded((m, n), torch.float32)
+    _pq2().pq2_matmul_w4(q, xs, tiles, y.t, wg)
+    _pq2().pq2_linear_w4(x.to(DEV), tiles, z.t, wg, torch.empty_like(q), torch.empty_like(xs))
+    want, bound = ref.product(*ref.quantised(x, k), (c - 8).double(), scales, wg)
+    assert float(want.abs().max()) > 2.0 ** 124
+    within(y.read(), want, bound, "y")
+    assert torch.equal(y.t, z.t)
+
+
+@pytest.mark.parametrize("wg", [128, 64, 32])
+@pytest.mark.parametrize("m,n,k", [(2, 40, 1152), (13, 40, 1152), (60, 1200, 384), (2201, 2083, 256)])
+def test_gated_w4_sums_near_the_largest_float(m, n, k, wg):
+    """A gate or an up product near the largest float against one that is zero: zero, not inf * 0."""
+    announce(f"gated w4 huge m={m} n={n} k={k} wg={wg}")
+    tiles, c, scales = huge_weights(n, k, wg, n + k)
+    x = huge_activations(m, k, wg, c, scales)
+    q, xs = quantise(x, k)
+    zero = torch.empty_like(tiles)
+    _pq2().pq2_prepare_w4_tiles(torch.full((n, k // 2), 0x88, dtype=torch.uint8, device=DEV), scales.to(DEV), wg, zero)
+    for gate, up in ((tiles, zero), (zero, tiles)):
+        h = Guarded((m, n), torch.float32)
+        _pq2().pq2_gated_matmul_w4(q, xs, gate, up, h.t, wg)
+        assert bool((h.read() == 0).all())
 
 
 def test_w4_zero_activations():
