@@ -10,7 +10,6 @@
 
 namespace {
 
-constexpr int64_t kMaxN = (int64_t)1 << 30;
 constexpr int64_t kMaxStride = (int64_t)1 << 31;  // elements: spans stay within 64 bits
 constexpr int64_t kMaxQuantised = (int64_t)1 << 34;  // elements of x: the quantiser's grid
 constexpr double kMinEps = 1e-70;
@@ -43,7 +42,7 @@ int check_product(const int8_t* q, const float* xs, const void* w0, const void* 
     if (!q || !xs || !w0 || !out || (gated && !w1)) return PQ2_EINVAL;
     if (wgroup != 0 && !group_ok(wgroup)) return PQ2_EINVAL;
     if (gated && ((act != PQ2_ACT_SILU && act != PQ2_ACT_GELU_TANH) || !dtype_ok(out_dtype))) return PQ2_EINVAL;
-    if (m < 1 || m > PQ2_MAX_BLOCK_M || n < 1 || n > kMaxN || !k_ok(k)) return PQ2_ESHAPE;
+    if (m < 1 || m > PQ2_MAX_BLOCK_M || n < 1 || n > PQ2_MAX_BLOCK_N || !k_ok(k)) return PQ2_ESHAPE;
     const int os = gated ? esize(out_dtype) : 4;
     if (!aligned(q, 16) || !aligned(xs, 4) || !aligned(w0, 16) || (gated && !aligned(w1, 16)) || !aligned(out, os))
         return PQ2_EALIGN;
@@ -107,7 +106,7 @@ int linear(const void* x, int dtype, int64_t stride, const void* w0, const void*
 extern "C" {
 
 int64_t pq2_w4_tiles_bytes(int64_t n, int64_t k, int64_t wgroup) {
-    if (n < 1 || n > kMaxN || !k_ok(k) || !group_ok(wgroup)) return -1;
+    if (n < 1 || n > PQ2_MAX_BLOCK_N || !k_ok(k) || !group_ok(wgroup)) return -1;
     return pq2::w4_tiles_bytes(n, k, wgroup);
 }
 
@@ -115,7 +114,7 @@ int pq2_prepare_w4_tiles(const uint8_t* codes, int64_t codes_row_stride_bytes, c
                          int64_t scales_row_stride_elems, int64_t n, int64_t k, int64_t wgroup, void* tiles,
                          void* stream) {
     if (!codes || !scales || !tiles || !group_ok(wgroup)) return PQ2_EINVAL;
-    if (n < 1 || n > kMaxN || !k_ok(k)) return PQ2_ESHAPE;
+    if (n < 1 || n > PQ2_MAX_BLOCK_N || !k_ok(k)) return PQ2_ESHAPE;
     if (codes_row_stride_bytes < k / 2 || scales_row_stride_elems < k / wgroup) return PQ2_ESHAPE;
     if (codes_row_stride_bytes > kMaxStride || scales_row_stride_elems > kMaxStride) return PQ2_ESHAPE;
     if (!aligned(tiles, 16) || !aligned(scales, 2)) return PQ2_EALIGN;

@@ -17,6 +17,7 @@
 // terms of block_small_m.hip.  That rescale (a conversion, a product and a
 // multiply-add per output and weight group, 12 issue cycles against 8 of the
 // matrix core for the group's 128 multiply-adds) bounds the kernel.
+#include "../../include/pq2_block.h"
 #include "block_internal.h"
 
 #include <algorithm>
@@ -302,10 +303,12 @@ hipError_t launch_one(const BlockMatmul& p) {
                   (int)((p.n + 15) / 16), 0, 0, p.act, p.out_dtype};
     a.nblk = (a.tiles + 4 * NT - 1) / (4 * NT);
     // A launch holds fewer than 2^32 threads: outputs of some 10^10 elements
-    // take several, each of whole workgroup rows.
+    // take several, each of whole workgroup rows.  PQ2_MAX_BLOCK_N keeps a row
+    // of the narrowest blocks (64 columns) within one.
+    constexpr int64_t kMostGroups = (int64_t)UINT32_MAX / 256;
+    static_assert((PQ2_MAX_BLOCK_N + 63) / 64 % 8 == 0 && (PQ2_MAX_BLOCK_N + 63) / 64 <= kMostGroups, "a row of workgroups");
     const int64_t per_row = a.nblk >= 8 ? (int64_t)8 * ((a.nblk + 7) / 8) : a.nblk;
-    const int64_t most = ((int64_t)UINT32_MAX / 256) / per_row * (16 * MT);
-    if (most < 1) return hipErrorInvalidValue;
+    const int64_t most = kMostGroups / per_row * (16 * MT);
     for (int64_t m0 = 0; m0 < p.m; m0 += most) {
         a.m = (int)std::min(p.m - m0, most);
         a.mblk = (a.m + 16 * MT - 1) / (16 * MT);

@@ -24,8 +24,10 @@ extern "C" {
  * SiLU g / (1 + exp(-g)); GELU 0.5 g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))). */
 enum { PQ2_ACT_SILU = 0, PQ2_ACT_GELU_TANH = 1 };
 
-/* Largest m of the entry points below. */
+/* Largest m and n of the entry points below (n: what one launch can hold a
+ * row of workgroups for, with the narrowest of the kernels' column blocks). */
 #define PQ2_MAX_BLOCK_M (65535 * 16)
+#define PQ2_MAX_BLOCK_N ((1 << 30) - 512)
 
 /* ---- 4-bit weights.
  *
@@ -48,8 +50,8 @@ enum { PQ2_ACT_SILU = 0, PQ2_ACT_GELU_TANH = 1 };
  *    8192 + 16*S*j;
  *  - padding rows (>= n) and weights (>= k) hold weight 0, scale 0. */
 
-/* Bytes of the w4 tile layout; -1 if n < 1, n > 2^30, k < 128, k % 128,
- * k > PQ2_MAX_K, or wgroup is not 128, 64 or 32. */
+/* Bytes of the w4 tile layout; -1 if n < 1, n > PQ2_MAX_BLOCK_N, k < 128,
+ * k % 128, k > PQ2_MAX_K, or wgroup is not 128, 64 or 32. */
 int64_t pq2_w4_tiles_bytes(int64_t n, int64_t k, int64_t wgroup);
 
 /* Rows of 4-bit codes and fp16 scales -> w4 tile layout.  One-time weight

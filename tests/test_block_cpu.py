@@ -147,6 +147,28 @@ def test_linear_validation(kind):
         assert f() == EDEVICE and f(x=F + 2) == EDEVICE
 
 
+@pytest.mark.parametrize("m", [1, 33, 65535 * 16])
+def test_the_largest_n_is_one_that_every_kernel_can_launch(m):
+    """Wider matrices are refused on the host (a complete call would have quantised x by the time its product has no
+    launch); the widest accepted one passes every check."""
+    most = (1 << 30) - 512          # 2^24 - 8 blocks of 64 columns; 2^24 workgroups of 256 threads are too many for a launch
+    far = [i << 52 for i in range(1, 7)]
+    def calls(n):
+        q, xs, w, u, y, x = far
+        return (pq2.lib.pq2_matmul_w4(q, xs, w, m, n, 128, 32, y, None),
+                pq2.lib.pq2_linear_w4(x, 0, 128, w, m, n, 128, 128, y, q, xs, None),
+                pq2.lib.pq2_gated_matmul_w4(q, xs, w, u, m, n, 128, 64, 0, y, 0, None),
+                pq2.lib.pq2_gated_matmul_tiles(q, xs, w, u, m, n, 128, 0, y, 0, None),
+                pq2.lib.pq2_gated_linear_w4(x, 0, 128, w, u, m, n, 128, 32, 1, y, 2, q, xs, None),
+                pq2.lib.pq2_gated_linear_tiles(x, 0, 128, w, u, m, n, 128, 1, y, 2, q, xs, None),
+                pq2.lib.pq2_prepare_w4_tiles(q, 64, xs, 4, n, 128, 32, w, None))
+    assert set(calls(most + 1)) == {ESHAPE} and set(calls(1 << 30)) == {ESHAPE}
+    assert pq2.lib.pq2_w4_tiles_bytes(most + 1, 128, 128) == -1
+    assert pq2.lib.pq2_w4_tiles_bytes(most, 128, 128) == most // 16 * (8192 + 256)
+    if torch.cuda.device_count() == 0:
+        assert set(calls(most)) == {EDEVICE}
+
+
 def norm_args(**kw):
     a = BlockNormArgs()
     a.r, a.r_stride, a.w, a.r_out, a.r_out_stride = A, 128, B, C, 128
