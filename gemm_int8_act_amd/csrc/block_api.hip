@@ -35,6 +35,25 @@ bool k_ok(int64_t k) { return k >= 128 && k % 128 == 0 && k <= PQ2_MAX_K; }
 // Rows of `stride` elements, k used in each.
 size_t row_span(int64_t m, int64_t stride, int64_t k, int es) { return ((size_t)(m - 1) * stride + k) * es; }
 
+// m rows of `bytes`, `stride` bytes apart.
+struct Rows {
+    const void* p;
+    int64_t m;
+    size_t stride, bytes;
+};
+
+// Rows of one stride may lie between each other (columns of one buffer); for
+// others the whole spans count.
+bool overlap(const Rows& a, const Rows& b) {
+    auto span = [](const Rows& r) { return Span{r.p, (size_t)(r.m - 1) * r.stride + r.bytes}; };
+    if (!a.p || !b.p || !overlap(span(a), span(b))) return false;
+    if (a.m == 1 || b.m == 1 || a.stride != b.stride) return true;
+    const size_t s = a.stride;
+    const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
+    const size_t d = y >= x ? (y - x) % s : (s - (x - y) % s) % s;  // from a row of a to the next one of b
+    return d < a.bytes || d + b.bytes > s;
+}
+
 // Checks of a product from q and xs (wgroup 0: ternary tiles; h_dtype < 0:
 // fp32 y), and its launch description.
 int check_product(const int8_t* q, const float* xs, const void* w0, const void* w1, int64_t m, int64_t n, int64_t k,
@@ -192,15 +211,14 @@ int pq2_block_norm(const pq2_block_norm_args* a, void* stream) {
         !aligned(a->gate, ws) || !aligned(a->x_out, xs) || (a->block && !aligned(a->block, bs)) ||
         !aligned(a->q, 8) || !aligned(a->xs, 4))
         return PQ2_EALIGN;
-    const Span r{a->r, row_span(m, a->r_stride, k, rs)};
-    const Span in[4] = {{a->block, row_span(m, a->block_stride, k, bs)},
-                        {a->post_w, (size_t)k * ws},
-                        {a->gate, a->gate_stride ? row_span(m, a->gate_stride, k, ws) : (size_t)k * ws},
-                        {a->w, (size_t)k * ws}};
-    const Span out[4] = {{a->r_out, row_span(m, a->r_out_stride, k, rs)},
-                         {a->x_out, row_span(m, a->x_out_stride, k, xs)},
-                         {a->q, (size_t)m * k},
-                         {a->xs, a->q ? (size_t)m * (k / a->agroup) * 4 : 0}};
+    auto rows = [&](const void* p, int64_t stride, int es) { return Rows{p, m, (size_t)stride * es, (size_t)k * es}; };
+    auto vec = [&](const void* p) { return Rows{p, 1, 0, (size_t)k * ws}; };
+    const Rows r = rows(a->r, a->r_stride, rs);
+    const Rows in[4] = {rows(a->block, a->block_stride, bs), vec(a->post_w),
+                        a->gate_stride ? rows(a->gate, a->gate_stride, ws) : vec(a->gate), vec(a->w)};
+    const size_t xs_bytes = a->q ? (size_t)(k / a->agroup) * 4 : 0;
+    const Rows out[4] = {rows(a->r_out, a->r_out_stride, rs), rows(a->x_out, a->x_out_stride, xs), rows(a->q, k, 1),
+                         {a->xs, m, xs_bytes, xs_bytes}};
     const bool in_place = a->r_out == a->r && a->r_out_stride == a->r_stride;
     for (int i = 0; i < 4; ++i) {
         if (overlap(out[i], r) && !(i == 0 && in_place)) return PQ2_EINVAL;

@@ -143,7 +143,9 @@ int pq2_gated_linear_w4(const void* x, int dtype, int64_t x_row_stride_elems, co
  * Any of the outputs r_out, x_out and (q, xs) may be absent (NULL); at least
  * one is given.  A row does not depend on the others, and r_out may be r
  * itself (same pointer, same stride): otherwise no output overlaps an input
- * or another output. */
+ * or another output.  Rows of one stride in bytes may lie between each other
+ * (columns of one buffer); with different strides the whole spans from first
+ * to last element are kept apart. */
 typedef struct pq2_block_norm_args {
     const void* r;            /* residual stream [m][r_stride]                              */
     int64_t r_stride;         /* row strides in elements, >= k                              */

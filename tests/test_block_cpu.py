@@ -2,6 +2,7 @@
 exported and bound, and bad arguments are refused on the host (every case
 fails validation or the device check, so nothing is launched)."""
 import ctypes
+import functools
 import os
 import re
 
@@ -208,6 +209,22 @@ def test_block_norm_validation():
     if torch.cuda.device_count() == 0:
         assert f() == EDEVICE and f(r_out=A) == EDEVICE
         assert f(block=D, block_stride=128, gate=E, gate_stride=0, post_w=F) == EDEVICE
+
+
+def test_block_norm_columns_of_one_buffer():
+    """Rows that lie between each other do not overlap; rows that share a byte, or have other strides, do."""
+    f = functools.partial(norm_args, r_stride=512, r_out_stride=512)            # 256 of each 1024 bytes
+    shared = [f(r_out=A + d) for d in (1024, 254, -254, 1022, 1026, 2048 + 128)]
+    shared += [f(r_out=A + 256, r_out_stride=513), f(r_out=A + 256, r_out_stride=1024),
+               f(r_out=A + 256, x_out=A + 256, x_out_stride=512), f(r_out=A + 256, x_out=A + 510, x_out_stride=512),
+               f(r_out=A + 256, block=A + 384, block_stride=512), f(r_out=A + 256, w=A + 256),
+               f(r_out=A + 256, x_out=A + 512, x_out_stride=256, x_dtype=2)]    # 512 bytes of each 1024, up to 1024: fits
+    assert shared[:-1] == [EINVAL] * (len(shared) - 1)
+    apart = [shared[-1]] + [f(r_out=A + d) for d in (256, 768, -256, -768, 2048 + 512)]
+    apart += [f(r_out=A + 256, x_out=A + 512, x_out_stride=512, block=A + 768, block_stride=512),
+              f(r_out=A, x_out=A + 512, x_out_stride=512, block=A + 256, block_stride=512, gate=A + 768, gate_stride=512)]
+    if torch.cuda.device_count() == 0:
+        assert apart == [EDEVICE] * len(apart)
 
 
 @no_gpu

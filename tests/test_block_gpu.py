@@ -520,6 +520,26 @@ def test_block_norm_in_place(case):
     check_norm(case, in_place=True)
 
 
+@pytest.mark.parametrize("m,k,pad", [(5, 1152, 0), (3, 640, 3), (800, 5120, 8)])
+def test_block_norm_columns_of_one_buffer(m, k, pad):
+    """Stream, block, gate and outputs side by side in the rows of one buffer."""
+    announce(f"block norm columns of one buffer m={m} k={k} pad={pad}")
+    pq2 = _pq2()
+    wide = torch.full((m, 5 * k + pad), 7.0, dtype=torch.bfloat16, device=DEV)
+    r, b, g, ro, xo = (wide[:, i * k:(i + 1) * k] for i in range(5))
+    for i, t in enumerate((r, b, g)):
+        t.copy_(rand((m, k), i, torch.bfloat16, 0.8))
+    w = rand((k,), 5, torch.bfloat16, 0.1, 1)
+    before = wide.cpu()
+    want_r, want_x = ref.block_norm(before[:, :k], w, 1e-5, block=before[:, k:2 * k], post_w=w,
+                                    gate=before[:, 2 * k:3 * k], alpha=0.5)
+    pq2.pq2_block_norm(r, w.to(DEV), 1e-5, block=b, post_w=w.to(DEV), gate=g, alpha=0.5, r_out=ro, x_out=xo)
+    torch.cuda.synchronize()
+    after = wide.cpu()
+    assert torch.equal(after[:, 3 * k:4 * k], want_r) and torch.equal(after[:, 4 * k:5 * k], want_x)
+    assert torch.equal(after[:, :3 * k], before[:, :3 * k]) and bool((after[:, 5 * k:] == 7.0).all())
+
+
 def test_block_norm_single_outputs():
     """Each output alone has the bits it has beside the others."""
     announce("block norm single outputs")
