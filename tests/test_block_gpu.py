@@ -245,6 +245,81 @@ def test_w4_a_bad_row_stays_alone(m, n):
     assert torch.equal(y[rows], z[rows]) and bool(torch.isnan(z[2]).all())
 
 
+# Complete calls that one launch does (block_takes_x in block_small_m.hip: m times the 12288-weight parts of k is at
+# most four), with one to five segments of k a wave, ragged ends, and passes of fewer columns than m (K > 32768).
+ONE_LAUNCH = [(1, 640), (4, 1152), (3, 11392), (4, 12288), (1, 12416), (2, 12416), (2, 17408), (2, 24576), (1, 24704),
+              (1, 33024), (1, 36864), (1, 40960), (1, 49152)]
+
+
+def poisoned_scratch(m, k):
+    return (torch.full((m, k), -77, dtype=torch.int8, device=DEV),
+            torch.full((m, k // 128), -3.0, dtype=torch.float32, device=DEV))
+
+
+def untouched(qw, sw):
+    return bool((qw == -77).all()) and bool((sw == -3.0).all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("m,k", ONE_LAUNCH)
+def test_linear_w4_in_one_launch(m, k, dtype):
+    """The bits of quantiser and product, from the launch that leaves the scratch alone."""
+    n = 77
+    x = hard_activations(m, k, dtype, m + k).to(DEV)
+    q, xs = quantise(x, k)
+    for wg in (128, 64, 32):
+        announce(f"linear w4 in one launch {dtype} m={m} k={k} wg={wg}")
+        tiles, _, _ = w4(n, k, wg, k)
+        want, y = Guarded((m, n), torch.float32), Guarded((m, n), torch.float32)
+        _pq2().pq2_matmul_w4(q, xs, tiles, want.t, wg)
+        scratch = poisoned_scratch(m, k)
+        _pq2().pq2_linear_w4(x, tiles, y.t, wg, *scratch)
+        assert torch.equal(y.read().view(torch.int32), want.read().view(torch.int32)), wg
+        assert untouched(*scratch), "took two launches"
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("m,k", ONE_LAUNCH)
+def test_gated_linear_in_one_launch(m, k, dtype):
+    pq2 = _pq2()
+    n = 45
+    x = activations(m, k, m + k, DT[dtype]).to(DEV)
+    q, xs = quantise(x, k)
+    for wg in (0, 128, 64, 32):
+        announce(f"gated linear in one launch {dtype} m={m} k={k} wg={wg}")
+        a, b = (w4(n, k, wg, i)[0] if wg else ternary_tiles(n, k, i)[0] for i in (3, 4))
+        want, h = Guarded((m, n), torch.float32), Guarded((m, n), torch.float32)
+        scratch = poisoned_scratch(m, k)
+        if wg:
+            pq2.pq2_gated_matmul_w4(q, xs, a, b, want.t, wg, pq2.ACT_GELU_TANH)
+            pq2.pq2_gated_linear_w4(x, a, b, h.t, wg, *scratch, pq2.ACT_GELU_TANH)
+        else:
+            pq2.pq2_gated_matmul_tiles(q, xs, a, b, want.t)
+            pq2.pq2_gated_linear_tiles(x, a, b, h.t, *scratch)
+        assert bool(torch.isfinite(want.t).all())
+        assert torch.equal(h.read().view(torch.int32), want.read().view(torch.int32)), wg
+        assert untouched(*scratch), "took two launches"
+
+
+@pytest.mark.parametrize("m,k", [(3, 17408), (4, 24576), (2, 36864), (1, 61440), (5, 640)])
+def test_linear_w4_in_two_launches(m, k):
+    """Past that rule, and for rows that 16-byte loads do not reach: the scratch holds the quantiser's results."""
+    announce(f"linear w4 in two launches m={m} k={k}")
+    n, wg = 33, 64
+    tiles, _, _ = w4(n, k, wg, 6)
+    for mm, shift in ((m, 0), (1, 1)):
+        x = torch.zeros(mm * k + 8, dtype=torch.bfloat16, device=DEV)[shift:shift + mm * k].view(mm, k)
+        x.copy_(activations(mm, k, 7))
+        q, xs = quantise(x, k)
+        want, y = torch.empty((mm, n), device=DEV), torch.empty((mm, n), device=DEV)
+        _pq2().pq2_matmul_w4(q, xs, tiles, want, wg)
+        qw, sw = poisoned_scratch(mm, k)
+        _pq2().pq2_linear_w4(x, tiles, y, wg, qw, sw)
+        torch.cuda.synchronize()
+        assert torch.equal(y, want)
+        assert torch.equal(qw, q) and torch.equal(sw, xs), (mm, shift)
+
+
 # m, n, k: decode of up to four and of more columns, each prefill kernel.
 HUGE_SHAPES = [(1, 40, 1152), (4, 40, 17408), (7, 40, 1152), (16, 40, 17408), (12, 4130, 17408), (60, 1200, 384), (200, 1200, 1152),
                (2100, 1100, 256), (2201, 2083, 256)]
