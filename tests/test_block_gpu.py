@@ -582,6 +582,38 @@ def test_block_norm_bits(case):
     check_norm(case)
 
 
+def guarded_rows(m, k, pad, dtype, shift):
+    """(m rows of k elements, the buffer they lie in, where they lie in it): poisoned rows, 64 elements of 42 in front of
+    the first and behind the last, and 42 between them."""
+    wide = torch.full((64 + shift + (m - 1) * (k + pad) + k + 64,), 42.0, dtype=dtype, device=DEV)
+    where = (torch.arange(m)[:, None] * (k + pad) + torch.arange(k)[None, :] + 64 + shift).flatten()
+    rows = wide.as_strided((m, k), (k + pad, 1), 64 + shift)
+    rows.fill_(float("nan"))
+    return rows, wide, where
+
+
+@pytest.mark.parametrize("m,k", [(3, 128), (2, 5120), (800, 1152), (769, 2176), (2, 8320), (770, 9216), (3, 20480), (2, 33024),
+                                 (2, 65536)])
+@pytest.mark.parametrize("pad,shift", [(0, 0), (8, 8), (0, 1), (3, 1)])
+def test_block_norm_writes_its_rows_only(m, k, pad, shift):
+    """Workgroups of one, two, four and eight chunks a thread, the last chunks partial: what lies in front of, between
+    and behind the rows of r_out and x_out stays, as does what lies behind q and xs."""
+    announce(f"block norm guards m={m} k={k} pad={pad} shift={shift}")
+    r, b, w = rand((m, k), 1, torch.bfloat16), rand((m, k), 2, torch.float32), rand((k,), 3, torch.bfloat16, 0.1, 1)
+    want_r, want_x = ref.block_norm(r, w, 1e-5, block=b, alpha=0.5, x_dtype=torch.float16)
+    r_out, r_wide, where = guarded_rows(m, k, pad, torch.bfloat16, shift)
+    x_out, x_wide, _ = guarded_rows(m, k, pad, torch.float16, shift)
+    q, xs = Guarded((m, k), torch.int8), Guarded((m, k // 32), torch.float32)
+    _pq2().pq2_block_norm(r.to(DEV), w.to(DEV), 1e-5, block=b.to(DEV), alpha=0.5, r_out=r_out, x_out=x_out, q=q.t, xs=xs.t,
+                          agroup=32)
+    q.read(), xs.read()
+    assert torch.equal(r_out.cpu(), want_r) and torch.equal(x_out.cpu(), want_x)
+    for wide in (r_wide, x_wide):
+        rest = torch.ones(wide.numel(), dtype=torch.bool)
+        rest[where] = False
+        assert bool((wide.cpu()[rest] == 42).all()), "wrote outside its rows"
+
+
 @pytest.mark.parametrize("pad,shift", [(8, 0), (16, 8), (3, 1), (0, 1), (5, 0)])
 @pytest.mark.parametrize("case", NORM_CASES[1:4], ids=lambda c: f"{c[0]}-{c[1]}-{c[2]}")
 def test_block_norm_strides(case, pad, shift):
