@@ -79,12 +79,15 @@ __device__ __forceinline__ float half_bits(uint32_t h) { return __half2float(__u
 // RN(v / d) comes from FP32 operations alone (a double product per element,
 // as in quantize.hip, issues at half their rate and the decode kernels
 // quantise in every workgroup): with d scaled to [1, 2) by a power of two,
-// y = RN(1 / d) and t0 = RN(v y) within an ulp of the quotient, the residual
-// v - t0 d is exact in one fma and RN(t0 + residual y) is the correctly
-// rounded quotient (Markstein, "Computation of elementary functions on the
-// IBM RISC System/6000 processor", 1990).  Scaling v by the same power is
-// exact for every quotient that does not round to 0: |v / d| >= 1/4 leaves
-// |v| >= 1/4.
+// y = RN(1 / d), t0 = RN(v y), e = RN(v - t0 d) and t = RN(t0 + e y), one
+// Newton step.  t0 may be off by more than an ulp (1.49 occurs), so t is not
+// RN(v / d) by a general theorem; what the codes need holds: t0 + e y is
+// within 2 * 2^-23 ulp of the quotient, so t lies on the wrong side of a border
+// h + 1/2 only for quotients that near the midpoint beside it.  With 24-bit v
+// and d those are 1246, found by their residues, and on each of them t is
+// RN(v / d) (test_quantiser_codes_at_the_hardest_quotients).
+// Scaling v by the same power is exact for every quotient that does not round
+// to 0: |v / d| >= 1/4 leaves |v| >= 1/4.
 template <int N>
 __device__ __forceinline__ void quantise_bits(const float (&v)[N], float amax, float& scale, uint32_t (&bits)[N]) {
 #pragma clang fp contract(off)

@@ -8,6 +8,8 @@ A gated output adds the activation's own error: expf within two units and the
 division and products around it, with the exponent's relative error entering
 times |z| (z the sigmoid's argument); |act'| <= 1.13 for SiLU and GELU.
 """
+import math
+
 import numpy as np
 import torch
 
@@ -88,6 +90,37 @@ def gated(g, dg, u, du, act, dtype):
     bound = da * (u.abs() + du) + a.abs() * du + h.abs() * 2 * U24
     half_step = torch.finfo(dtype).eps / 2
     return h, bound + (h.abs() + bound) * half_step + torch.finfo(dtype).tiny * torch.finfo(dtype).eps + 1e-30
+
+
+def hard_quotients():
+    """Every (x, d, M), x and d float32 with 1 <= d < 2, whose quotient q = x / d lies next to a border h + 1/2 of the codes
+    (0 <= h <= 126) and so near the FP32 midpoint M beside it that quantise_bits might round it to the other side.
+
+    Its t = RN(t0 + e y), with y = RN(1 / d), t0 = RN(x y), e = RN(x - t0 d), is RN(q + delta).  y is within 2^-24 of
+    1 / d, relative; x y hence within one ulp of q and t0 within two.  e and y bring a relative error of 2^-24 each into
+    e y ~ q - t0, so |delta| <= 2 ulp * 2^-23 * (1 + 2^-25).  t is RN(q) unless a midpoint lies between q and q + delta,
+    and the code is that of RN(q) unless this midpoint is beside a border.  With M = M' 2^(m-24), M' odd and of 25 bits,
+    d = D 2^-23 and x = X 2^(s+m-47), s = 24 or 25: x - M d = (X 2^s - M' D) 2^(m-47), and |q - M| <= |delta| leaves
+    |X 2^s - M' D| < 8: zero never (M' is odd, D of at most 24 bits), so for each M and s seven values of either sign,
+    each with one D modulo 2^s."""
+    x, d, mids = [], [], []
+    for h in range(127):
+        border = np.float32(h + 0.5)
+        for side in (np.float32(0), np.float32(1000)):
+            mid = (float(border) + float(np.nextafter(border, side))) / 2
+            e = math.frexp(mid)[1] - 1
+            big = int(math.ldexp(mid, 24 - e))
+            assert big % 2 == 1 and 1 << 24 <= big < 1 << 25
+            for s in (24, 25):
+                inverse = pow(big, -1, 1 << s)
+                for rest in (r for r in range(-7, 8) if r):
+                    den = -rest * inverse % (1 << s)
+                    num = (rest + big * den) >> s
+                    if 1 << 23 <= den < 1 << 24 and 1 << 23 <= num <= 1 << 24:
+                        d.append(math.ldexp(den, -23))
+                        x.append(math.ldexp(num, s + e - 47))
+                        mids.append(mid)
+    return np.array(x), np.array(d), np.array(mids)
 
 
 def block_norm(r, w, eps, block=None, post_w=None, gate=None, alpha=1.0, unit_offset=False, x_dtype=None):

@@ -3,9 +3,12 @@ exported and bound, and bad arguments are refused on the host (every case
 fails validation or the device check, so nothing is launched)."""
 import ctypes
 import functools
+import math
 import os
 import re
+from fractions import Fraction
 
+import numpy as np
 import pytest
 import torch
 
@@ -225,6 +228,71 @@ def test_block_norm_columns_of_one_buffer():
               f(r_out=A, x_out=A + 512, x_out_stride=512, block=A + 256, block_stride=512, gate=A + 768, gate_stride=512)]
     if torch.cuda.device_count() == 0:
         assert apart == [EDEVICE] * len(apart)
+
+
+def rn32(v):
+    """A positive Fraction rounded to 24 significant bits, ties to even."""
+    e = v.numerator.bit_length() - v.denominator.bit_length()
+    while v >= Fraction(2) ** e:
+        e += 1
+    while v < Fraction(2) ** (e - 1):
+        e -= 1
+    unit = Fraction(2) ** (e - 24)
+    return round(v / unit) * unit        # (Python's round: ties to even)
+
+
+def test_quantiser_codes_at_the_hardest_quotients():
+    """The steps of quantise_bits in exact arithmetic, on every quotient where they might miss the correctly rounded one
+    at a border of the codes: the same codes."""
+    xs, ds, _ = ref.hard_quotients()
+    assert len(xs) > 1000
+    differ = 0
+    for x, d in zip(map(Fraction, xs), map(Fraction, ds)):
+        y = rn32(1 / d)
+        t0 = rn32(x * y)
+        e = x - t0 * d
+        e = (rn32(e) if e > 0 else -rn32(-e)) if e else e
+        t, q = rn32(t0 + e * y), rn32(x / d)
+        assert abs(t0 - x / d) <= 2 * Fraction(float(np.spacing(np.float32(float(q))))), (float(x), float(d))
+        differ += t != q
+        assert round(t) == round(q), (float(x), float(d))
+    print(f"{len(xs)} quotients, {differ} rounded otherwise")
+
+
+def test_hard_quotients_are_all_there_are():
+    """Found by their residue, against all 2^23 divisors tried for some of the midpoints."""
+    xs, ds, mids = ref.hard_quotients()
+    den = np.arange(1 << 23, 1 << 24, dtype=np.int64)
+    for mid in np.unique(mids)[::23]:
+        e = math.frexp(mid)[1] - 1
+        product = int(math.ldexp(mid, 24 - e)) * den
+        tried = set()
+        for s in (24, 25):
+            num = (product + (1 << s >> 1)) >> s
+            hit = (np.abs((num << s) - product) < 8) & (num >= 1 << 23) & (num <= 1 << 24)
+            tried |= {(math.ldexp(int(a), s + e - 47), math.ldexp(int(b), -23)) for a, b in zip(num[hit], den[hit])}
+        assert tried == set(zip(xs[mids == mid].tolist(), ds[mids == mid].tolist()))
+
+
+def test_quantiser_codes_next_to_the_borders():
+    """The same steps in float arithmetic, for random divisors and the four x around each border and the midpoints
+    beside it.  (Products of floats are exact in doubles, and x - t0 d is a double; t0 + e y, rounded to a double
+    first, could only differ within 2^-28 ulp of a midpoint: the cases of the test above.)"""
+    rng = np.random.default_rng(1)
+    f32, f64 = np.float32, np.float64
+    for h in range(127):
+        d = (rng.integers(1 << 23, 1 << 24, 4000) * 2.0 ** -23).astype(f32)
+        border = f32(h + 0.5)
+        for mid in (f64(border), (f64(border) + f64(np.nextafter(border, f32(0)))) / 2,
+                    (f64(border) + f64(np.nextafter(border, f32(1000)))) / 2):
+            x = (mid * d.astype(f64)).astype(f32)
+            for step in (x, np.nextafter(x, f32(0)), np.nextafter(x, f32(1000))):
+                q = (step.astype(f64) / d).astype(f32)
+                y = f32(1) / d
+                t0 = step * y
+                e = (step.astype(f64) - t0.astype(f64) * d).astype(f32)
+                t = (t0.astype(f64) + e.astype(f64) * y).astype(f32)
+                assert np.array_equal(np.rint(t), np.rint(q)), h
 
 
 @no_gpu

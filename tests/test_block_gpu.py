@@ -245,12 +245,6 @@ def test_w4_a_bad_row_stays_alone(m, n):
     assert torch.equal(y[rows], z[rows]) and bool(torch.isnan(z[2]).all())
 
 
-# Complete calls that one launch does (block_takes_x in block_small_m.hip: m times the 12288-weight parts of k is at
-# most four), with one to five segments of k a wave, ragged ends, and passes of fewer columns than m (K > 32768).
-ONE_LAUNCH = [(1, 640), (4, 1152), (3, 11392), (4, 12288), (1, 12416), (2, 12416), (2, 17408), (2, 24576), (1, 24704),
-              (1, 33024), (1, 36864), (1, 40960), (1, 49152)]
-
-
 def poisoned_scratch(m, k):
     return (torch.full((m, k), -77, dtype=torch.int8, device=DEV),
             torch.full((m, k // 128), -3.0, dtype=torch.float32, device=DEV))
@@ -258,6 +252,41 @@ def poisoned_scratch(m, k):
 
 def untouched(qw, sw):
     return bool((qw == -77).all()) and bool((sw == -3.0).all())
+
+
+def test_linear_w4_codes_at_the_hardest_quotients():
+    """The in-kernel quantiser on every quotient where its steps might miss a border, one to a group (the group's
+    largest element gives its divisor), over exponents and signs; a row of weights picks each group's code."""
+    announce("linear w4 hardest quotients")
+    xs, ds, _ = ref.hard_quotients()
+    amax = (ds * 127).astype("float32")
+    fits = ((amax.astype("float64") / 127).astype("float32") == ds) & (amax >= xs)
+    xs, ds, amax = (torch.from_numpy(v[fits].astype("float64")) for v in (xs, ds, amax))
+    assert len(xs) > 1000
+    k = 49152
+    groups = k // 128
+    codes = torch.full((groups, k // 2), 0x88, dtype=torch.uint8)
+    codes[torch.arange(groups), 64 * torch.arange(groups)] = 0x98           # weight 1 at the group's second element
+    tiles = torch.empty(_pq2().pq2_w4_tiles_bytes(groups, k, 32), dtype=torch.uint8, device=DEV)
+    _pq2().pq2_prepare_w4_tiles(codes.to(DEV), torch.ones((groups, k // 32), dtype=torch.float16, device=DEV), 32, tiles)
+    for first in range(0, len(xs), groups):
+        part = slice(first, min(first + groups, len(xs)))
+        some = part.stop - first
+        scale = torch.exp2((torch.arange(some) * 37 % 201 - 100).double()) * (1 - 2 * (torch.arange(some) % 2)).double()
+        x = torch.zeros((1, groups, 128), dtype=torch.float64)
+        x[0, :some, 0], x[0, :some, 1] = amax[part] * scale, xs[part] * scale
+        x = x.float().view(1, k)
+        q, s = ref.quantised(x, k)
+        assert torch.equal(s[0, :some], ds[part] * scale.abs())
+        y, (qw, sw) = Guarded((1, groups), torch.float32), poisoned_scratch(1, k)
+        _pq2().pq2_linear_w4(x.to(DEV), tiles, y.t, 32, qw, sw)
+        assert torch.equal(y.read()[0], (q[0, :, 1] * s[0]).float()) and untouched(qw, sw)
+
+
+# Complete calls that one launch does (block_takes_x in block_small_m.hip: m times the 12288-weight parts of k is at
+# most four), with one to five segments of k a wave, ragged ends, and passes of fewer columns than m (K > 32768).
+ONE_LAUNCH = [(1, 640), (4, 1152), (3, 11392), (4, 12288), (1, 12416), (2, 12416), (2, 17408), (2, 24576), (1, 24704),
+              (1, 33024), (1, 36864), (1, 40960), (1, 49152)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
