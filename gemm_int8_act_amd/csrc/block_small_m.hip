@@ -490,7 +490,8 @@ hipError_t launch_cols(const BlockMatmul& p) {
         }
         if constexpr (NB == 1) {
             // K = 17408, N = 5120, m = 16: kABoth 18.9 against 23.7 us streamed; with
-            // four scales a group, or two matrices, the registers spill.
+            // four scales a group, or two matrices, the registers spill (three of
+            // them at wgroup 64 as it is).
             const bool both = S <= 2 && a.per_wave == 2 && lds_bytes<NB, 16, kABoth>(a, waves) <= kLdsBytes;
             const bool registers = S <= 2 && a.per_wave == 1;
             // Two tiles at a time: twice the weights in flight and half the
@@ -508,7 +509,8 @@ hipError_t launch_cols(const BlockMatmul& p) {
         // K = 10240, N = 8192 gated, m = 16: wgroup 128 in registers 18.9 us,
         // streamed 24.6; but with four scales a group (67.9 against 30.0) or the
         // ternary kernel's eight sums and sixteen waves (41.5 against 31.8) the
-        // registers spill.
+        // registers spill more than streaming's (45 in the ternary kernel, which
+        // sixteen waves leave 128 registers; none in the 4-bit ones).
         if constexpr (FMT == kFmtW4 && S <= 2) {
             if (a.per_wave == 1) return launch_one<FMT, S, NB, 16, kSrcNatural, kARegisters, kMany>(p, a, waves);
         }
@@ -538,6 +540,12 @@ hipError_t launch_cols(const BlockMatmul& p) {
 // 40 34.2 / 44.4.  The ternary kernels stream the activations from K = 8192 on,
 // slowly: one workgroup a CU there (K = 11264, N = 109 m = 400 / 800 27.8 / 41.2,
 // 47.7 / 41.9).
+// The rule knows neither the weight group nor k beyond that, and misses sizes on
+// both sides: decode would be faster at m = 64 for N = 4096, K = 8192 wgroup 32 /
+// 128 (24.4 / 33.1, 20.8 / 22.5), N = 5120, K = 17408 wgroup 32 (56.9 / 71.4) and N =
+// 4096, K = 12288 gated wgroup 64 (55.0 / 60.4), but not wgroup 128 there (37.2 /
+// 32.4) nor gated ternary (57.5 / 38.2 at N = 4096, K = 8192); prefill at m = 96
+// for N = 2000, K = 1024 wgroup 64 (6.7 / 6.3).
 bool block_takes_small_m(const BlockMatmul& p) {
     const int64_t passes = (p.m + 15) / 16, tiles = (p.n + 15) / 16;
     const int64_t most = p.fmt == kFmtTernary && p.k > 7168 ? 256 : passes == 3 ? 1152 : 768;
