@@ -410,6 +410,26 @@ def test_gated_w4_sums_near_the_largest_float(m, n, k, wg):
         assert bool((h.read() == 0).all())
 
 
+@pytest.mark.parametrize("m,n", [(1, 48), (4, 48), (9, 48), (64, 48), (200, 1200), (2200, 2083)])
+def test_w4_subnormal_scales_and_sums(m, n):
+    """One group: y = RN(RN(dot * ws) * xs) bit for bit, with subnormal fp16 weight scales, and activation scales down
+    to where y is subnormal."""
+    announce(f"w4 subnormals m={m} n={n}")
+    k = 128
+    codes, scales, c = ref.make_w4(n, k, k, 5)
+    scales = (torch.arange(1, n + 1)[:, None] % 1500 * 2.0 ** -24).half()
+    tiles = torch.empty(_pq2().pq2_w4_tiles_bytes(n, k, k), dtype=torch.uint8, device=DEV)
+    _pq2().pq2_prepare_w4_tiles(codes.to(DEV), scales.to(DEV), k, tiles)
+    x = workloads.make_activations(m, k, 6, "normal").float() * torch.exp2(-(torch.arange(m) * 29 % 130).float())[:, None]
+    q, xs = ref.quantised(x, k)
+    dot = q[:, 0] @ (c - 8).double().t()
+    want = (dot * scales.double().t()).float() * xs.float()
+    y = Guarded((m, n), torch.float32)
+    _pq2().pq2_matmul_w4(*quantise(x, k), tiles, y.t, k)
+    assert torch.equal(y.read(), want)
+    assert m < 64 or bool(((want != 0) & (want.abs() < 2.0 ** -126)).any())
+
+
 def test_w4_zero_activations():
     announce("w4 zero activations")
     tiles, _, _ = w4(30, 640, 32, 1)
