@@ -692,3 +692,14 @@ from .block import (  # noqa: E402
     pq2_prepare_w4_tiles,
     pq2_w4_tiles_bytes,
 )
+
+# The operators of include/pq2_attention.h.
+from .attention import (  # noqa: E402
+    ATTENTION_EXPORTED,
+    pq2_attention_paged,
+    pq2_attention_paged_workspace,
+    pq2_attention_prompt,
+    pq2_kv_page_bytes,
+    pq2_kv_read,
+    pq2_kv_write,
+)

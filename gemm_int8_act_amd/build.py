@@ -22,7 +22,7 @@ LIB = os.path.join(HERE, "libpq2.so")
 BUILD_DIR = os.path.join(HERE, "_build")
 SOURCES = ["api.hip", "quantize.hip", "small_m.hip", "small_m_wg.hip", "tiles.hip", "prefill.hip", "probe.hip",
            "block_api.hip", "w4.hip", "block_small_m.hip", "block_prefill.hip",
-           "norm.hip"]
+           "norm.hip", "attention_api.hip", "kv_cache.hip", "attention_paged.hip", "attention_prompt.hip"]
 ARCH = "gfx950"
 
 COMMON_FLAGS = [
