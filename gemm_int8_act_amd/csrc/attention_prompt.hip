@@ -17,11 +17,9 @@ namespace pq2 {
 
 namespace {
 
-constexpr int kWaves = 4;
-constexpr int kThreads = 64 * kWaves;
-constexpr int kBM = 32 * kWaves;    // query rows of a workgroup
 constexpr int kKeys = 64;           // keys of a step
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kSlack = 8.0f;      // weights grow to 2^8 before a row's reference moves
 
 struct PromptArgs {
     const uint16_t* q;
@@ -31,22 +29,25 @@ struct PromptArgs {
     int64_t q_stride, q_head, k_stride, k_head, v_stride, v_head, out_stride, out_head;
     const int32_t* starts_q;
     const int32_t* starts_k;
-    int rows_q, rows_k, seqs, group, window, causal;
-    float scale2;
+    int rows_q, rows_k, seqs, heads, group, window, causal, tiles;
+    float scale2, slack;  // scale * log2(e); how far scores may pass a row's reference (in scores)
 };
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
 
 template <typename T> struct Half;
 template <> struct Half<__bf16> {
     typedef bf16x8 v8;
     typedef __bf16 v2 __attribute__((ext_vector_type(2)));
     static __device__ __forceinline__ v16f mfma(v8 a, v8 b, v16f c) { return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0); }
+    static __device__ __forceinline__ float add2(v2 e, float s) { return __builtin_amdgcn_fdot2_f32_bf16(e, v2{(__bf16)1.0f, (__bf16)1.0f}, s, false); }
 };
 template <> struct Half<_Float16> {
     typedef f16x8 v8;
     typedef _Float16 v2 __attribute__((ext_vector_type(2)));
     static __device__ __forceinline__ v16f mfma(v8 a, v8 b, v16f c) { return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0); }
+    static __device__ __forceinline__ float add2(v2 e, float s) { return __builtin_amdgcn_fdot2(e, v2{(_Float16)1.0f, (_Float16)1.0f}, s, false); }
 };
 
 // 16-byte chunk c of row r of a tile, as it lies in LDS: keys are read 16 bytes
@@ -71,18 +72,34 @@ __device__ __forceinline__ float sum_halves(float v) {
     return __uint_as_float(a[0]) + __uint_as_float(a[1]);
 }
 
-// The sequence and query tile of a workgroup: tiles are counted through the
-// sequences, 64 of them a step; seq < 0 behind the last tile.
+// 16 bytes a lane from a buffer straight into LDS: lane i's go to lds_addr +
+// 16 i.  Its completion is waited for by wait_loads, not by the compiler.
+__device__ __forceinline__ void load_lds(i32x4_t rsrc, uint32_t voff, uint32_t lds_addr) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                 :
+                 : "s"(lds_addr), "v"(voff), "s"(rsrc)
+                 : "memory", "m0");
+}
+
+__device__ __forceinline__ void wait_loads() {
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+}
+
+// The sequence and query tile of a workgroup: tiles of BM rows are counted
+// through the sequences, 64 of them a step; seq < 0 behind the last tile.
 struct Place {
     int seq, tile, tiles;
 };
 
+template <int BM>
 __device__ __forceinline__ Place place_of(const int32_t* starts, int seqs, int index) {
     const int lane = threadIdx.x & 63;
     for (int s0 = 0; s0 < seqs; s0 += 64) {
         const int s = s0 + lane;
         int tiles = 0;
-        if (s < seqs) tiles = (max(starts[s + 1] - starts[s], 0) + kBM - 1) / kBM;
+        if (s < seqs) tiles = (max(starts[s + 1] - starts[s], 0) + BM - 1) / BM;
         int sum = tiles;
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) {
@@ -99,30 +116,41 @@ __device__ __forceinline__ Place place_of(const int32_t* starts, int seqs, int i
     return {-1, 0, 0};
 }
 
-template <int D, typename T>
-__global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attention_prompt_kernel(PromptArgs a) {
+// Workgroups go to the eight XCDs in turn: the one at `id` takes the item at
+// which its XCD's share, a stretch of neighbouring items, has come.
+__device__ __forceinline__ int item_of(int id, int total) {
+    const int xcd = id & 7, share = total >> 3, more = total & 7;
+    return xcd * share + min(xcd, more) + (id >> 3);
+}
+
+template <int D, typename T, int W>
+__global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attention_prompt_kernel(PromptArgs a) {
     typedef typename Half<T>::v8 v8;
     typedef typename Half<T>::v2 v2;
-    constexpr int CH = kKeys * D / 8;          // chunks of a tile
-    constexpr int PER = CH / kThreads;         // of them a thread's
+    constexpr int BM = 32 * W;                   // query rows of a workgroup, 32 of them a wave's
     constexpr int DB = D / 32;
-    extern __shared__ uint4 lds[];             // [2][K tile, V tile]
+    constexpr int TILE = kKeys * D * 2;          // bytes of a tile in LDS
+    constexpr int LOADS = TILE / 1024 / W;       // 1 KB loads of a wave for a tile
+    constexpr int LROWS = 512 / D;               // rows of such a load
+    extern __shared__ uint4 lds[];               // K tiles 0 and 1, V tiles 0 and 1
 
-    const Place place = place_of(a.starts_q, a.seqs, blockIdx.x);
+    // Items: heads of a key-value head next to each other, then its tiles.
+    const int item = item_of(blockIdx.y * gridDim.x + blockIdx.x, gridDim.x * gridDim.y);
+    const int per = a.tiles * a.group, kvh = item / per, head = kvh * a.group + item % a.group;
+    const Place place = place_of<BM>(a.starts_q, a.seqs, item % per / a.group);
     if (place.seq < 0) return;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int row = lane & 31, half = lane >> 5;
     const int seq = __builtin_amdgcn_readfirstlane(place.seq);
     const int tile = __builtin_amdgcn_readfirstlane(place.tiles - 1 - place.tile);  // the longest first
-    const int head = blockIdx.y, kvh = head / a.group;
 
     // Queries and keys of the sequence, kept inside the tensors.
     const int qs = a.starts_q[seq], ks = a.starts_k[seq];
     const int nq = a.starts_q[seq + 1] - qs;
     const int nk = ks < 0 ? 0 : max(0, min(a.starts_k[seq + 1], a.rows_k) - ks);
-    const int q0 = tile * kBM;
+    const int q0 = tile * BM;
     const int offset = nk - nq;  // a query's position is its index + offset
-    const int hi = a.causal ? min(nk, offset + min(q0 + kBM, nq)) : nk;
+    const int hi = a.causal ? min(nk, offset + min(q0 + BM, nq)) : nk;
     const int lo = a.window ? max(0, offset + q0 - a.window + 1) & ~(kKeys - 1) : 0;
 
     const int qi = q0 + 32 * wave + row;
@@ -143,86 +171,56 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attention_prompt_k
     const int all_hi = a.causal ? min(nk, wave_first + 1) : nk;
     const int all_lo = a.window ? wave_first + 31 - a.window + 1 : 0;
 
-    uint4 stage[2][PER];
+    // Loads: chunk `lane` of load i of this wave is row lrow + i * W * LROWS of
+    // the tile (a multiple of eight apart: one swizzle).  Rows behind the last key repeat it.
     const uint16_t* kbase = a.k + (int64_t)ks * a.k_stride + kvh * a.k_head;
     const uint16_t* vbase = a.v + (int64_t)ks * a.v_stride + kvh * a.v_head;
-    auto records = [&](int key0, int64_t stride) {
-        const int64_t rows = nk - key0;
-        return rows <= 0 ? 0u : (uint32_t)min((rows - 1) * stride * 2 + D * 2, (int64_t)0x7FFFFFFF);
-    };
-    auto fetch = [&](int key0) {
-        const auto rk = make_rsrc(kbase + (int64_t)key0 * a.k_stride, records(key0, a.k_stride));
-        const auto rv = make_rsrc(vbase + (int64_t)key0 * a.v_stride, records(key0, a.v_stride));
+    const int lrow = wave * LROWS + lane / (D / 8), lcol = lane % (D / 8);
+    const uint32_t kcol = 16 * (k_chunk<D>(lrow, lcol) - lrow * (D / 8));
+    const uint32_t vcol = 16 * (v_chunk<D>(lrow, lcol) - lrow * (D / 8));
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint4*)lds;
+    auto fetch = [&](const uint16_t* base, int64_t stride, uint32_t col, int key0, uint32_t to) {
+        const i32x4_t r = make_srsrc(base + (int64_t)key0 * stride, 0x7FFFFFFFu);
+        const int last = nk - 1 - key0;
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int c = threadIdx.x + i * kThreads, r = c / (D / 8), col = c % (D / 8);
-            stage[0][i] = buf_load16(rk, (uint32_t)r * (uint32_t)(a.k_stride * 2) + col * 16);
-            stage[1][i] = buf_load16(rv, (uint32_t)r * (uint32_t)(a.v_stride * 2) + col * 16);
-        }
-    };
-    auto put = [&](int buf) {
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int c = threadIdx.x + i * kThreads, r = c / (D / 8), col = c % (D / 8);
-            lds[buf * 2 * CH + k_chunk<D>(r, col)] = stage[0][i];
-            lds[buf * 2 * CH + CH + v_chunk<D>(r, col)] = stage[1][i];
-        }
+        for (int i = 0; i < LOADS; ++i)
+            load_lds(r, (uint32_t)min(lrow + i * W * LROWS, last) * (uint32_t)(stride * 2) + col,
+                     lds0 + to + 1024 * (wave + i * W));
     };
 
     v16f acc[DB];
 #pragma unroll
     for (int d = 0; d < DB; ++d) acc[d] = v16f{};
     float m = -INFINITY, l = 0.0f;
+    v16f sc[2];
+    v8 p[2][2];
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int t = 0; t < 2; ++t) p[b][t] = v8{};
 
-    if (lo < hi) {
-        fetch(lo);
-        put(0);
-    }
-    int buf = 0;
-    for (int key0 = lo; key0 < hi; key0 += kKeys, buf ^= 1) {
-        const bool more = key0 + kKeys < hi;
-        if (more) fetch(key0 + kKeys);
-        __syncthreads();
-        const uint4* kt = lds + buf * 2 * CH;
-        const uint4* vt = kt + CH;
-        v16f sc[2] = {};
+    auto scores = [&](int buf, v16f (&s2)[2]) {
+        const uint4* kt = lds + buf * (TILE / 16);
+#pragma unroll
+        for (int b = 0; b < 2; ++b) s2[b] = v16f{};
 #pragma unroll
         for (int s = 0; s < D / 16; ++s)
 #pragma unroll
             for (int b = 0; b < 2; ++b)
-                sc[b] = Half<T>::mfma(__builtin_bit_cast(v8, kt[k_chunk<D>(32 * b + row, 2 * s + half)]), qf[s], sc[b]);
-        if (key0 + kKeys > all_hi || key0 < all_lo) {
-#pragma unroll
-            for (int b = 0; b < 2; ++b)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const int key = key0 + 32 * b + 8 * (r / 4) + 4 * half + r % 4;
-                    if (key >= seen_hi || key < seen_lo) sc[b][r] = -INFINITY;
-                }
-        }
-        float top = -INFINITY;
-#pragma unroll
-        for (int b = 0; b < 2; ++b)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) top = fmaxf(top, sc[b][r]);
-        // (scale2 may be negative or zero: the maximum is of the scaled scores.)
-        top = fmaxf(m, max_halves(top));
-        const float ref = top == -INFINITY ? 0.0f : top;
-        const float alpha = __builtin_amdgcn_exp2f((m - ref) * a.scale2);
-        const float bias = ref * a.scale2;
-        m = top;
-        l *= alpha;
-#pragma unroll
-        for (int d = 0; d < DB; ++d) acc[d] *= alpha;
-        v8 p[2][2];
+                s2[b] = Half<T>::mfma(__builtin_bit_cast(v8, kt[k_chunk<D>(32 * b + row, 2 * s + half)]), qf[s], s2[b]);
+    };
+    auto mask = [&](int key0, v16f (&s2)[2]) {
+        if (key0 + kKeys <= all_hi && key0 >= all_lo) return;
 #pragma unroll
         for (int b = 0; b < 2; ++b)
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
-                const T e = (T)__builtin_amdgcn_exp2f(__builtin_fmaf(sc[b][r], a.scale2, -bias));
-                l += (float)e;
-                p[b][r / 8][r % 8] = e;
+                const int key = key0 + 32 * b + 8 * (r / 4) + 4 * half + r % 4;
+                if (key >= seen_hi || key < seen_lo) s2[b][r] = -INFINITY;
             }
+    };
+    auto values = [&](int buf) {
+        const char* vt = reinterpret_cast<const char*>(lds) + (2 + buf) * TILE;
 #pragma unroll
         for (int b = 0; b < 2; ++b)
 #pragma unroll
@@ -234,15 +232,67 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attention_prompt_k
                     for (int x = 0; x < 2; ++x) {
                         const int vr = 32 * b + 16 * t + 8 * x + 4 * half + (lane & 15) / 4;
                         const int col = 32 * d + 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
-                        const char* at = reinterpret_cast<const char*>(vt + v_chunk<D>(vr, col / 8)) + 2 * (col % 8);
                         part[x] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                            (__attribute__((address_space(3))) s16x4*)(at));
+                            (__attribute__((address_space(3))) s16x4*)(vt + 16 * v_chunk<D>(vr, col / 8) + 2 * (col % 8)));
                     }
-                    typedef short s16x8 __attribute__((ext_vector_type(8)));
                     const s16x8 v = __builtin_shufflevector(part[0], part[1], 0, 1, 2, 3, 4, 5, 6, 7);
                     acc[d] = Half<T>::mfma(__builtin_bit_cast(v8, v), p[b][t], acc[d]);
                 }
-        if (more) put(buf ^ 1);
+    };
+
+    if (lo < hi) {
+        // Values before the first tile: zeros, for the first step's product.
+        for (int i = threadIdx.x; i < TILE / 16; i += 64 * W) lds[3 * (TILE / 16) + i] = make_uint4(0, 0, 0, 0);
+        fetch(kbase, a.k_stride, kcol, lo, 0);
+        if (lo + kKeys < hi) fetch(kbase, a.k_stride, kcol, lo + kKeys, TILE);
+        wait_loads();
+        __syncthreads();
+        scores(0, sc);
+        mask(lo, sc);
+        __syncthreads();
+        int buf = 0;
+        for (int key0 = lo; key0 < hi; key0 += kKeys, buf ^= 1) {
+            // Keys two tiles ahead and this tile's values are on their way
+            // while the next tile's scores, this tile's softmax and the last
+            // tile's values, which do not need each other, are computed.
+            if (key0 + 2 * kKeys < hi) fetch(kbase, a.k_stride, kcol, key0 + 2 * kKeys, buf * TILE);
+            fetch(vbase, a.v_stride, vcol, key0, (2 + buf) * TILE);
+            v16f next[2];
+            scores(buf ^ 1, next);
+            values(buf ^ 1);
+            float top = sc[0][0];
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) top = fmaxf(top, sc[b][r]);
+            top = max_halves(top);
+            const float old = m;
+            if (top > m + a.slack) m = top;
+            const float ref = m == -INFINITY ? 0.0f : m;
+            const float alpha = __builtin_amdgcn_exp2f((old - ref) * a.scale2);
+            const float bias = ref * a.scale2;
+            l *= alpha;
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int r = 0; r < 16; r += 2) {
+                    const v2 e = {(T)__builtin_amdgcn_exp2f(__builtin_fmaf(sc[b][r], a.scale2, -bias)),
+                                  (T)__builtin_amdgcn_exp2f(__builtin_fmaf(sc[b][r + 1], a.scale2, -bias))};
+                    l = Half<T>::add2(e, l);
+                    p[b][r / 8][r % 8] = e[0];
+                    p[b][r / 8][r % 8 + 1] = e[1];
+                }
+            if (__any(alpha != 1.0f)) {
+#pragma unroll
+                for (int d = 0; d < DB; ++d) acc[d] *= alpha;
+            }
+            sc[0] = next[0];
+            sc[1] = next[1];
+            mask(key0 + kKeys, sc);
+            wait_loads();
+            __syncthreads();
+        }
+        values(buf ^ 1);
     }
 
     l = sum_halves(l);
@@ -259,26 +309,32 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attention_prompt_k
         }
 }
 
-template <int D, typename T>
-void start(const PromptArgs& a, int heads, hipStream_t stream) {
-    const dim3 grid((unsigned)((a.rows_q + kBM - 1) / kBM + a.seqs), (unsigned)heads);
+template <int D, typename T, int W>
+void start(PromptArgs a, hipStream_t stream) {
+    a.tiles = (a.rows_q + 32 * W - 1) / (32 * W) + a.seqs;
     const size_t lds = 4 * (size_t)kKeys * D * 2;
-    hipLaunchKernelGGL((attention_prompt_kernel<D, T>), grid, dim3(kThreads), lds, stream, a);
+    hipLaunchKernelGGL((attention_prompt_kernel<D, T, W>), dim3((unsigned)a.tiles, (unsigned)a.heads), dim3(64 * W), lds, stream, a);
+}
+
+template <typename T>
+void start(const PromptArgs& a, int d, hipStream_t stream) {
+    const bool few = ((a.rows_q + 255) / 256) * a.heads < 512;
+    if (d == 64) few ? start<64, T, 4>(a, stream) : start<64, T, 8>(a, stream);
+    else if (d == 128) few ? start<128, T, 4>(a, stream) : start<128, T, 8>(a, stream);
+    else start<256, T, 4>(a, stream);
 }
 
 }  // namespace
 
 hipError_t launch_attention_prompt(const pq2_attention_prompt_args& a, hipStream_t stream) {
+    const float scale2 = a.scale * kLog2e;
     const PromptArgs k{static_cast<const uint16_t*>(a.q), static_cast<const uint16_t*>(a.k),
                        static_cast<const uint16_t*>(a.v), static_cast<uint16_t*>(a.out), a.q_stride, a.q_head, a.k_stride,
                        a.k_head, a.v_stride, a.v_head, a.out_stride, a.out_head, a.starts_q, a.starts_k, (int)a.rows_q,
-                       (int)a.rows_k, (int)a.seqs, (int)(a.heads / a.kv_heads),
-                       (int)std::min<int64_t>(a.window, 0x40000000), a.causal, a.scale * kLog2e};
+                       (int)a.rows_k, (int)a.seqs, (int)a.heads, (int)(a.heads / a.kv_heads),
+                       (int)std::min<int64_t>(a.window, 0x40000000), a.causal, 0, scale2, kSlack / scale2};
     clear_stale_error();
-    const bool f16 = a.dtype == PQ2_F16;
-    if (a.head_dim == 64) f16 ? start<64, _Float16>(k, (int)a.heads, stream) : start<64, __bf16>(k, (int)a.heads, stream);
-    else if (a.head_dim == 128) f16 ? start<128, _Float16>(k, (int)a.heads, stream) : start<128, __bf16>(k, (int)a.heads, stream);
-    else f16 ? start<256, _Float16>(k, (int)a.heads, stream) : start<256, __bf16>(k, (int)a.heads, stream);
+    a.dtype == PQ2_F16 ? start<_Float16>(k, (int)a.head_dim, stream) : start<__bf16>(k, (int)a.head_dim, stream);
     return hipGetLastError();
 }
 
