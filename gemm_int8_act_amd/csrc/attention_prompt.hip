@@ -12,12 +12,14 @@
 #include "attention_internal.h"
 
 #include <algorithm>
+#include <utility>
 
 namespace pq2 {
 
 namespace {
 
 constexpr int kKeys = 64;           // keys of a step
+constexpr int kAhead = 4;           // products that an operand is read ahead
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 8.0f;      // weights grow to 2^8 before a row's reference moves
 
@@ -85,6 +87,16 @@ __device__ __forceinline__ void wait_loads() {
     __atomic_signal_fence(__ATOMIC_SEQ_CST);
     __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
     __atomic_signal_fence(__ATOMIC_SEQ_CST);
+}
+
+// f(0), f(1), ... f(N - 1), the index a constant in each.
+template <typename F, int... I>
+__device__ __forceinline__ void each_of(F&& f, std::integer_sequence<int, I...>) {
+    (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, typename F>
+__device__ __forceinline__ void each(F&& f) {
+    each_of(f, std::make_integer_sequence<int, N>{});
 }
 
 // The sequence and query tile of a workgroup: tiles of BM rows are counted
@@ -192,23 +204,39 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attention_prompt_ker
 #pragma unroll
     for (int d = 0; d < DB; ++d) acc[d] = v16f{};
     float m = -INFINITY, l = 0.0f;
-    v16f sc[2];
-    v8 p[2][2];
+    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+    u32x4 p[4];  // the weights, 16 keys each, as operands
 #pragma unroll
-    for (int b = 0; b < 2; ++b)
-#pragma unroll
-        for (int t = 0; t < 2; ++t) p[b][t] = v8{};
+    for (int f = 0; f < 4; ++f) p[f] = u32x4{};
 
-    auto scores = [&](int buf, v16f (&s2)[2]) {
-        const uint4* kt = lds + buf * (TILE / 16);
+    // Operand i of a step's products: the values' (b, t, d) for the last tile's
+    // weights, then the keys' (s, b) for the next tile's scores.  A lane's place
+    // depends on the swizzle in four ways; the rest is a constant offset.
+    constexpr int PV = 4 * DB, N = 2 * PV, RB = 2 * D;  // RB: bytes of a row
+    typedef __attribute__((address_space(3))) char lds_char;
+    lds_char* kat[4];
+    lds_char* vat[DB < 4 ? DB : 4];
+    {
+        const int r3 = (lane & 15) / 4, swz = D == 64 ? r3 >> 1 : r3;
 #pragma unroll
-        for (int b = 0; b < 2; ++b) s2[b] = v16f{};
+        for (int x = 0; x < 4; ++x) kat[x] = (lds_char*)lds + row * RB + 16 * ((2 * x + half) ^ (row & 7));
 #pragma unroll
-        for (int s = 0; s < D / 16; ++s)
-#pragma unroll
-            for (int b = 0; b < 2; ++b)
-                s2[b] = Half<T>::mfma(__builtin_bit_cast(v8, kt[k_chunk<D>(32 * b + row, 2 * s + half)]), qf[s], s2[b]);
+        for (int x = 0; x < (DB < 4 ? DB : 4); ++x)
+            vat[x] = (lds_char*)lds + 2 * TILE + (4 * half + r3) * RB +
+                     16 * (4 * (x ^ swz) + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1)) + 8 * (lane & 1);
+    }
+    auto operand = [&](int i, int buf) -> v8 {
+        if (i < PV) {
+            const int d = i % DB, bt = i / DB;
+            lds_char* at = vat[d % 4] + buf * TILE + 16 * bt * RB + 256 * (d / 4);
+            const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)at);
+            const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(at + 8 * RB));
+            return __builtin_bit_cast(v8, (s16x8)__builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
+        }
+        const int s = (i - PV) / 2, b = i % 2;
+        return *(__attribute__((address_space(3))) v8*)(kat[s % 4] + buf * TILE + 32 * b * RB + 128 * (s / 4));
     };
+    auto weights = [&](int f) { return __builtin_bit_cast(v8, p[f]); };
     auto mask = [&](int key0, v16f (&s2)[2]) {
         if (key0 + kKeys <= all_hi && key0 >= all_lo) return;
 #pragma unroll
@@ -219,25 +247,59 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attention_prompt_ker
                 if (key >= seen_hi || key < seen_lo) s2[b][r] = -INFINITY;
             }
     };
-    auto values = [&](int buf) {
-        const char* vt = reinterpret_cast<const char*>(lds) + (2 + buf) * TILE;
+    // One step: this tile's softmax (sc -> p), the last tile's values and the
+    // next tile's scores (-> next), which do not need each other, in turns; keys two tiles ahead and
+    // this tile's values are on their way meanwhile.  Operands are read kAhead products
+    // ahead.  A piece of p is written behind its last use for the last tile.
+    auto step = [&](int key0, int buf, v16f (&sc)[2], v16f (&next)[2]) {
+        v8 ring[kAhead];
 #pragma unroll
-        for (int b = 0; b < 2; ++b)
+        for (int i = 0; i < kAhead; ++i) ring[i] = operand(i, buf ^ 1);
+        if (key0 + 2 * kKeys < hi) fetch(kbase, a.k_stride, kcol, key0 + 2 * kKeys, buf * TILE);
+        fetch(vbase, a.v_stride, vcol, key0, (2 + buf) * TILE);
+        float top = -INFINITY, alpha = 1.0f, bias = 0.0f;
+        each<N>([&](auto at) {
+            constexpr int i = decltype(at)::value;
+            __builtin_amdgcn_sched_barrier(0);
+            if constexpr (i < PV) acc[i % DB] = Half<T>::mfma(ring[i % kAhead], weights(i / DB), acc[i % DB]);
+            else next[i % 2] = Half<T>::mfma(ring[i % kAhead], qf[(i - PV) / 2], i < PV + 2 ? v16f{} : next[i % 2]);
+            if constexpr (i + kAhead < N) ring[i % kAhead] = operand(i + kAhead, buf ^ 1);
+            if constexpr (i < N / 4) {
+                constexpr int E = 128 / N;  // scores a product
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
+                for (int e = i * E; e < i * E + E; ++e) top = fmaxf(top, sc[e / 16][e % 16]);
+            } else if constexpr (i == N / 4) {
+                top = max_halves(top);
+                const float old = m;
+                if (top > m + a.slack) m = top;
+                const float ref = m == -INFINITY ? 0.0f : m;
+                alpha = __builtin_amdgcn_exp2f((old - ref) * a.scale2);
+                bias = ref * a.scale2;
+                l *= alpha;
+            } else {
 #pragma unroll
-                for (int d = 0; d < DB; ++d) {
-                    s16x4 part[2];
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        const int vr = 32 * b + 16 * t + 8 * x + 4 * half + (lane & 15) / 4;
-                        const int col = 32 * d + 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
-                        part[x] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                            (__attribute__((address_space(3))) s16x4*)(vt + 16 * v_chunk<D>(vr, col / 8) + 2 * (col % 8)));
-                    }
-                    const s16x8 v = __builtin_shufflevector(part[0], part[1], 0, 1, 2, 3, 4, 5, 6, 7);
-                    acc[d] = Half<T>::mfma(__builtin_bit_cast(v8, v), p[b][t], acc[d]);
+                for (int k = 0; k < 16; ++k) {
+                    if (N / 4 + 1 + k * (3 * N / 4 - 1) / 16 != i) continue;
+                    const int b = k / 8, r = k % 8 * 2;
+                    const v2 e = {(T)__builtin_amdgcn_exp2f(__builtin_fmaf(sc[b][r], a.scale2, -bias)),
+                                  (T)__builtin_amdgcn_exp2f(__builtin_fmaf(sc[b][r + 1], a.scale2, -bias))};
+                    l = Half<T>::add2(e, l);
+                    uint32_t w = __builtin_bit_cast(uint32_t, e);
+                    asm volatile("" : "+v"(w));  // formed here, not where it is used
+                    p[k / 4][k % 4] = w;
                 }
+            }
+        });
+        __builtin_amdgcn_sched_barrier(0);
+        if (__any(alpha != 1.0f)) {
+            float f = alpha;
+            asm volatile("" : "+v"(f));  // or the products would be formed ahead of the branch
+#pragma unroll
+            for (int d = 0; d < DB; ++d) acc[d] *= f;
+        }
+        mask(key0 + kKeys, next);
+        wait_loads();
+        __syncthreads();
     };
 
     if (lo < hi) {
@@ -247,52 +309,26 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attention_prompt_ker
         if (lo + kKeys < hi) fetch(kbase, a.k_stride, kcol, lo + kKeys, TILE);
         wait_loads();
         __syncthreads();
-        scores(0, sc);
-        mask(lo, sc);
+        v16f even[2], odd[2];
+        each<PV>([&](auto at) {
+            constexpr int i = PV + decltype(at)::value;
+            even[i % 2] = Half<T>::mfma(operand(i, 0), qf[(i - PV) / 2], i < PV + 2 ? v16f{} : even[i % 2]);
+        });
+        mask(lo, even);
         __syncthreads();
-        int buf = 0;
-        for (int key0 = lo; key0 < hi; key0 += kKeys, buf ^= 1) {
-            // Keys two tiles ahead and this tile's values are on their way
-            // while the next tile's scores, this tile's softmax and the last
-            // tile's values, which do not need each other, are computed.
-            if (key0 + 2 * kKeys < hi) fetch(kbase, a.k_stride, kcol, key0 + 2 * kKeys, buf * TILE);
-            fetch(vbase, a.v_stride, vcol, key0, (2 + buf) * TILE);
-            v16f next[2];
-            scores(buf ^ 1, next);
-            values(buf ^ 1);
-            float top = sc[0][0];
-#pragma unroll
-            for (int b = 0; b < 2; ++b)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) top = fmaxf(top, sc[b][r]);
-            top = max_halves(top);
-            const float old = m;
-            if (top > m + a.slack) m = top;
-            const float ref = m == -INFINITY ? 0.0f : m;
-            const float alpha = __builtin_amdgcn_exp2f((old - ref) * a.scale2);
-            const float bias = ref * a.scale2;
-            l *= alpha;
-#pragma unroll
-            for (int b = 0; b < 2; ++b)
-#pragma unroll
-                for (int r = 0; r < 16; r += 2) {
-                    const v2 e = {(T)__builtin_amdgcn_exp2f(__builtin_fmaf(sc[b][r], a.scale2, -bias)),
-                                  (T)__builtin_amdgcn_exp2f(__builtin_fmaf(sc[b][r + 1], a.scale2, -bias))};
-                    l = Half<T>::add2(e, l);
-                    p[b][r / 8][r % 8] = e[0];
-                    p[b][r / 8][r % 8 + 1] = e[1];
-                }
-            if (__any(alpha != 1.0f)) {
-#pragma unroll
-                for (int d = 0; d < DB; ++d) acc[d] *= alpha;
-            }
-            sc[0] = next[0];
-            sc[1] = next[1];
-            mask(key0 + kKeys, sc);
-            wait_loads();
-            __syncthreads();
+        int key0 = lo, last = 0;
+        while (true) {
+            step(key0, 0, even, odd);
+            if ((key0 += kKeys) >= hi) break;
+            step(key0, 1, odd, even);
+            last = 1;
+            if ((key0 += kKeys) >= hi) break;
+            last = 0;
         }
-        values(buf ^ 1);
+        each<PV>([&](auto at) {
+            constexpr int i = decltype(at)::value;
+            acc[i % DB] = Half<T>::mfma(operand(i, last), weights(i / DB), acc[i % DB]);
+        });
     }
 
     l = sum_halves(l);
