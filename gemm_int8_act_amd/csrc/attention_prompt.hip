@@ -18,7 +18,7 @@ namespace pq2 {
 
 namespace {
 
-constexpr int kKeys = 64;           // keys of a step
+constexpr int kBufs = 4;            // tiles of keys, and of values, in LDS
 constexpr int kAhead = 4;           // products that an operand is read ahead
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 8.0f;      // weights grow to 2^8 before a row's reference moves
@@ -83,9 +83,12 @@ __device__ __forceinline__ void load_lds(i32x4_t rsrc, uint32_t voff, uint32_t l
                  : "memory", "m0");
 }
 
+// All but this wave's N most recent loads have arrived.
+template <int N>
 __device__ __forceinline__ void wait_loads() {
+    static_assert(N < 64, "vmcnt");
     __atomic_signal_fence(__ATOMIC_SEQ_CST);
-    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
+    __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | (N >> 4) << 14);  // vmcnt(N)
     __atomic_signal_fence(__ATOMIC_SEQ_CST);
 }
 
@@ -99,33 +102,24 @@ __device__ __forceinline__ void each(F&& f) {
     each_of(f, std::make_integer_sequence<int, N>{});
 }
 
-// The sequence and query tile of a workgroup: tiles of BM rows are counted
-// through the sequences, 64 of them a step; seq < 0 behind the last tile.
-struct Place {
-    int seq, tile, tiles;
-};
-
+// The first of a sequence's places among the workgroups of a head: places
+// starts[s] / BM + s, enough for its tiles of BM rows, whatever the lengths.
 template <int BM>
-__device__ __forceinline__ Place place_of(const int32_t* starts, int seqs, int index) {
+__device__ __forceinline__ int first_place(int start, int s) { return (int)((uint32_t)start / BM) + s; }
+
+// The sequence at `place`: the last one whose first place is not behind it, 64
+// sequences a step of the search.
+template <int BM>
+__device__ __forceinline__ int sequence_at(const int32_t* starts, int seqs, int place) {
     const int lane = threadIdx.x & 63;
-    for (int s0 = 0; s0 < seqs; s0 += 64) {
-        const int s = s0 + lane;
-        int tiles = 0;
-        if (s < seqs) tiles = (max(starts[s + 1] - starts[s], 0) + BM - 1) / BM;
-        int sum = tiles;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int o = __shfl_up(sum, d);
-            if (lane >= d) sum += o;
-        }
-        const int total = __shfl(sum, 63);
-        if (index < total) {
-            const int at = __ffsll(__ballot(sum > index)) - 1;
-            return {s0 + at, index - (__shfl(sum, at) - __shfl(tiles, at)), __shfl(tiles, at)};
-        }
-        index -= total;
+    int lo = 0, count = seqs;
+    while (true) {
+        const int step = (count + 63) >> 6, at = lane * step;
+        const bool below = at < count && first_place<BM>(starts[lo + at], lo + at) <= place;
+        lo += max((int)__popcll(__ballot(below)) - 1, 0) * step;
+        if (step == 1) return __builtin_amdgcn_readfirstlane(lo);
+        count = min(step, seqs - lo);
     }
-    return {-1, 0, 0};
 }
 
 // Workgroups go to the eight XCDs in turn: the one at `id` takes the item at
@@ -141,29 +135,30 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attention_prompt_ker
     typedef typename Half<T>::v2 v2;
     constexpr int BM = 32 * W;                   // query rows of a workgroup, 32 of them a wave's
     constexpr int DB = D / 32;
-    constexpr int TILE = kKeys * D * 2;          // bytes of a tile in LDS
+    constexpr int KT = D == 256 ? 32 : 64;       // keys of a step
+    constexpr int KB = KT / 32, NF = KT / 16;    // in blocks of the scores, in operands of the weights
+    constexpr int TILE = KT * D * 2;             // bytes of a tile in LDS
     constexpr int LOADS = TILE / 1024 / W;       // 1 KB loads of a wave for a tile
     constexpr int LROWS = 512 / D;               // rows of such a load
-    extern __shared__ uint4 lds[];               // K tiles 0 and 1, V tiles 0 and 1
+    extern __shared__ uint4 lds[];               // kBufs K tiles, kBufs V tiles
 
     // Items: heads of a key-value head next to each other, then its tiles.
     const int item = item_of(blockIdx.y * gridDim.x + blockIdx.x, gridDim.x * gridDim.y);
     const int per = a.tiles * a.group, kvh = item / per, head = kvh * a.group + item % a.group;
-    const Place place = place_of<BM>(a.starts_q, a.seqs, item % per / a.group);
-    if (place.seq < 0) return;
+    const int place = item % per / a.group, seq = a.seqs == 1 ? 0 : sequence_at<BM>(a.starts_q, a.seqs, place);
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int row = lane & 31, half = lane >> 5;
-    const int seq = __builtin_amdgcn_readfirstlane(place.seq);
-    const int tile = __builtin_amdgcn_readfirstlane(place.tiles - 1 - place.tile);  // the longest first
-
     // Queries and keys of the sequence, kept inside the tensors.
     const int qs = a.starts_q[seq], ks = a.starts_k[seq];
     const int nq = a.starts_q[seq + 1] - qs;
+    // The longest tile first; places behind a sequence's last tile have no work.
+    const int tile = (max(nq, 0) + BM - 1) / BM - 1 - (place - first_place<BM>(qs, seq));
+    if (tile < 0 || place < first_place<BM>(qs, seq)) return;
     const int nk = ks < 0 ? 0 : max(0, min(a.starts_k[seq + 1], a.rows_k) - ks);
     const int q0 = tile * BM;
     const int offset = nk - nq;  // a query's position is its index + offset
     const int hi = a.causal ? min(nk, offset + min(q0 + BM, nq)) : nk;
-    const int lo = a.window ? max(0, offset + q0 - a.window + 1) & ~(kKeys - 1) : 0;
+    const int lo = a.window ? max(0, offset + q0 - a.window + 1) & ~(KT - 1) : 0;
 
     const int qi = q0 + 32 * wave + row;
     const bool valid = qi < nq && qs + qi >= 0 && qs + qi < a.rows_q;
@@ -205,14 +200,14 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attention_prompt_ker
     for (int d = 0; d < DB; ++d) acc[d] = v16f{};
     float m = -INFINITY, l = 0.0f;
     typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-    u32x4 p[4];  // the weights, 16 keys each, as operands
+    u32x4 p[NF];  // the weights, 16 keys each, as operands
 #pragma unroll
-    for (int f = 0; f < 4; ++f) p[f] = u32x4{};
+    for (int f = 0; f < NF; ++f) p[f] = u32x4{};
 
     // Operand i of a step's products: the values' (b, t, d) for the last tile's
     // weights, then the keys' (s, b) for the next tile's scores.  A lane's place
     // depends on the swizzle in four ways; the rest is a constant offset.
-    constexpr int PV = 4 * DB, N = 2 * PV, RB = 2 * D;  // RB: bytes of a row
+    constexpr int PV = NF * DB, N = 2 * PV, RB = 2 * D;  // RB: bytes of a row
     typedef __attribute__((address_space(3))) char lds_char;
     lds_char* kat[4];
     lds_char* vat[DB < 4 ? DB : 4];
@@ -222,7 +217,7 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attention_prompt_ker
         for (int x = 0; x < 4; ++x) kat[x] = (lds_char*)lds + row * RB + 16 * ((2 * x + half) ^ (row & 7));
 #pragma unroll
         for (int x = 0; x < (DB < 4 ? DB : 4); ++x)
-            vat[x] = (lds_char*)lds + 2 * TILE + (4 * half + r3) * RB +
+            vat[x] = (lds_char*)lds + kBufs * TILE + (4 * half + r3) * RB +
                      16 * (4 * (x ^ swz) + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1)) + 8 * (lane & 1);
     }
     auto operand = [&](int i, int buf) -> v8 {
@@ -233,14 +228,14 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attention_prompt_ker
             const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(at + 8 * RB));
             return __builtin_bit_cast(v8, (s16x8)__builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
         }
-        const int s = (i - PV) / 2, b = i % 2;
+        const int s = (i - PV) / KB, b = i % KB;
         return *(__attribute__((address_space(3))) v8*)(kat[s % 4] + buf * TILE + 32 * b * RB + 128 * (s / 4));
     };
     auto weights = [&](int f) { return __builtin_bit_cast(v8, p[f]); };
-    auto mask = [&](int key0, v16f (&s2)[2]) {
-        if (key0 + kKeys <= all_hi && key0 >= all_lo) return;
+    auto mask = [&](int key0, v16f (&s2)[KB]) {
+        if (key0 + KT <= all_hi && key0 >= all_lo) return;
 #pragma unroll
-        for (int b = 0; b < 2; ++b)
+        for (int b = 0; b < KB; ++b)
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
                 const int key = key0 + 32 * b + 8 * (r / 4) + 4 * half + r % 4;
@@ -248,24 +243,32 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attention_prompt_ker
             }
     };
     // One step: this tile's softmax (sc -> p), the last tile's values and the
-    // next tile's scores (-> next), which do not need each other, in turns; keys two tiles ahead and
-    // this tile's values are on their way meanwhile.  Operands are read kAhead products
-    // ahead.  A piece of p is written behind its last use for the last tile.
-    auto step = [&](int key0, int buf, v16f (&sc)[2], v16f (&next)[2]) {
+    // next tile's scores (-> next), which do not need each other, in turns.
+    // Operands are read kAhead products ahead; a piece of p is written behind
+    // its last use for the last tile.  Keys four tiles ahead and values two
+    // tiles ahead go into the buffers that the step before read last, and are
+    // waited for two steps later (behind the last tile it is loaded again, so that the count of
+    // loads on their way is always the same).
+    const int last_tile = lo + (hi - 1 - lo) / KT * KT;
+    auto fetch_k = [&](int key0, int buf) { fetch(kbase, a.k_stride, kcol, min(key0, last_tile), buf * TILE); };
+    auto fetch_v = [&](int key0, int buf) { fetch(vbase, a.v_stride, vcol, min(key0, last_tile), (kBufs + buf) * TILE); };
+    auto step = [&](int key0, auto at_buf, v16f (&sc)[KB], v16f (&next)[KB]) {
+        constexpr int buf = decltype(at_buf)::value;       // of this tile
+        constexpr int kbuf = (buf + 1) % kBufs, vbuf = (buf + kBufs - 1) % kBufs;
         v8 ring[kAhead];
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) ring[i] = operand(i, buf ^ 1);
-        if (key0 + 2 * kKeys < hi) fetch(kbase, a.k_stride, kcol, key0 + 2 * kKeys, buf * TILE);
-        fetch(vbase, a.v_stride, vcol, key0, (2 + buf) * TILE);
+        for (int i = 0; i < kAhead; ++i) ring[i] = operand(i, vbuf);
+        fetch_k(key0 + 4 * KT, buf);
+        fetch_v(key0 + 2 * KT, (buf + 2) % kBufs);
         float top = -INFINITY, alpha = 1.0f, bias = 0.0f;
         each<N>([&](auto at) {
             constexpr int i = decltype(at)::value;
             __builtin_amdgcn_sched_barrier(0);
             if constexpr (i < PV) acc[i % DB] = Half<T>::mfma(ring[i % kAhead], weights(i / DB), acc[i % DB]);
-            else next[i % 2] = Half<T>::mfma(ring[i % kAhead], qf[(i - PV) / 2], i < PV + 2 ? v16f{} : next[i % 2]);
-            if constexpr (i + kAhead < N) ring[i % kAhead] = operand(i + kAhead, buf ^ 1);
+            else next[i % KB] = Half<T>::mfma(ring[i % kAhead], qf[(i - PV) / KB], i < PV + KB ? v16f{} : next[i % KB]);
+            if constexpr (i + kAhead < N) ring[i % kAhead] = operand(i + kAhead, i + kAhead < PV ? vbuf : kbuf);
             if constexpr (i < N / 4) {
-                constexpr int E = 128 / N;  // scores a product
+                constexpr int E = 64 * KB / N;  // scores a product
 #pragma unroll
                 for (int e = i * E; e < i * E + E; ++e) top = fmaxf(top, sc[e / 16][e % 16]);
             } else if constexpr (i == N / 4) {
@@ -278,8 +281,8 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attention_prompt_ker
                 l *= alpha;
             } else {
 #pragma unroll
-                for (int k = 0; k < 16; ++k) {
-                    if (N / 4 + 1 + k * (3 * N / 4 - 1) / 16 != i) continue;
+                for (int k = 0; k < 8 * KB; ++k) {
+                    if (N / 4 + 1 + k * (3 * N / 4 - 1) / (8 * KB) != i) continue;
                     const int b = k / 8, r = k % 8 * 2;
                     const v2 e = {(T)__builtin_amdgcn_exp2f(__builtin_fmaf(sc[b][r], a.scale2, -bias)),
                                   (T)__builtin_amdgcn_exp2f(__builtin_fmaf(sc[b][r + 1], a.scale2, -bias))};
@@ -297,33 +300,44 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attention_prompt_ker
 #pragma unroll
             for (int d = 0; d < DB; ++d) acc[d] *= f;
         }
-        mask(key0 + kKeys, next);
-        wait_loads();
+        mask(key0 + KT, next);
+        wait_loads<4 * LOADS>();
         __syncthreads();
     };
 
     if (lo < hi) {
         // Values before the first tile: zeros, for the first step's product.
-        for (int i = threadIdx.x; i < TILE / 16; i += 64 * W) lds[3 * (TILE / 16) + i] = make_uint4(0, 0, 0, 0);
-        fetch(kbase, a.k_stride, kcol, lo, 0);
-        if (lo + kKeys < hi) fetch(kbase, a.k_stride, kcol, lo + kKeys, TILE);
-        wait_loads();
+        for (int i = threadIdx.x; i < TILE / 16; i += 64 * W) lds[(2 * kBufs - 1) * (TILE / 16) + i] = make_uint4(0, 0, 0, 0);
+        fetch_k(lo, 0);
+        fetch_k(lo + KT, 1);
+        fetch_k(lo + 2 * KT, 2);
+        fetch_v(lo, 0);
+        fetch_k(lo + 3 * KT, 3);
+        fetch_v(lo + KT, 1);
+        wait_loads<4 * LOADS>();
         __syncthreads();
-        v16f even[2], odd[2];
+        v16f even[KB], odd[KB];
         each<PV>([&](auto at) {
             constexpr int i = PV + decltype(at)::value;
-            even[i % 2] = Half<T>::mfma(operand(i, 0), qf[(i - PV) / 2], i < PV + 2 ? v16f{} : even[i % 2]);
+            even[i % KB] = Half<T>::mfma(operand(i, 0), qf[(i - PV) / KB], i < PV + KB ? v16f{} : even[i % KB]);
         });
         mask(lo, even);
         __syncthreads();
         int key0 = lo, last = 0;
+        auto behind = [&](int buf) {
+            key0 += KT;
+            last = buf;
+            return key0 >= hi;
+        };
         while (true) {
-            step(key0, 0, even, odd);
-            if ((key0 += kKeys) >= hi) break;
-            step(key0, 1, odd, even);
-            last = 1;
-            if ((key0 += kKeys) >= hi) break;
-            last = 0;
+            step(key0, std::integral_constant<int, 0>{}, even, odd);
+            if (behind(0)) break;
+            step(key0, std::integral_constant<int, 1>{}, odd, even);
+            if (behind(1)) break;
+            step(key0, std::integral_constant<int, 2>{}, even, odd);
+            if (behind(2)) break;
+            step(key0, std::integral_constant<int, 3>{}, odd, even);
+            if (behind(3)) break;
         }
         each<PV>([&](auto at) {
             constexpr int i = decltype(at)::value;
@@ -348,7 +362,7 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attention_prompt_ker
 template <int D, typename T, int W>
 void start(PromptArgs a, hipStream_t stream) {
     a.tiles = (a.rows_q + 32 * W - 1) / (32 * W) + a.seqs;
-    const size_t lds = 4 * (size_t)kKeys * D * 2;
+    const size_t lds = 2 * kBufs * (size_t)(D == 256 ? 32 : 64) * D * 2;
     hipLaunchKernelGGL((attention_prompt_kernel<D, T, W>), dim3((unsigned)a.tiles, (unsigned)a.heads), dim3(64 * W), lds, stream, a);
 }
 
