@@ -31,6 +31,9 @@ constexpr int kTile = 32;                  // keys of a wave's step
 constexpr int kStep = kWaves * kTile;      // keys of a workgroup's step
 constexpr int kRows = 16;                  // query rows of a tile
 constexpr int kMaxSplits = 128;
+constexpr int kFan = 8;                    // parts that are joined first, of more than kJoin
+constexpr int kJoin = 16;                  // parts that are joined at once
+constexpr int kTileCounters = 1 + kMaxSplits / kFan;
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct PagedArgs {
@@ -112,13 +115,80 @@ __device__ __forceinline__ void load_dwords(const uint8_t* p, uint32_t (&w)[N]) 
     }
 }
 
+// Whether this workgroup is the last of `count` to come here, with all its
+// stores in memory.  The counter is zero again behind the last one.
+__device__ __forceinline__ bool last_of(uint32_t* counter, int count, int* shared) {
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        const uint32_t before = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        *shared = before == (uint32_t)(count - 1);
+        if (*shared) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    __syncthreads();
+    const bool last = *shared;
+    __syncthreads();
+    return last;
+}
+
+// `count` <= kJoin parts of a tile, every `every`th from `first` on, joined:
+// into the output (LAST), or into the first of them.  A thread takes four
+// columns of a row and reads all it needs at once, past the caches that other XCDs'
+// stores do not reach.
+template <int D, typename T, bool LAST>
+__device__ __forceinline__ void join(const PagedArgs& a, float* first, int count, int every, int r0, int start, int nq, int kvh) {
+    constexpr int kAgent = 16;  // cache policy bits of a load or store at agent scope
+    const int part_bytes = every * a.tile_rows * (D + 2) * 4;
+    const auto parts = make_rsrc(first, (uint32_t)(count * part_bytes));
+    for (int e = threadIdx.x; e < a.tile_rows * (D / 4); e += 64 * kWaves) {
+        const int row = e / (D / 4), dim = 4 * (e % (D / 4));
+        const int at = (row * D + dim) * 4, at_ml = (a.tile_rows * D + 2 * row) * 4;
+        u32x2_t ml[kJoin];
+        uint4 v[kJoin];
+#pragma unroll
+        for (int s = 0; s < kJoin; ++s) {
+            const int off = min(s, count - 1) * part_bytes;
+            ml[s] = __builtin_amdgcn_raw_buffer_load_b64(parts, off + at_ml, 0, kAgent);
+            v[s] = buf_load16<kAgent>(parts, (uint32_t)(off + at));
+        }
+        float top = -INFINITY;
+#pragma unroll
+        for (int s = 0; s < kJoin; ++s) top = fmaxf(top, __uint_as_float(ml[s][0]));
+        const float ref = top == -INFINITY ? 0.0f : top;
+        float l = 0.0f, sum[4] = {};
+#pragma unroll
+        for (int s = 0; s < kJoin; ++s) {
+            const float f = s < count ? __builtin_amdgcn_exp2f(__uint_as_float(ml[s][0]) - ref) : 0.0f;
+            l += __uint_as_float(ml[s][1]) * f;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) sum[c] += __uint_as_float(word_of(v[s], c)) * f;
+        }
+        if constexpr (LAST) {
+            const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+            const int i = (r0 + row) / a.group, g = r0 + row - i * a.group;
+            if (i >= nq || start + i < 0 || start + i >= a.rows) continue;
+            typedef T T4 __attribute__((ext_vector_type(4)));
+            T* o = reinterpret_cast<T*>(a.out) + (int64_t)(start + i) * a.out_stride + (int64_t)(kvh * a.group + g) * a.out_head + dim;
+            *reinterpret_cast<T4*>(o) = T4{(T)(sum[0] * inv), (T)(sum[1] * inv), (T)(sum[2] * inv), (T)(sum[3] * inv)};
+        } else {
+            // (A row's threads are of one wave, which has read all of the row
+            // before it writes.)
+            const u32x4_t w = {__float_as_uint(sum[0]), __float_as_uint(sum[1]), __float_as_uint(sum[2]), __float_as_uint(sum[3])};
+            __builtin_amdgcn_raw_buffer_store_b128(w, parts, at, 0, kAgent);
+            const u32x2_t w2 = {__float_as_uint(top), __float_as_uint(l)};
+            if (dim == 0) __builtin_amdgcn_raw_buffer_store_b64(w2, parts, at_ml, 0, kAgent);
+        }
+    }
+}
+
 template <int D, typename T>
 __global__ __launch_bounds__(64 * kWaves) void attention_paged_kernel(PagedArgs a) {
     typedef typename Half<T>::v8 v8;
     constexpr int F = D / 16;                 // 16-column pieces of the output
     __shared__ float red[kWaves][kRows][68];  // 64 columns of every wave's output
     __shared__ float2 wave_ml[kWaves][kRows];
-    __shared__ float part_w[kMaxSplits][kRows];
     __shared__ int last;
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -299,60 +369,19 @@ __global__ __launch_bounds__(64 * kWaves) void attention_paged_kernel(PagedArgs 
                            __builtin_bit_cast(unsigned long long, make_float2(row_m, row_l)), __ATOMIC_RELAXED,
                            __HIP_MEMORY_SCOPE_AGENT);
 
-    // The last workgroup of the tile joins its parts, in their order.
-    __atomic_signal_fence(__ATOMIC_SEQ_CST);
-    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): the stores have reached memory
-    __atomic_signal_fence(__ATOMIC_SEQ_CST);
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        const uint32_t before = __hip_atomic_fetch_add(a.counters + tile, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        last = before == (uint32_t)(parts - 1);
-        if (last) __hip_atomic_store(a.counters + tile, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    // The last workgroup of a tile joins its parts, in their order; of many
+    // parts, the last workgroup of each kFan first joins these (a compute unit alone
+    // reads about 20 GB/s: 64 parts of 4 KB would take it 13 us).
+    const bool two = parts > kJoin;
+    uint32_t* counters = a.counters + tile * kTileCounters;
+    if (two) {
+        const int g = split / kFan, count = min(kFan, parts - g * kFan);
+        if (!last_of(counters + 1 + g, count, &last)) return;
+        join<D, T, false>(a, a.partials + (tile * a.splits + g * kFan) * part_floats, count, 1, r0, start, nq, kvh);
     }
-    __syncthreads();
-    if (!last) return;
-    const float* first = a.partials + tile * a.splits * part_floats;
-    auto load2 = [](const float* p) {
-        return __builtin_bit_cast(float2, __hip_atomic_load(reinterpret_cast<const unsigned long long*>(p),
-                                                            __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
-    };
-    if (threadIdx.x < (unsigned)a.tile_rows) {
-        const int rr = threadIdx.x;
-        float top = -INFINITY, total = 0.0f;
-        for (int s = 0; s < parts; ++s) top = fmaxf(top, load2(first + s * part_floats + a.tile_rows * D + 2 * rr).x);
-        const float at = top == -INFINITY ? 0.0f : top;
-        for (int s = 0; s < parts; ++s) {
-            const float2 v = load2(first + s * part_floats + a.tile_rows * D + 2 * rr);
-            const float f = __builtin_amdgcn_exp2f(v.x - at);
-            part_w[s][rr] = f;
-            total += v.y * f;
-        }
-        const float norm = total > 0.0f ? 1.0f / total : 0.0f;
-        for (int s = 0; s < parts; ++s) part_w[s][rr] *= norm;
-    }
-    __syncthreads();
-    for (int e = threadIdx.x; e < a.tile_rows * (D / 2); e += 64 * kWaves) {
-        const int rr = e / (D / 2), dim = 2 * (e % (D / 2));
-        float2 sum = make_float2(0.0f, 0.0f);
-        for (int s0 = 0; s0 < parts; s0 += 8) {
-            float2 v[8];
-#pragma unroll
-            for (int x = 0; x < 8; ++x) v[x] = load2(first + min(s0 + x, parts - 1) * part_floats + rr * D + dim);
-#pragma unroll
-            for (int x = 0; x < 8; ++x)
-                if (s0 + x < parts) {
-                    const float f = part_w[s0 + x][rr];
-                    sum.x += v[x].x * f;
-                    sum.y += v[x].y * f;
-                }
-        }
-        const int oi = (r0 + rr) / a.group, og = r0 + rr - oi * a.group;
-        if (oi < nq && start + oi >= 0 && start + oi < a.rows) {
-            T* o = reinterpret_cast<T*>(a.out) + (int64_t)(start + oi) * a.out_stride + (int64_t)(kvh * a.group + og) * a.out_head + dim;
-            o[0] = (T)sum.x;
-            o[1] = (T)sum.y;
-        }
-    }
+    const int count = two ? (parts + kFan - 1) / kFan : parts;
+    if (!last_of(counters, count, &last)) return;
+    join<D, T, true>(a, a.partials + tile * a.splits * part_floats, count, two ? kFan : 1, r0, start, nq, kvh);
 }
 
 template <int D, typename T>
@@ -374,7 +403,7 @@ PagedPlan paged_plan(int64_t seqs, int64_t max_new, int64_t heads, int64_t kv_he
     p.splits = std::max<int64_t>(1, std::min({p.splits, (max_len + kStep - 1) / kStep, (int64_t)kMaxSplits}));
     p.min_chunk = base >= 256 ? 2 * kStep : kStep;
     p.partial_floats = p.splits > 1 ? base * p.splits * p.rows * (head_dim + 2) : 0;
-    p.counter_words = p.splits > 1 ? base : 0;
+    p.counter_words = p.splits > 1 ? base * kTileCounters : 0;
     return p;
 }
 
