@@ -35,6 +35,7 @@ constexpr int kFan = 8;                    // parts that are joined first, of mo
 constexpr int kJoin = 16;                  // parts that are joined at once
 constexpr int kTileCounters = 1 + kMaxSplits / kFan;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kSlack = 8.0f;             // weights grow to 2^8 before a row's reference moves
 
 struct PagedArgs {
     const uint16_t* q;
@@ -183,12 +184,14 @@ __device__ __forceinline__ void join(const PagedArgs& a, float* first, int count
     }
 }
 
-template <int D, typename T>
-__global__ __launch_bounds__(64 * kWaves) void attention_paged_kernel(PagedArgs a) {
+// RT: tiles of 16 query rows that share what a workgroup loads and widens.
+template <int D, typename T, int RT>
+__global__ __launch_bounds__(64 * kWaves, D == 256 || RT > 1 ? 2 : 4) void attention_paged_kernel(PagedArgs a) {
     typedef typename Half<T>::v8 v8;
     constexpr int F = D / 16;                 // 16-column pieces of the output
+    constexpr int ROWS = kRows * RT;
     __shared__ float red[kWaves][kRows][68];  // 64 columns of every wave's output
-    __shared__ float2 wave_ml[kWaves][kRows];
+    __shared__ float2 wave_ml[kWaves][ROWS];
     __shared__ int last;
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -200,102 +203,139 @@ __global__ __launch_bounds__(64 * kWaves) void attention_paged_kernel(PagedArgs 
     const int start = a.starts ? a.starts[seq] : seq;
     const int n = a.starts ? a.starts[seq + 1] - start : 1;
     const int nq = min(n, a.max_new);
-    const int r0 = rt * kRows, i0 = r0 / a.group;
+    const int r0 = rt * ROWS, i0 = r0 / a.group;
     if (i0 >= nq) return;
-    const int i1 = min(nq - 1, (r0 + kRows - 1) / a.group);
-    const int hi = min(len, len - n + i1 + 1);
-    const int lo = a.window ? max(0, len - n + i0 - a.window + 1) & ~15 : 0;
+    const int i1 = min(nq - 1, (r0 + ROWS - 1) / a.group);
+    const int first = len - n;  // the first new token's position
+    const int hi = min(len, first + i1 + 1);
+    const int lo = a.window ? max(0, first + i0 - a.window + 1) & ~15 : 0;
     const int span = max(0, hi - lo);
     const int chunk = max(a.min_chunk, ((span + a.splits - 1) / a.splits + kStep - 1) / kStep * kStep);
     const int parts = max(1, (span + chunk - 1) / chunk);
     if (split >= parts) return;
     const int k0 = lo + split * chunk, k1 = min(hi, k0 + chunk);
+    // Keys that every row sees.
+    const int all_hi = min(k1, first + i0 + 1), all_lo = a.window ? first + i1 - a.window + 1 : 0;
 
-    // This lane's query row.
-    const int r = r0 + j, i = r / a.group, g = r - i * a.group;
-    const bool valid = i < nq && start + i >= 0 && start + i < a.rows;
-    const int seen_hi = valid ? min(len, len - n + i + 1) : 0;
-    const int seen_lo = a.window ? max(0, len - n + i - a.window + 1) : 0;
-    v8 qf[D / 32];
-    if (valid) {
-        const uint16_t* q = a.q + (int64_t)(start + i) * a.q_stride + (int64_t)(kvh * a.group + g) * a.q_head + 16 * kb;
+    // This lane's query rows, one a tile.
+    int seen_hi[RT], seen_lo[RT];
+    v8 qf[RT][D / 32];
 #pragma unroll
-        for (int c = 0; c < D / 64; ++c) {
-            qf[2 * c] = *reinterpret_cast<const v8*>(q + 64 * c);
-            qf[2 * c + 1] = *reinterpret_cast<const v8*>(q + 64 * c + 8);
+    for (int t = 0; t < RT; ++t) {
+        const int r = r0 + 16 * t + j, i = r / a.group, g = r - i * a.group;
+        const bool valid = i < nq && start + i >= 0 && start + i < a.rows;
+        seen_hi[t] = valid ? min(len, first + i + 1) : 0;
+        seen_lo[t] = a.window ? first + i - a.window + 1 : 0;
+        const uint16_t* q = a.q + (int64_t)(valid ? start + i : 0) * a.q_stride + (int64_t)(kvh * a.group + (valid ? g : 0)) * a.q_head + 16 * kb;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+            const v8 v = *reinterpret_cast<const v8*>(q + 64 * (c / 2) + 8 * (c % 2));
+            qf[t][c] = valid ? v : v8{};
         }
-    } else {
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c) qf[c] = v8{};
     }
 
     const int64_t block_bytes = kv_block_bytes(1, D) << a.page_shift;
     const int32_t* table = a.table + seq * a.table_stride;
     const int page_mask = (1 << a.page_shift) - 1;
 
-    v4f acc[F];
+    v4f acc[RT][F];
+    float m[RT], ref[RT], l[RT];  // the weights' reference (-inf before the first key; 0 then), their sum
 #pragma unroll
-    for (int f = 0; f < F; ++f) acc[f] = v4f{0, 0, 0, 0};
-    float m = -INFINITY, l = 0.0f;
+    for (int t = 0; t < RT; ++t) {
+#pragma unroll
+        for (int f = 0; f < F; ++f) acc[t][f] = v4f{0, 0, 0, 0};
+        m[t] = -INFINITY;
+        ref[t] = l[t] = 0.0f;
+    }
+
+    // Pages of the two halves of a step's keys, -1 if not to be seen; looked up
+    // a step ahead.
+    auto page_of = [&](int key) { return key < k1 && (key >> a.page_shift) < a.table_pages ? table[key >> a.page_shift] : -1; };
+    int pages[2] = {page_of(k0 + wave * kTile), page_of(k0 + wave * kTile + 16)};
 
     for (int base = k0 + wave * kTile; base < k1; base += kStep) {
         Raw<D> w;
         bool there[2];
+        const int now[2] = {pages[0], pages[1]};
+        pages[0] = page_of(base + kStep);
+        pages[1] = page_of(base + kStep + 16);
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            const int key = base + 16 * s, idx = key >> a.page_shift;
-            const int page = key < k1 && idx < a.table_pages ? table[idx] : -1;
-            there[s] = page >= 0 && page < a.pages;
-            const int tok = key & page_mask;
-            const uint8_t* block = a.cache + ((int64_t)(there[s] ? page : 0) * a.kv_heads + kvh) * block_bytes;
+            there[s] = now[s] >= 0 && now[s] < a.pages;
+            const int tok = (base + 16 * s) & page_mask;
+            const uint8_t* block = a.cache + ((int64_t)(there[s] ? now[s] : 0) * a.kv_heads + kvh) * block_bytes;
             const uint8_t* kc = block + (int64_t)(tok + j) * D + 16 * kb;
             const uint8_t* vc = block + ((int64_t)D << a.page_shift) + (int64_t)(tok + 4 * kb) * D + F * j;
             const float* ks = reinterpret_cast<const float*>(block + ((int64_t)(2 * D) << a.page_shift)) + tok + 4 * kb;
 #pragma unroll
             for (int c = 0; c < D / 64; ++c) w.k[s][c] = *reinterpret_cast<const uint4*>(kc + 64 * c);
+            w.ks[s] = *reinterpret_cast<const float4*>(ks);
 #pragma unroll
             for (int x = 0; x < 4; ++x) load_dwords<D / 64>(vc + x * D, w.v[4 * s + x]);
-            w.ks[s] = *reinterpret_cast<const float4*>(ks);
             w.vs[s] = *reinterpret_cast<const float4*>(ks + (1 << a.page_shift));
         }
-        float p[8];
-        float top = -INFINITY;
+        v4f sc[RT][2];
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            v4f sc = {0, 0, 0, 0};
 #pragma unroll
-            for (int c = 0; c < D / 64; ++c) {
-                sc = Half<T>::mfma(widen<T>(w.k[s][c].x, w.k[s][c].y), qf[2 * c], sc);
-                sc = Half<T>::mfma(widen<T>(w.k[s][c].z, w.k[s][c].w), qf[2 * c + 1], sc);
-            }
-            const float ks[4] = {w.ks[s].x, w.ks[s].y, w.ks[s].z, w.ks[s].w};
+            for (int t = 0; t < RT; ++t) sc[t][s] = v4f{0, 0, 0, 0};
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                const int key = base + 16 * s + 4 * kb + x;
-                const bool seen = there[s] && key >= seen_lo && key < seen_hi;
-                p[4 * s + x] = seen ? sc[x] * (ks[x] * a.scale2) : -INFINITY;
-                top = fmaxf(top, p[4 * s + x]);
+            for (int c = 0; c < D / 32; ++c) {
+                const uint4 k = w.k[s][c / 2];
+                const v8 kf = c % 2 ? widen<T>(k.z, k.w) : widen<T>(k.x, k.y);
+#pragma unroll
+                for (int t = 0; t < RT; ++t) sc[t][s] = Half<T>::mfma(kf, qf[t][c], sc[t][s]);
             }
         }
-        top = fmaxf(m, max_row(top));
-        const float ref = top == -INFINITY ? 0.0f : top;
-        const float alpha = __builtin_amdgcn_exp2f(m - ref);
-        m = top;
-        l *= alpha;
+        // Scores scaled; where not every row sees every key, the hidden ones'
+        // are -inf and the rows' own copies of the value scales 0 (a hidden key's may be anything).
+        const float ks[8] = {w.ks[0].x * a.scale2, w.ks[0].y * a.scale2, w.ks[0].z * a.scale2, w.ks[0].w * a.scale2,
+                             w.ks[1].x * a.scale2, w.ks[1].y * a.scale2, w.ks[1].z * a.scale2, w.ks[1].w * a.scale2};
+        float vs[RT][8];
 #pragma unroll
-        for (int f = 0; f < F; ++f) acc[f] *= alpha;
-        bf16x8 ph, pl;
+        for (int t = 0; t < RT; ++t)
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            const float vs[4] = {w.vs[s].x, w.vs[s].y, w.vs[s].z, w.vs[s].w};
+            for (int x = 0; x < 8; ++x) {
+                const float4 v = w.vs[x / 4];
+                vs[t][x] = x % 4 == 0 ? v.x : x % 4 == 1 ? v.y : x % 4 == 2 ? v.z : v.w;
+                sc[t][x / 4][x % 4] *= ks[x];
+            }
+        if (!(there[0] && there[1] && base + kTile <= all_hi && base >= all_lo)) {
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                const float e = __builtin_amdgcn_exp2f(p[4 * s + x] - ref);
-                l += e;
-                // (A masked key's scale may be anything.)
-                const float ev = p[4 * s + x] == -INFINITY ? 0.0f : e * vs[x];
-                ph[4 * s + x] = (__bf16)ev;
-                pl[4 * s + x] = (__bf16)(ev - (float)ph[4 * s + x]);
+            for (int t = 0; t < RT; ++t)
+#pragma unroll
+                for (int x = 0; x < 8; ++x) {
+                    const int key = base + 16 * (x / 4) + 4 * kb + x % 4;
+                    if (!(there[x / 4] && key >= seen_lo[t] && key < seen_hi[t])) {
+                        sc[t][x / 4][x % 4] = -INFINITY;
+                        vs[t][x] = 0.0f;
+                    }
+                }
+        }
+        bf16x8 ph[RT], pl[RT];
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+            float top = -INFINITY;
+#pragma unroll
+            for (int x = 0; x < 8; ++x) top = fmaxf(top, sc[t][x / 4][x % 4]);
+            // The reference moves only when a score passes it by far.
+            if (__any(top > m[t] + kSlack)) {
+                top = max_row(top);
+                const float old = m[t];
+                if (top > old + kSlack) m[t] = top;
+                ref[t] = m[t] == -INFINITY ? 0.0f : m[t];
+                float alpha = __builtin_amdgcn_exp2f(old - ref[t]);
+                l[t] *= alpha;
+#pragma unroll
+                for (int f = 0; f < F; ++f) acc[t][f] *= alpha;
+            }
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+                const float e = __builtin_amdgcn_exp2f(sc[t][x / 4][x % 4] - ref[t]);
+                l[t] += e;
+                const float ev = e * vs[t][x];
+                ph[t][x] = (__bf16)ev;
+                pl[t][x] = (__bf16)(ev - (float)ph[t][x]);
             }
         }
 #pragma unroll
@@ -303,71 +343,79 @@ __global__ __launch_bounds__(64 * kWaves) void attention_paged_kernel(PagedArgs 
             bf16x8 v;
 #pragma unroll
             for (int x = 0; x < 8; ++x) v[x] = (__bf16)code_at(w.v[x][f / 4], f % 4);
-            acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, ph, acc[f], 0, 0, 0);
-            acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, pl, acc[f], 0, 0, 0);
+#pragma unroll
+            for (int t = 0; t < RT; ++t) {
+                acc[t][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, ph[t], acc[t][f], 0, 0, 0);
+                acc[t][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, pl[t], acc[t][f], 0, 0, 0);
+            }
         }
     }
 
-    // The waves' parts joined: each scales its own to the common maximum.
-    l = sum_row(l);
-    if (kb == 0) wave_ml[wave][j] = make_float2(m, l);
+    // The waves' parts joined: each scales its own to the common reference.
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+        l[t] = sum_row(l[t]);
+        if (kb == 0) wave_ml[wave][16 * t + j] = make_float2(m[t], l[t]);
+    }
     __syncthreads();
-    float common = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) common = fmaxf(common, wave_ml[w][j].x);
-    const float ref = common == -INFINITY ? 0.0f : common;
-    const float mine = __builtin_amdgcn_exp2f(m - ref);
-
-    // Thread (row, cols): two neighbouring columns of the 64 of each round.
-    const int row = threadIdx.x >> 5, pair = threadIdx.x & 31;
-    float row_m = -INFINITY, row_l = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) row_m = fmaxf(row_m, wave_ml[w][row].x);
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w)
-        row_l += wave_ml[w][row].y * __builtin_amdgcn_exp2f(wave_ml[w][row].x - (row_m == -INFINITY ? 0.0f : row_m));
-    const float inv = row_l > 0.0f ? 1.0f / row_l : 0.0f;
-    const int out_i = (r0 + row) / a.group, out_g = r0 + row - out_i * a.group;
-    const bool out_valid = out_i < nq && start + out_i >= 0 && start + out_i < a.rows;
-    T* out = reinterpret_cast<T*>(a.out) + (int64_t)(start + out_i) * a.out_stride +
-             (int64_t)(kvh * a.group + out_g) * a.out_head;
     const int64_t tile = ((int64_t)seq * a.kv_heads + kvh) * a.row_tiles + rt;
     const int64_t part_floats = (int64_t)a.tile_rows * (D + 2);
     float* part = a.partials + (tile * a.splits + split) * part_floats;
-    const bool keep = row < a.tile_rows;
 #pragma unroll
-    for (int round = 0; round < F / 4; ++round) {
-        if (round) __syncthreads();
+    for (int t = 0; t < RT; ++t) {
+        float common = -INFINITY;
 #pragma unroll
-        for (int x = 0; x < 4; ++x)
-            *reinterpret_cast<float4*>(&red[wave][j][4 * (4 * kb + x)]) =
-                make_float4(acc[4 * round][x] * mine, acc[4 * round + 1][x] * mine, acc[4 * round + 2][x] * mine,
-                            acc[4 * round + 3][x] * mine);
-        __syncthreads();
-        float2 sum = make_float2(0.0f, 0.0f);
+        for (int w = 0; w < kWaves; ++w) common = fmaxf(common, wave_ml[w][16 * t + j].x);
+        const float mine = __builtin_amdgcn_exp2f(m[t] - (common == -INFINITY ? 0.0f : common));
+
+        // Thread (row, pair): two neighbouring columns of the 64 of each round.
+        const int row = 16 * t + (threadIdx.x >> 5), pair = threadIdx.x & 31;
+        float row_m = -INFINITY, row_l = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) {
-            const float2 v = *reinterpret_cast<const float2*>(&red[w][row][2 * pair]);
-            sum.x += v.x;
-            sum.y += v.y;
-        }
-        // Column c of the round's 64: dimension F (c / 4) + 4 round + c % 4.
-        const int dim = F * (pair >> 1) + 4 * round + 2 * (pair & 1);
-        if (parts == 1) {
-            if (out_valid) {
-                out[dim] = (T)(sum.x * inv);
-                out[dim + 1] = (T)(sum.y * inv);
+        for (int w = 0; w < kWaves; ++w) row_m = fmaxf(row_m, wave_ml[w][row].x);
+        const float row_ref = row_m == -INFINITY ? 0.0f : row_m;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) row_l += wave_ml[w][row].y * __builtin_amdgcn_exp2f(wave_ml[w][row].x - row_ref);
+        const float inv = row_l > 0.0f ? 1.0f / row_l : 0.0f;
+        const int out_i = (r0 + row) / a.group, out_g = r0 + row - out_i * a.group;
+        const bool out_valid = out_i < nq && start + out_i >= 0 && start + out_i < a.rows;
+        T* out = reinterpret_cast<T*>(a.out) + (int64_t)(start + out_i) * a.out_stride +
+                 (int64_t)(kvh * a.group + out_g) * a.out_head;
+        const bool keep = row < a.tile_rows;
+#pragma unroll
+        for (int round = 0; round < F / 4; ++round) {
+            if (t || round) __syncthreads();
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+                *reinterpret_cast<float4*>(&red[wave][j][4 * (4 * kb + x)]) =
+                    make_float4(acc[t][4 * round][x] * mine, acc[t][4 * round + 1][x] * mine, acc[t][4 * round + 2][x] * mine,
+                                acc[t][4 * round + 3][x] * mine);
+            __syncthreads();
+            float2 sum = make_float2(0.0f, 0.0f);
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) {
+                const float2 v = *reinterpret_cast<const float2*>(&red[w][threadIdx.x >> 5][2 * pair]);
+                sum.x += v.x;
+                sum.y += v.y;
             }
-        } else if (keep) {
-            __hip_atomic_store(reinterpret_cast<unsigned long long*>(part + row * D + dim),
-                               __builtin_bit_cast(unsigned long long, sum), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            // Column c of the round's 64: dimension F (c / 4) + 4 round + c % 4.
+            const int dim = F * (pair >> 1) + 4 * round + 2 * (pair & 1);
+            if (parts == 1) {
+                if (out_valid) {
+                    typedef T T2 __attribute__((ext_vector_type(2)));
+                    *reinterpret_cast<T2*>(out + dim) = T2{(T)(sum.x * inv), (T)(sum.y * inv)};
+                }
+            } else if (keep) {
+                __hip_atomic_store(reinterpret_cast<unsigned long long*>(part + row * D + dim),
+                                   __builtin_bit_cast(unsigned long long, sum), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            }
         }
+        if (parts > 1 && keep && pair == 0)
+            __hip_atomic_store(reinterpret_cast<unsigned long long*>(part + a.tile_rows * D + 2 * row),
+                               __builtin_bit_cast(unsigned long long, make_float2(row_m, row_l)), __ATOMIC_RELAXED,
+                               __HIP_MEMORY_SCOPE_AGENT);
     }
     if (parts == 1) return;
-    if (keep && pair == 0)
-        __hip_atomic_store(reinterpret_cast<unsigned long long*>(part + a.tile_rows * D + 2 * row),
-                           __builtin_bit_cast(unsigned long long, make_float2(row_m, row_l)), __ATOMIC_RELAXED,
-                           __HIP_MEMORY_SCOPE_AGENT);
 
     // The last workgroup of a tile joins its parts, in their order; of many
     // parts, the last workgroup of each kFan first joins these (a compute unit alone
@@ -387,7 +435,8 @@ __global__ __launch_bounds__(64 * kWaves) void attention_paged_kernel(PagedArgs 
 template <int D, typename T>
 void start(const PagedArgs& a, int64_t seqs, hipStream_t stream) {
     const dim3 grid((unsigned)a.splits, (unsigned)(a.kv_heads * a.row_tiles), (unsigned)seqs);
-    hipLaunchKernelGGL((attention_paged_kernel<D, T>), grid, dim3(64 * kWaves), 0, stream, a);
+    if (D == 256 || a.tile_rows <= kRows) hipLaunchKernelGGL((attention_paged_kernel<D, T, 1>), grid, dim3(64 * kWaves), 0, stream, a);
+    else hipLaunchKernelGGL((attention_paged_kernel<D, T, D == 256 ? 1 : 2>), grid, dim3(64 * kWaves), 0, stream, a);
 }
 
 }  // namespace
@@ -396,10 +445,12 @@ PagedPlan paged_plan(int64_t seqs, int64_t max_new, int64_t heads, int64_t kv_he
                      int64_t max_len) {
     PagedPlan p;
     const int64_t rows = max_new * (heads / kv_heads);
-    p.rows = std::min<int64_t>(rows, kRows);
-    p.row_tiles = (rows + kRows - 1) / kRows;
+    const int64_t most = rows > kRows && head_dim != 256 ? 2 * kRows : kRows;
+    const int64_t resident = head_dim == 256 || most > kRows ? 256 : 512;  // workgroups that run at once
+    p.rows = std::min<int64_t>(rows, most);
+    p.row_tiles = (rows + most - 1) / most;
     const int64_t base = seqs * kv_heads * p.row_tiles;
-    p.splits = std::max((512 + base - 1) / base, (max_len + 2047) / 2048);
+    p.splits = std::max(resident / base, (max_len + 2047) / 2048);
     p.splits = std::max<int64_t>(1, std::min({p.splits, (max_len + kStep - 1) / kStep, (int64_t)kMaxSplits}));
     p.min_chunk = base >= 256 ? 2 * kStep : kStep;
     p.partial_floats = p.splits > 1 ? base * p.splits * p.rows * (head_dim + 2) : 0;
