@@ -66,7 +66,8 @@ int check_strides(int64_t rows, int64_t heads, int64_t d, int64_t stride, int64_
 bool paged_sizes_ok(int64_t seqs, int64_t max_new, int64_t heads, int64_t kv_heads, int64_t head_dim,
                     int64_t max_len) {
     return seqs >= 1 && seqs <= PQ2_MAX_ATTN_SEQS && max_new >= 1 && max_new <= PQ2_MAX_ATTN_ROWS &&
-           heads_ok(heads, kv_heads) && dim_ok(head_dim) && max_len >= 1 && max_len <= kMaxIndex;
+           heads_ok(heads, kv_heads) && dim_ok(head_dim) && max_len >= 1 && max_len <= kMaxIndex &&
+           seqs * kv_heads * ((max_new * (heads / kv_heads) + 15) / 16) <= ((int64_t)1 << 23);
 }
 
 }  // namespace
@@ -193,7 +194,6 @@ int pq2_attention_paged(const pq2_attention_paged_args* a, void* stream) {
     if (rq == PQ2_ESHAPE || ro == PQ2_ESHAPE) return PQ2_ESHAPE;
     const pq2::PagedPlan plan = pq2::paged_plan(a->seqs, a->max_new, a->heads, a->kv_heads, d, a->max_len);
     if (plan.splits > 1 && (!a->partials || !a->counters)) return PQ2_EINVAL;
-    if (plan.row_tiles * a->kv_heads > 65535 || plan.splits > 65535) return PQ2_ESHAPE;
     if (rq || ro || !aligned(a->q, 16) || !aligned(a->out, 16) || !aligned(a->cache, 16) || !aligned(a->table, 4) ||
         !aligned(a->lens, 4) || !aligned(a->starts, 4) || !aligned(a->partials, 16) || !aligned(a->counters, 4))
         return PQ2_EALIGN;

@@ -49,7 +49,8 @@ struct PagedArgs {
     uint32_t* counters;
     int64_t table_stride;
     int rows, table_pages, kv_heads, group, pages, page_shift, max_new, window, splits, row_tiles, tile_rows, min_chunk;
-    float scale2;  // scale * log2(e)
+    uint32_t items;  // (sequence, key-value head, part)
+    float scale2;    // scale * log2(e)
 };
 
 template <typename T> struct Half;
@@ -196,14 +197,19 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 || RT > 1 ? 2 : 4) void atten
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int j = lane & 15, kb = lane >> 4;
-    const int split = blockIdx.x, kvh = blockIdx.y / a.row_tiles, rt = blockIdx.y % a.row_tiles, seq = blockIdx.z;
+    // Workgroups go to the eight XCDs in turn: the row tiles that read the same
+    // keys follow each other on one of them.
+    const uint32_t id = blockIdx.y * gridDim.x + blockIdx.x, turn = id >> 3;
+    const uint32_t rt = turn % a.row_tiles, item = turn / a.row_tiles * 8 + (id & 7);
+    if (item >= a.items) return;
+    const int split = item % a.splits, kvh = item / a.splits % a.kv_heads, seq = item / a.splits / a.kv_heads;
 
     // The sequence, this tile's rows and the keys that any of them sees.
     const int len = max(0, (int)min((int64_t)a.lens[seq], (int64_t)a.table_pages << a.page_shift));
     const int start = a.starts ? a.starts[seq] : seq;
     const int n = a.starts ? a.starts[seq + 1] - start : 1;
     const int nq = min(n, a.max_new);
-    const int r0 = rt * ROWS, i0 = r0 / a.group;
+    const int r0 = (int)rt * ROWS, i0 = r0 / a.group;
     if (i0 >= nq) return;
     const int i1 = min(nq - 1, (r0 + ROWS - 1) / a.group);
     const int first = len - n;  // the first new token's position
@@ -251,29 +257,46 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 || RT > 1 ? 2 : 4) void atten
     // Pages of the two halves of a step's keys, -1 if not to be seen; looked up
     // a step ahead.
     auto page_of = [&](int key) { return key < k1 && (key >> a.page_shift) < a.table_pages ? table[key >> a.page_shift] : -1; };
-    int pages[2] = {page_of(k0 + wave * kTile), page_of(k0 + wave * kTile + 16)};
+    const int base0 = k0 + wave * kTile;
+    int pages[2] = {page_of(base0), page_of(base0 + 16)};
 
-    for (int base = k0 + wave * kTile; base < k1; base += kStep) {
-        Raw<D> w;
-        bool there[2];
-        const int now[2] = {pages[0], pages[1]};
-        pages[0] = page_of(base + kStep);
-        pages[1] = page_of(base + kStep + 16);
+    // The next step's keys are loaded into the registers of this step's as soon
+    // as its scores are formed, its values behind the output's products: either
+    // arrives while the other half of a step is computed.
+    Raw<D> w;
+    bool there[2];
+    auto block_of = [&](int page) { return a.cache + ((int64_t)(page >= 0 && page < a.pages ? page : 0) * a.kv_heads + kvh) * block_bytes; };
+    auto load_k = [&](int base) {
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            there[s] = now[s] >= 0 && now[s] < a.pages;
             const int tok = (base + 16 * s) & page_mask;
-            const uint8_t* block = a.cache + ((int64_t)(there[s] ? now[s] : 0) * a.kv_heads + kvh) * block_bytes;
+            const uint8_t* block = block_of(pages[s]);
             const uint8_t* kc = block + (int64_t)(tok + j) * D + 16 * kb;
-            const uint8_t* vc = block + ((int64_t)D << a.page_shift) + (int64_t)(tok + 4 * kb) * D + F * j;
-            const float* ks = reinterpret_cast<const float*>(block + ((int64_t)(2 * D) << a.page_shift)) + tok + 4 * kb;
 #pragma unroll
             for (int c = 0; c < D / 64; ++c) w.k[s][c] = *reinterpret_cast<const uint4*>(kc + 64 * c);
-            w.ks[s] = *reinterpret_cast<const float4*>(ks);
+            w.ks[s] = *reinterpret_cast<const float4*>(block + ((int64_t)(2 * D) << a.page_shift) + (tok + 4 * kb) * 4);
+        }
+    };
+    auto load_v = [&](int base) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const int tok = (base + 16 * s) & page_mask;
+            const uint8_t* block = block_of(pages[s]);
+            const uint8_t* vc = block + ((int64_t)D << a.page_shift) + (int64_t)(tok + 4 * kb) * D + F * j;
 #pragma unroll
             for (int x = 0; x < 4; ++x) load_dwords<D / 64>(vc + x * D, w.v[4 * s + x]);
-            w.vs[s] = *reinterpret_cast<const float4*>(ks + (1 << a.page_shift));
+            w.vs[s] = *reinterpret_cast<const float4*>(block + ((int64_t)(2 * D + 4) << a.page_shift) + (tok + 4 * kb) * 4);
         }
+    };
+    if (base0 < k1) {
+        load_k(base0);
+        load_v(base0);
+    }
+    for (int base = base0; base < k1; base += kStep) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s) there[s] = pages[s] >= 0 && pages[s] < a.pages;
+        pages[0] = page_of(base + kStep);
+        pages[1] = page_of(base + kStep + 16);
         v4f sc[RT][2];
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
@@ -291,6 +314,9 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 || RT > 1 ? 2 : 4) void atten
         // are -inf and the rows' own copies of the value scales 0 (a hidden key's may be anything).
         const float ks[8] = {w.ks[0].x * a.scale2, w.ks[0].y * a.scale2, w.ks[0].z * a.scale2, w.ks[0].w * a.scale2,
                              w.ks[1].x * a.scale2, w.ks[1].y * a.scale2, w.ks[1].z * a.scale2, w.ks[1].w * a.scale2};
+        __builtin_amdgcn_sched_barrier(0);
+        if (base + kStep < k1) load_k(base + kStep);
+        __builtin_amdgcn_sched_barrier(0);
         float vs[RT][8];
 #pragma unroll
         for (int t = 0; t < RT; ++t)
@@ -349,6 +375,8 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 || RT > 1 ? 2 : 4) void atten
                 acc[t][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, pl[t], acc[t][f], 0, 0, 0);
             }
         }
+        __builtin_amdgcn_sched_barrier(0);
+        if (base + kStep < k1) load_v(base + kStep);
     }
 
     // The waves' parts joined: each scales its own to the common reference.
@@ -433,8 +461,10 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 || RT > 1 ? 2 : 4) void atten
 }
 
 template <int D, typename T>
-void start(const PagedArgs& a, int64_t seqs, hipStream_t stream) {
-    const dim3 grid((unsigned)a.splits, (unsigned)(a.kv_heads * a.row_tiles), (unsigned)seqs);
+void start(PagedArgs a, int64_t seqs, hipStream_t stream) {
+    a.items = (uint32_t)(a.splits * a.kv_heads * seqs);
+    const int64_t total = (int64_t)((a.items + 7) / 8 * 8) * a.row_tiles, wide = std::min<int64_t>(total, 1 << 20);
+    const dim3 grid((unsigned)wide, (unsigned)((total + wide - 1) / wide));
     if (D == 256 || a.tile_rows <= kRows) hipLaunchKernelGGL((attention_paged_kernel<D, T, 1>), grid, dim3(64 * kWaves), 0, stream, a);
     else hipLaunchKernelGGL((attention_paged_kernel<D, T, D == 256 ? 1 : 2>), grid, dim3(64 * kWaves), 0, stream, a);
 }
@@ -464,7 +494,7 @@ hipError_t launch_attention_paged(const pq2_attention_paged_args& a, const Paged
                       a.partials, a.counters, a.table_stride, (int)a.rows, (int)a.table_pages, (int)a.kv_heads,
                       (int)(a.heads / a.kv_heads), (int)a.pages, log2_of(a.page_tokens), (int)a.max_new,
                       (int)std::min<int64_t>(a.window, 0x40000000), (int)plan.splits, (int)plan.row_tiles, (int)plan.rows,
-                      (int)plan.min_chunk, a.scale * kLog2e};
+                      (int)plan.min_chunk, 0, a.scale * kLog2e};
     clear_stale_error();
     const bool f16 = a.dtype == PQ2_F16;
     if (a.head_dim == 64) f16 ? start<64, _Float16>(k, a.seqs, stream) : start<64, __bf16>(k, a.seqs, stream);

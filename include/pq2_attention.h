@@ -162,7 +162,7 @@ int pq2_attention_paged_workspace(int64_t seqs, int64_t max_new, int64_t heads, 
                                   int64_t max_len, int64_t* partials, int64_t* counters);
 
 /* Errors: EINVAL (null, dtype, scale, window < 0, overlap), ESHAPE (sizes; heads % kv_heads; rows != seqs without
- *         starts), EALIGN, ELAUNCH, EDEVICE. */
+ *         starts; more than 2^23 tiles of 16 query rows: seqs * kv_heads * ceil(max_new * heads / kv_heads / 16)), EALIGN, ELAUNCH, EDEVICE. */
 int pq2_attention_paged(const pq2_attention_paged_args* args, void* stream);
 
 /* ---- Attention over packed prompts

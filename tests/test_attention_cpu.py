@@ -155,7 +155,7 @@ REFUSED = {
         (ESHAPE, dict(max_len=0)), (ESHAPE, dict(heads=9)), (ESHAPE, dict(kv_heads=3)), (ESHAPE, dict(head_dim=80)),
         (ESHAPE, dict(rows=0)), (ESHAPE, dict(page_tokens=20)), (ESHAPE, dict(pages=0)), (ESHAPE, dict(table_pages=0)),
         (ESHAPE, dict(table_stride=299)), (ESHAPE, dict(table_pages=1 << 27, table_stride=1 << 27)), (ESHAPE, dict(q_stride=512)),
-        (ESHAPE, dict(max_new=1 << 20)), (EALIGN, dict(q_stride=1028)), (EALIGN, dict(q=A + 8)), (EALIGN, dict(out=B + 4)),
+        (ESHAPE, dict(max_new=1 << 24, seqs=65535)), (EALIGN, dict(q_stride=1028)), (EALIGN, dict(q=A + 8)), (EALIGN, dict(out=B + 4)),
         (EALIGN, dict(cache=C + 8)), (EALIGN, dict(table=D + 2)), (EALIGN, dict(lens=E + 1)), (EALIGN, dict(starts=F + 2)),
         (EALIGN, dict(partials=G + 4)), (EALIGN, dict(counters=H + 2)), (EINVAL, dict(out=A)), (EINVAL, dict(out=C)),
         (EINVAL, dict(out=E)), (EINVAL, dict(partials=A)), (EINVAL, dict(counters=G)), (EINVAL, dict(counters=D)),
