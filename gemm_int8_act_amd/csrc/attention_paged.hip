@@ -26,13 +26,14 @@ namespace pq2 {
 
 namespace {
 
-constexpr int kWaves = 8;
+constexpr int kWaves = 4;
 constexpr int kTile = 32;                  // keys of a wave's step
 constexpr int kStep = kWaves * kTile;      // keys of a workgroup's step
 constexpr int kRows = 16;                  // query rows of a tile
 constexpr int kMaxSplits = 128;
 constexpr int kFan = 8;                    // parts that are joined first, of more than kJoin
 constexpr int kJoin = 16;                  // parts that are joined at once
+constexpr int kAgent = 16;                 // cache policy of a load or store at agent scope
 constexpr int kTileCounters = 1 + kMaxSplits / kFan;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 8.0f;             // weights grow to 2^8 before a row's reference moves
@@ -49,8 +50,7 @@ struct PagedArgs {
     uint32_t* counters;
     int64_t table_stride;
     int rows, table_pages, kv_heads, group, pages, page_shift, max_new, window, splits, row_tiles, tile_rows, min_chunk;
-    uint32_t items;  // (sequence, key-value head, part)
-    float scale2;    // scale * log2(e)
+    float scale2;  // scale * log2(e)
 };
 
 template <typename T> struct Half;
@@ -141,7 +141,6 @@ __device__ __forceinline__ bool last_of(uint32_t* counter, int count, int* share
 // stores do not reach.
 template <int D, typename T, bool LAST>
 __device__ __forceinline__ void join(const PagedArgs& a, float* first, int count, int every, int r0, int start, int nq, int kvh) {
-    constexpr int kAgent = 16;  // cache policy bits of a load or store at agent scope
     const int part_bytes = every * a.tile_rows * (D + 2) * 4;
     const auto parts = make_rsrc(first, (uint32_t)(count * part_bytes));
     for (int e = threadIdx.x; e < a.tile_rows * (D / 4); e += 64 * kWaves) {
@@ -197,19 +196,17 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 || RT > 1 ? 2 : 4) void atten
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int j = lane & 15, kb = lane >> 4;
-    // Workgroups go to the eight XCDs in turn: the row tiles that read the same
-    // keys follow each other on one of them.
-    const uint32_t id = blockIdx.y * gridDim.x + blockIdx.x, turn = id >> 3;
-    const uint32_t rt = turn % a.row_tiles, item = turn / a.row_tiles * 8 + (id & 7);
-    if (item >= a.items) return;
-    const int split = item % a.splits, kvh = item / a.splits % a.kv_heads, seq = item / a.splits / a.kv_heads;
+    // Parts outermost: a sequence that has none so far out leaves at once,
+    // behind the workgroups that have work and beside the last of them.
+    const int split = blockIdx.z, seq = blockIdx.y, rt = blockIdx.x % a.row_tiles, kvh = blockIdx.x / a.row_tiles;
+    if (split && split * a.min_chunk >= a.lens[seq]) return;
 
     // The sequence, this tile's rows and the keys that any of them sees.
     const int len = max(0, (int)min((int64_t)a.lens[seq], (int64_t)a.table_pages << a.page_shift));
     const int start = a.starts ? a.starts[seq] : seq;
     const int n = a.starts ? a.starts[seq + 1] - start : 1;
     const int nq = min(n, a.max_new);
-    const int r0 = (int)rt * ROWS, i0 = r0 / a.group;
+    const int r0 = rt * ROWS, i0 = r0 / a.group;
     if (i0 >= nq) return;
     const int i1 = min(nq - 1, (r0 + ROWS - 1) / a.group);
     const int first = len - n;  // the first new token's position
@@ -388,7 +385,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 || RT > 1 ? 2 : 4) void atten
     __syncthreads();
     const int64_t tile = ((int64_t)seq * a.kv_heads + kvh) * a.row_tiles + rt;
     const int64_t part_floats = (int64_t)a.tile_rows * (D + 2);
-    float* part = a.partials + (tile * a.splits + split) * part_floats;
+    const auto own = make_rsrc(a.partials + (tile * a.splits + split) * part_floats, (uint32_t)(part_floats * 4));
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
         float common = -INFINITY;
@@ -396,8 +393,9 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 || RT > 1 ? 2 : 4) void atten
         for (int w = 0; w < kWaves; ++w) common = fmaxf(common, wave_ml[w][16 * t + j].x);
         const float mine = __builtin_amdgcn_exp2f(m[t] - (common == -INFINITY ? 0.0f : common));
 
-        // Thread (row, pair): two neighbouring columns of the 64 of each round.
-        const int row = 16 * t + (threadIdx.x >> 5), pair = threadIdx.x & 31;
+        // Thread (row, quad): four neighbouring columns of the 64 of each round.
+        static_assert(kWaves * 64 == kRows * 16, "threads");
+        const int row = 16 * t + (threadIdx.x >> 4), quad = threadIdx.x & 15;
         float row_m = -INFINITY, row_l = 0.0f;
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) row_m = fmaxf(row_m, wave_ml[w][row].x);
@@ -419,29 +417,28 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 || RT > 1 ? 2 : 4) void atten
                     make_float4(acc[t][4 * round][x] * mine, acc[t][4 * round + 1][x] * mine, acc[t][4 * round + 2][x] * mine,
                                 acc[t][4 * round + 3][x] * mine);
             __syncthreads();
-            float2 sum = make_float2(0.0f, 0.0f);
+            float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
             for (int w = 0; w < kWaves; ++w) {
-                const float2 v = *reinterpret_cast<const float2*>(&red[w][threadIdx.x >> 5][2 * pair]);
-                sum.x += v.x;
-                sum.y += v.y;
+                const float4 v = *reinterpret_cast<const float4*>(&red[w][threadIdx.x >> 4][4 * quad]);
+                sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
             }
-            // Column c of the round's 64: dimension F (c / 4) + 4 round + c % 4.
-            const int dim = F * (pair >> 1) + 4 * round + 2 * (pair & 1);
+            // Columns 4 q .. 4 q + 3 of the round's 64: dimensions F q + 4 round .. + 3.
+            const int dim = F * quad + 4 * round;
             if (parts == 1) {
                 if (out_valid) {
-                    typedef T T2 __attribute__((ext_vector_type(2)));
-                    *reinterpret_cast<T2*>(out + dim) = T2{(T)(sum.x * inv), (T)(sum.y * inv)};
+                    typedef T T4 __attribute__((ext_vector_type(4)));
+                    *reinterpret_cast<T4*>(out + dim) = T4{(T)(sum.x * inv), (T)(sum.y * inv), (T)(sum.z * inv), (T)(sum.w * inv)};
                 }
             } else if (keep) {
-                __hip_atomic_store(reinterpret_cast<unsigned long long*>(part + row * D + dim),
-                                   __builtin_bit_cast(unsigned long long, sum), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                const u32x4_t w = {__float_as_uint(sum.x), __float_as_uint(sum.y), __float_as_uint(sum.z), __float_as_uint(sum.w)};
+                __builtin_amdgcn_raw_buffer_store_b128(w, own, (row * D + dim) * 4, 0, kAgent);
             }
         }
-        if (parts > 1 && keep && pair == 0)
-            __hip_atomic_store(reinterpret_cast<unsigned long long*>(part + a.tile_rows * D + 2 * row),
-                               __builtin_bit_cast(unsigned long long, make_float2(row_m, row_l)), __ATOMIC_RELAXED,
-                               __HIP_MEMORY_SCOPE_AGENT);
+        if (parts > 1 && keep && quad == 0) {
+            const u32x2_t w = {__float_as_uint(row_m), __float_as_uint(row_l)};
+            __builtin_amdgcn_raw_buffer_store_b64(w, own, (a.tile_rows * D + 2 * row) * 4, 0, kAgent);
+        }
     }
     if (parts == 1) return;
 
@@ -461,10 +458,8 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 || RT > 1 ? 2 : 4) void atten
 }
 
 template <int D, typename T>
-void start(PagedArgs a, int64_t seqs, hipStream_t stream) {
-    a.items = (uint32_t)(a.splits * a.kv_heads * seqs);
-    const int64_t total = (int64_t)((a.items + 7) / 8 * 8) * a.row_tiles, wide = std::min<int64_t>(total, 1 << 20);
-    const dim3 grid((unsigned)wide, (unsigned)((total + wide - 1) / wide));
+void start(const PagedArgs& a, int64_t seqs, hipStream_t stream) {
+    const dim3 grid((unsigned)(a.kv_heads * a.row_tiles), (unsigned)seqs, (unsigned)a.splits);
     if (D == 256 || a.tile_rows <= kRows) hipLaunchKernelGGL((attention_paged_kernel<D, T, 1>), grid, dim3(64 * kWaves), 0, stream, a);
     else hipLaunchKernelGGL((attention_paged_kernel<D, T, D == 256 ? 1 : 2>), grid, dim3(64 * kWaves), 0, stream, a);
 }
@@ -476,13 +471,13 @@ PagedPlan paged_plan(int64_t seqs, int64_t max_new, int64_t heads, int64_t kv_he
     PagedPlan p;
     const int64_t rows = max_new * (heads / kv_heads);
     const int64_t most = rows > kRows && head_dim != 256 ? 2 * kRows : kRows;
-    const int64_t resident = head_dim == 256 || most > kRows ? 256 : 512;  // workgroups that run at once
+    const int64_t resident = head_dim == 256 || most > kRows ? 512 : 1024;  // workgroups that run at once
     p.rows = std::min<int64_t>(rows, most);
     p.row_tiles = (rows + most - 1) / most;
     const int64_t base = seqs * kv_heads * p.row_tiles;
-    p.splits = std::max(resident / base, (max_len + 2047) / 2048);
+    p.splits = std::max(resident / base, (max_len + 1023) / 1024);
     p.splits = std::max<int64_t>(1, std::min({p.splits, (max_len + kStep - 1) / kStep, (int64_t)kMaxSplits}));
-    p.min_chunk = base >= 256 ? 2 * kStep : kStep;
+    p.min_chunk = base >= resident / 4 ? 1024 : base >= resident / 16 ? 512 : 256;
     p.partial_floats = p.splits > 1 ? base * p.splits * p.rows * (head_dim + 2) : 0;
     p.counter_words = p.splits > 1 ? base * kTileCounters : 0;
     return p;
@@ -494,7 +489,7 @@ hipError_t launch_attention_paged(const pq2_attention_paged_args& a, const Paged
                       a.partials, a.counters, a.table_stride, (int)a.rows, (int)a.table_pages, (int)a.kv_heads,
                       (int)(a.heads / a.kv_heads), (int)a.pages, log2_of(a.page_tokens), (int)a.max_new,
                       (int)std::min<int64_t>(a.window, 0x40000000), (int)plan.splits, (int)plan.row_tiles, (int)plan.rows,
-                      (int)plan.min_chunk, 0, a.scale * kLog2e};
+                      (int)plan.min_chunk, a.scale * kLog2e};
     clear_stale_error();
     const bool f16 = a.dtype == PQ2_F16;
     if (a.head_dim == 64) f16 ? start<64, _Float16>(k, a.seqs, stream) : start<64, __bf16>(k, a.seqs, stream);
