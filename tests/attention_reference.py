@@ -9,6 +9,9 @@ the 16-bit type:
 - a score is a sum of head_dim exact products in FP32 (products of two 8- or
   11-bit numbers are exact), scaled with at most four roundings: off by at
   most d_j = (head_dim + 4) u A_j + 4 u |s_j|, A_j = scale * sum |q k_j|;
+  paged: the products are q (c + 1152), |c + 1152| <= 1279, with 1152 sum q taken off, so that A_j is joined by
+  2 * 1279 / 127 * scale * max|k_j| * sum |q|, a bound for the worst order of signs (for random ones the
+  norm of the whole error is held to that of the last rounding);
 - a weight exp(s_j - m), with the subtraction and exp2 (two units), is then
   off by e_j = d_j + d_m + 8 u + 2 u (|s_j| + |m|) of itself, d_m the same bound of the row's largest A;
 - paged: the weight times the value's scale is kept as two bf16, 2^-16 of itself
@@ -115,6 +118,8 @@ def attention(q, k, v, first, *, scale, causal=True, window=0, there=None, paged
         w = torch.exp(s - top[:, None])
         total = w.sum(1).clamp(min=1e-300)
         sa = torch.where(seen, s.abs(), torch.zeros_like(s))
+        if paged:
+            a = a + 20.2 * scale * qh.abs().sum(1)[:, None] * kh.abs().amax(1)[None]
         dj = (d + 4) * U * a + 4 * U * sa
         e = dj + dj.amax(1, keepdim=True) + 8 * U + 2 * U * (sa + top.abs()[:, None]) + (256 + nk / 32) * U
         e = e + (2.0 ** -16 if paged else half)

@@ -248,7 +248,10 @@ PAGED = [
 @pytest.mark.parametrize("lengths,new,heads,kv,d,page,dt,window", PAGED)
 def test_attention_paged(lengths, new, heads, kv, d, page, dt, window):
     announce(f"paged lengths={lengths} new={new} heads={heads}/{kv} d={d} page={page} {dt} window={window}")
-    within(*paged_case(lengths, new, heads, kv, d, page, dt, window, seed=heads + d), "o")
+    got, want, bound = paged_case(lengths, new, heads, kv, d, page, dt, window, seed=heads + d)
+    within(got, want, bound, "o")
+    # The last rounding is off by at most half of each value; all other errors together are a tenth of that.
+    assert float((got.double() - want).norm()) <= 1.1 * torch.finfo(DT[dt]).eps / 2 * float(want.norm())
 
 
 @pytest.mark.parametrize("d", ref.DIMS)
