@@ -17,6 +17,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int64_t kMaxGridX = 1 << 20;
+constexpr int64_t kFewElements = 4 << 20;
 
 struct HeadRows {
     const void* p;
@@ -150,48 +151,55 @@ struct ReadArgs {
     int rows, seqs, table_pages, kv_heads, pages, page_shift, out_dtype;
 };
 
-// E elements of a row a lane, 16 bytes of output; a workgroup takes kThreads /
-// (D / E) rows of one head, keys and values.
-template <int D, int E>
+// E elements of a row a lane, 16 bytes of output; a workgroup takes U times
+// kThreads / (D / E) rows of one head, keys and values, all their loads at once.
+template <int D, int E, int U>
 __global__ __launch_bounds__(kThreads) void kv_read_kernel(ReadArgs a) {
     constexpr int LPR = D / E, RB = kThreads / LPR;
     const int j = threadIdx.x % LPR, h = blockIdx.y;
-    for (int64_t row0 = (int64_t)blockIdx.x * RB; row0 < a.rows; row0 += (int64_t)gridDim.x * RB) {
+    for (int64_t row0 = (int64_t)blockIdx.x * (RB * U); row0 < a.rows; row0 += (int64_t)gridDim.x * (RB * U)) {
         const int end = min(a.rows, a.starts[a.seqs]);
-        const int row = (int)row0 + threadIdx.x / LPR;
-        int s = sequence_of(a.starts, a.seqs, (int)row0);
-        if (row >= end) continue;
-        while (s + 1 < a.seqs && a.starts[s + 1] <= row) ++s;
-        const int t = row - a.starts[s];
-        const int idx = t >> a.page_shift;
-        const int page = t >= 0 && idx < a.table_pages ? a.table[s * a.table_stride + idx] : -1;
-        const bool there = page >= 0 && page < a.pages;
-        const int tok = t & ((1 << a.page_shift) - 1);
-        const uint8_t* block = a.cache + ((int64_t)(there ? page : 0) * a.kv_heads + h) * (kv_block_bytes(1, D) << a.page_shift);
-        const float* scales = reinterpret_cast<const float*>(block + ((int64_t)(2 * D) << a.page_shift));
+        int s = a.seqs == 1 ? 0 : sequence_of(a.starts, a.seqs, (int)row0);
+        uint32_t code[U][2][E / 4] = {};
+        float scale[U][2] = {};
 #pragma unroll
-        for (int w = 0; w < 2; ++w) {
-            float v[E];
-            float scale = 0.0f;
-            uint32_t code[E / 4] = {};
-            if (there) {
+        for (int u = 0; u < U; ++u) {
+            const int row = (int)row0 + u * RB + threadIdx.x / LPR;
+            if (row >= end) continue;
+            while (s + 1 < a.seqs && a.starts[s + 1] <= row) ++s;
+            const int t = row - a.starts[s], idx = t >> a.page_shift, tok = t & ((1 << a.page_shift) - 1);
+            const int page = t >= 0 && idx < a.table_pages ? a.table[s * a.table_stride + idx] : -1;
+            if (page < 0 || page >= a.pages) continue;
+            const uint8_t* block = a.cache + ((int64_t)page * a.kv_heads + h) * (kv_block_bytes(1, D) << a.page_shift);
+            const float* scales = reinterpret_cast<const float*>(block + ((int64_t)(2 * D) << a.page_shift));
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
                 const uint8_t* codes = block + (((int64_t)w << a.page_shift) + tok) * D + j * E;
-                scale = scales[(w << a.page_shift) + tok];
+                scale[u][w] = scales[(w << a.page_shift) + tok];
 #pragma unroll
-                for (int i = 0; i < E / 4; ++i) code[i] = reinterpret_cast<const uint32_t*>(codes)[i];
+                for (int i = 0; i < E / 4; ++i) code[u][w][i] = reinterpret_cast<const uint32_t*>(codes)[i];
             }
+        }
 #pragma unroll
-            for (int i = 0; i < E; ++i) v[i] = (float)(int8_t)(code[i / 4] >> (8 * (i % 4))) * scale;
-            const int64_t to = row * a.out[w].stride + h * a.out[w].head + j * E;
-            if constexpr (E == 4) {
-                store4(a.out[w].p, to, PQ2_F32, v);
-            } else {
-                const uint4 x = a.out_dtype == PQ2_BF16
-                                    ? make_uint4(pack2<__bf16>(v[0], v[1]), pack2<__bf16>(v[2], v[3]),
-                                                 pack2<__bf16>(v[4], v[5]), pack2<__bf16>(v[6], v[7]))
-                                    : make_uint4(pack2<_Float16>(v[0], v[1]), pack2<_Float16>(v[2], v[3]),
-                                                 pack2<_Float16>(v[4], v[5]), pack2<_Float16>(v[6], v[7]));
-                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(const_cast<void*>(a.out[w].p)) + to) = x;
+        for (int u = 0; u < U; ++u) {
+            const int row = (int)row0 + u * RB + threadIdx.x / LPR;
+            if (row >= end) continue;
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+                float v[E];
+#pragma unroll
+                for (int i = 0; i < E; ++i) v[i] = (float)(int8_t)(code[u][w][i / 4] >> (8 * (i % 4))) * scale[u][w];
+                const int64_t to = row * a.out[w].stride + h * a.out[w].head + j * E;
+                if constexpr (E == 4) {
+                    store4(a.out[w].p, to, PQ2_F32, v);
+                } else {
+                    const uint4 x = a.out_dtype == PQ2_BF16
+                                        ? make_uint4(pack2<__bf16>(v[0], v[1]), pack2<__bf16>(v[2], v[3]),
+                                                     pack2<__bf16>(v[4], v[5]), pack2<__bf16>(v[6], v[7]))
+                                        : make_uint4(pack2<_Float16>(v[0], v[1]), pack2<_Float16>(v[2], v[3]),
+                                                     pack2<_Float16>(v[4], v[5]), pack2<_Float16>(v[6], v[7]));
+                    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(const_cast<void*>(a.out[w].p)) + to) = x;
+                }
             }
         }
     }
@@ -203,12 +211,20 @@ void start_write(const WriteArgs& a, hipStream_t stream) {
     hipLaunchKernelGGL((kv_write_kernel<D>), grid, dim3(kThreads), 0, stream, a);
 }
 
+template <int D, int E, int U>
+void start_read(const ReadArgs& a, hipStream_t stream) {
+    const int rb = U * kThreads * E / D;
+    const dim3 grid((unsigned)std::min<int64_t>((a.rows + rb - 1) / rb, kMaxGridX), (unsigned)a.kv_heads);
+    hipLaunchKernelGGL((kv_read_kernel<D, E, U>), grid, dim3(kThreads), 0, stream, a);
+}
+
+// Few rows: one a lane, over as many workgroups as there are. Many: two (32768
+// tokens of 8 heads of 128 to bf16 47 us; one 54, four 49, eight 55).
 template <int D>
 void start_read(const ReadArgs& a, hipStream_t stream) {
-    const int rb = kThreads * (a.out_dtype == PQ2_F32 ? 4 : 8) / D;
-    const dim3 grid((unsigned)std::min<int64_t>((a.rows + rb - 1) / rb, kMaxGridX), (unsigned)a.kv_heads);
-    if (a.out_dtype == PQ2_F32) hipLaunchKernelGGL((kv_read_kernel<D, 4>), grid, dim3(kThreads), 0, stream, a);
-    else hipLaunchKernelGGL((kv_read_kernel<D, 8>), grid, dim3(kThreads), 0, stream, a);
+    const bool few = (int64_t)a.rows * a.kv_heads * D < kFewElements;
+    if (a.out_dtype == PQ2_F32) few ? start_read<D, 4, 1>(a, stream) : start_read<D, 4, 2>(a, stream);
+    else few ? start_read<D, 8, 1>(a, stream) : start_read<D, 8, 2>(a, stream);
 }
 
 }  // namespace
