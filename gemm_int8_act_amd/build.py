@@ -19,6 +19,7 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libpq2.so")
+MARSHAL = os.path.join(HERE, "_marshal.so")  # host code only: arguments from torch tensors
 BUILD_DIR = os.path.join(HERE, "_build")
 SOURCES = ["api.hip", "quantize.hip", "small_m.hip", "small_m_wg.hip", "tiles.hip", "prefill.hip", "probe.hip",
            "block_api.hip", "w4.hip", "block_small_m.hip", "block_prefill.hip",
@@ -60,8 +61,27 @@ def _compile(src: str) -> str:
     return obj
 
 
+def _marshal_module() -> None:
+    """Compile the binding's argument marshaller (csrc/marshal.cpp) against torch's headers; it finds libpq2.so next to
+    itself."""
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    tmp = MARSHAL + ".tmp"
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-DUSE_ROCM",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", sysconfig.get_path("include"), "-isystem", os.path.join(root, "include"),
+           os.path.join(CSRC, "marshal.cpp"), "-o", tmp, "-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu",
+           "-lc10", "-L", HERE, "-lpq2", "-Wl,-rpath,$ORIGIN"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"g++ failed for marshal.cpp:\n{res.stdout}\n{res.stderr}")
+    os.replace(tmp, MARSHAL)
+
+
 def build(verbose: bool = False) -> str:
-    """Compile every HIP source for gfx950 and link libpq2.so; returns its path."""
+    """Compile every HIP source for gfx950, link libpq2.so and build the argument marshaller; returns libpq2's path."""
     os.makedirs(BUILD_DIR, exist_ok=True)
     workers = min(len(SOURCES), max(1, (os.cpu_count() or 1)))
     with concurrent.futures.ThreadPoolExecutor(max_workers=workers) as pool:
@@ -72,6 +92,7 @@ def build(verbose: bool = False) -> str:
     if res.returncode != 0:
         raise RuntimeError(f"link failed:\n{res.stdout}\n{res.stderr}")
     os.replace(tmp, LIB)
+    _marshal_module()
     if verbose:
         print(f"built {LIB}")
     return LIB

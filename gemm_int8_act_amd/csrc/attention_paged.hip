@@ -543,7 +543,7 @@ PagedPlan paged_plan(int64_t seqs, int64_t max_new, int64_t heads, int64_t kv_he
     // (64 sequences of 1 to 16384) 89 against 78.
     const int64_t base = seqs * kv_heads * p.row_tiles, fill = head_dim == 64 ? 1024 : 512;
     p.splits = std::max(fill / base, (max_len + 2047) / 2048);
-    p.splits = std::max<int64_t>(1, std::min({p.splits, (max_len + kStep - 1) / kStep, (int64_t)kMaxSplits}));
+    p.splits = std::max<int64_t>(1, std::min({p.splits, (max_len + 255) / 256, (int64_t)kMaxSplits}));
     p.splits = (int64_t)1 << log2_of(p.splits);
     p.min_chunk = base >= fill ? 2048 : base >= fill / 4 ? 1024 : base >= fill / 16 ? 512 : 256;
     p.partial_floats = p.splits > 1 ? base * p.splits * p.rows * (head_dim + 2) : 0;

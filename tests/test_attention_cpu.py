@@ -5,6 +5,7 @@ validation or the device check, so nothing is launched)."""
 import ctypes
 import os
 import re
+import struct
 import subprocess
 
 import pytest
@@ -12,7 +13,7 @@ import torch
 
 import attention_reference as ref
 import gemm_int8_act_amd as pq2
-from gemm_int8_act_amd import attention as binding
+from gemm_int8_act_amd import _marshal
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 OK, EINVAL, ESHAPE, EALIGN, EDEVICE = pq2.PQ2_OK, pq2.PQ2_EINVAL, pq2.PQ2_ESHAPE, pq2.PQ2_EALIGN, pq2.PQ2_EDEVICE
@@ -24,14 +25,55 @@ CTYPES = {"P": ctypes.c_void_p, "q": ctypes.c_int64, "f": ctypes.c_float, "i": c
 no_gpu = pytest.mark.skipif(torch.cuda.device_count() > 0, reason="the device check passes on a GPU")
 
 
+# The argument structures of include/pq2_attention.h: the fields in order, with
+# their native struct codes.
+WRITE_FIELDS = (
+    ("q", "P"), ("k", "P"), ("v", "P"),
+    ("q_stride", "q"), ("q_head", "q"), ("k_stride", "q"), ("k_head", "q"), ("v_stride", "q"), ("v_head", "q"),
+    ("q_out", "P"), ("k_out", "P"), ("v_out", "P"),
+    ("qo_stride", "q"), ("qo_head", "q"), ("ko_stride", "q"), ("ko_head", "q"), ("vo_stride", "q"), ("vo_head", "q"),
+    ("cos", "P"), ("sin", "P"), ("positions", "P"), ("slots", "P"), ("cache", "P"),
+    ("m", "q"), ("heads", "q"), ("kv_heads", "q"), ("head_dim", "q"), ("rot_dim", "q"), ("table_rows", "q"),
+    ("pages", "q"), ("page_tokens", "q"),
+    ("in_dtype", "i"), ("out_dtype", "i"), ("interleaved", "i"),
+)
+READ_FIELDS = (
+    ("cache", "P"), ("table", "P"), ("starts", "P"), ("k_out", "P"), ("v_out", "P"),
+    ("ko_stride", "q"), ("ko_head", "q"), ("vo_stride", "q"), ("vo_head", "q"),
+    ("rows", "q"), ("seqs", "q"), ("table_stride", "q"), ("table_pages", "q"), ("kv_heads", "q"), ("head_dim", "q"),
+    ("pages", "q"), ("page_tokens", "q"),
+    ("out_dtype", "i"),
+)
+PAGED_FIELDS = (
+    ("q", "P"), ("out", "P"), ("q_stride", "q"), ("q_head", "q"), ("out_stride", "q"), ("out_head", "q"),
+    ("cache", "P"), ("table", "P"), ("lens", "P"), ("starts", "P"), ("partials", "P"), ("counters", "P"),
+    ("rows", "q"), ("seqs", "q"), ("table_stride", "q"), ("table_pages", "q"), ("heads", "q"), ("kv_heads", "q"),
+    ("head_dim", "q"), ("pages", "q"), ("page_tokens", "q"), ("max_new", "q"), ("max_len", "q"), ("window", "q"),
+    ("scale", "f"), ("dtype", "i"),
+)
+PROMPT_FIELDS = (
+    ("q", "P"), ("k", "P"), ("v", "P"), ("out", "P"),
+    ("q_stride", "q"), ("q_head", "q"), ("k_stride", "q"), ("k_head", "q"), ("v_stride", "q"), ("v_head", "q"),
+    ("out_stride", "q"), ("out_head", "q"),
+    ("starts_q", "P"), ("starts_k", "P"),
+    ("rows_q", "q"), ("rows_k", "q"), ("seqs", "q"), ("heads", "q"), ("kv_heads", "q"), ("head_dim", "q"),
+    ("window", "q"), ("scale", "f"), ("dtype", "i"), ("causal", "i"),
+)
+
+
+def packer(fields):
+    # The structure ends at a multiple of its widest member, as in C.
+    return struct.Struct("@" + "".join(code for _, code in fields) + "0q")
+
+
 def structure(name, fields):
     return type(name, (ctypes.Structure,), {"_fields_": [(f, CTYPES[c]) for f, c in fields]})
 
 
-STRUCTS = {"pq2_kv_write_args": (binding.WRITE_FIELDS, binding._WRITE),
-           "pq2_kv_read_args": (binding.READ_FIELDS, binding._READ),
-           "pq2_attention_paged_args": (binding.PAGED_FIELDS, binding._PAGED),
-           "pq2_attention_prompt_args": (binding.PROMPT_FIELDS, binding._PROMPT)}
+STRUCTS = {"pq2_kv_write_args": (WRITE_FIELDS, packer(WRITE_FIELDS)),
+           "pq2_kv_read_args": (READ_FIELDS, packer(READ_FIELDS)),
+           "pq2_attention_paged_args": (PAGED_FIELDS, packer(PAGED_FIELDS)),
+           "pq2_attention_prompt_args": (PROMPT_FIELDS, packer(PROMPT_FIELDS))}
 
 
 def test_header_symbols_exported():
@@ -44,7 +86,7 @@ def test_header_symbols_exported():
 
 @pytest.mark.parametrize("name", list(STRUCTS))
 def test_args_struct_matches_the_header(tmp_path, name):
-    """Field order and offsets of the binding's structure, by the C compiler."""
+    """Field order and offsets of the structures used here, by the C compiler."""
     fields, packer = STRUCTS[name]
     cls = structure(name, fields)
     src = tmp_path / "offsets.c"
