@@ -18,8 +18,12 @@ namespace pq2 {
 
 namespace {
 
-constexpr int kBufs = 4;            // tiles of keys, and of values, in LDS
-constexpr int kAhead = 4;           // products that an operand is read ahead
+// Tiles of keys, and of values, in LDS; products that an operand is read ahead;
+// 16-column pieces of the queries in LDS instead of registers (of 256 columns: or a SIMD
+// holds one wave, which alone issues a vector instruction only every second time).
+constexpr int bufs_of(int d) { return d == 256 ? 2 : 4; }
+constexpr int ahead_of(int d) { return d == 256 ? 3 : 4; }
+constexpr int q_lds_of(int d) { return d == 256 ? 8 : 0; }
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 8.0f;      // weights grow to 2^8 before a row's reference moves
 
@@ -130,7 +134,7 @@ __device__ __forceinline__ int item_of(int id, int total) {
 }
 
 template <int D, typename T, int W>
-__global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attention_prompt_kernel(PromptArgs a) {
+__global__ __launch_bounds__(64 * W, 2) void attention_prompt_kernel(PromptArgs a) {
     typedef typename Half<T>::v8 v8;
     typedef typename Half<T>::v2 v2;
     constexpr int BM = 32 * W;                   // query rows of a workgroup, 32 of them a wave's
@@ -140,7 +144,8 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attention_prompt_ker
     constexpr int TILE = KT * D * 2;             // bytes of a tile in LDS
     constexpr int LOADS = TILE / 1024 / W;       // 1 KB loads of a wave for a tile
     constexpr int LROWS = 512 / D;               // rows of such a load
-    extern __shared__ uint4 lds[];               // kBufs K tiles, kBufs V tiles
+    constexpr int kBufs = bufs_of(D), kAhead = ahead_of(D), QR = D / 16 - q_lds_of(D);  // QR: pieces of q in registers
+    extern __shared__ uint4 lds[];               // kBufs K tiles, kBufs V tiles, pieces of q
 
     // Items: heads of a key-value head next to each other, then its tiles.
     const int item = item_of(blockIdx.y * gridDim.x + blockIdx.x, gridDim.x * gridDim.y);
@@ -162,15 +167,20 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attention_prompt_ker
 
     const int qi = q0 + 32 * wave + row;
     const bool valid = qi < nq && qs + qi >= 0 && qs + qi < a.rows_q;
-    v8 qf[D / 16];
-    if (valid) {
-        const uint16_t* q = a.q + (int64_t)(qs + qi) * a.q_stride + head * a.q_head + 8 * half;
+    v8 qf[QR];
+    uint4* q_lds = lds + 2 * kBufs * (TILE / 16) + wave * 64 + lane;
+    {
+        const uint16_t* q = a.q + (int64_t)(valid ? qs + qi : 0) * a.q_stride + head * a.q_head + 8 * half;
 #pragma unroll
-        for (int s = 0; s < D / 16; ++s) qf[s] = *reinterpret_cast<const v8*>(q + 16 * s);
-    } else {
-#pragma unroll
-        for (int s = 0; s < D / 16; ++s) qf[s] = v8{};
+        for (int s = 0; s < D / 16; ++s) {
+            const v8 x = *reinterpret_cast<const v8*>(q + 16 * s), y = valid ? x : v8{};
+            if (s < QR) qf[s] = y;
+            else q_lds[(s - QR) * 64 * W] = __builtin_bit_cast(uint4, y);
+        }
     }
+    typedef __attribute__((address_space(3))) char lds_char;
+    lds_char* qat = (lds_char*)q_lds;
+    auto query = [&](int s) -> v8 { return *(__attribute__((address_space(3))) v8*)(qat + (s - QR) * 1024 * W); };
     // Keys that this row, and the wave's rows all together, see.
     const int seen_hi = a.causal ? min(nk, qi + offset + 1) : nk;
     const int seen_lo = a.window ? qi + offset - a.window + 1 : 0;
@@ -208,7 +218,6 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attention_prompt_ker
     // weights, then the keys' (s, b) for the next tile's scores.  A lane's place
     // depends on the swizzle in four ways; the rest is a constant offset.
     constexpr int PV = NF * DB, N = 2 * PV, RB = 2 * D;  // RB: bytes of a row
-    typedef __attribute__((address_space(3))) char lds_char;
     lds_char* kat[4];
     lds_char* vat[DB < 4 ? DB : 4];
     {
@@ -245,28 +254,36 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attention_prompt_ker
     // One step: this tile's softmax (sc -> p), the last tile's values and the
     // next tile's scores (-> next), which do not need each other, in turns.
     // Operands are read kAhead products ahead; a piece of p is written behind
-    // its last use for the last tile.  Keys four tiles ahead and values two
-    // tiles ahead go into the buffers that the step before read last, and are
-    // waited for two steps later (behind the last tile it is loaded again, so that the count of
-    // loads on their way is always the same).
+    // its last use for the last tile.  Keys kBufs tiles ahead and values kBufs - 2
+    // ahead go into the buffers that the step before read last, and are waited for kBufs - 2
+    // steps later (behind the last tile it is loaded again, so that the count
+    // of loads on their way is always the same).
     const int last_tile = lo + (hi - 1 - lo) / KT * KT;
     auto fetch_k = [&](int key0, int buf) { fetch(kbase, a.k_stride, kcol, min(key0, last_tile), buf * TILE); };
     auto fetch_v = [&](int key0, int buf) { fetch(vbase, a.v_stride, vcol, min(key0, last_tile), (kBufs + buf) * TILE); };
     auto step = [&](int key0, auto at_buf, v16f (&sc)[KB], v16f (&next)[KB]) {
         constexpr int buf = decltype(at_buf)::value;       // of this tile
         constexpr int kbuf = (buf + 1) % kBufs, vbuf = (buf + kBufs - 1) % kBufs;
-        v8 ring[kAhead];
+        v8 ring[kAhead], q_ring[kAhead];
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) ring[i] = operand(i, vbuf);
-        fetch_k(key0 + 4 * KT, buf);
-        fetch_v(key0 + 2 * KT, (buf + 2) % kBufs);
+        fetch_k(key0 + kBufs * KT, buf);
+        fetch_v(key0 + (kBufs - 2) * KT, (buf + kBufs - 2) % kBufs);
         float top = -INFINITY, alpha = 1.0f, bias = 0.0f;
         each<N>([&](auto at) {
             constexpr int i = decltype(at)::value;
             __builtin_amdgcn_sched_barrier(0);
             if constexpr (i < PV) acc[i % DB] = Half<T>::mfma(ring[i % kAhead], weights(i / DB), acc[i % DB]);
-            else next[i % KB] = Half<T>::mfma(ring[i % kAhead], qf[(i - PV) / KB], i < PV + KB ? v16f{} : next[i % KB]);
-            if constexpr (i + kAhead < N) ring[i % kAhead] = operand(i + kAhead, i + kAhead < PV ? vbuf : kbuf);
+            else {
+                constexpr int qs = (i - PV) / KB;
+                next[i % KB] = Half<T>::mfma(ring[i % kAhead], qs < QR ? qf[qs < QR ? qs : 0] : q_ring[i % kAhead],
+                                             i < PV + KB ? v16f{} : next[i % KB]);
+            }
+            if constexpr (i + kAhead < N) {
+                constexpr int ahead = i + kAhead, qs = (ahead - PV) / KB;
+                ring[i % kAhead] = operand(ahead, ahead < PV ? vbuf : kbuf);
+                if constexpr (ahead >= PV && qs >= QR) q_ring[i % kAhead] = query(qs);
+            }
             if constexpr (i < N / 4) {
                 constexpr int E = 64 * KB / N;  // scores a product
 #pragma unroll
@@ -301,7 +318,7 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attention_prompt_ker
             for (int d = 0; d < DB; ++d) acc[d] *= f;
         }
         mask(key0 + KT, next);
-        wait_loads<4 * LOADS>();
+        wait_loads<(kBufs - 2) * 2 * LOADS>();
         __syncthreads();
     };
 
@@ -310,16 +327,21 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attention_prompt_ker
         for (int i = threadIdx.x; i < TILE / 16; i += 64 * W) lds[(2 * kBufs - 1) * (TILE / 16) + i] = make_uint4(0, 0, 0, 0);
         fetch_k(lo, 0);
         fetch_k(lo + KT, 1);
-        fetch_k(lo + 2 * KT, 2);
-        fetch_v(lo, 0);
-        fetch_k(lo + 3 * KT, 3);
-        fetch_v(lo + KT, 1);
-        wait_loads<4 * LOADS>();
+#pragma unroll
+        for (int i = 0; i < kBufs - 2; ++i) {
+            fetch_k(lo + (2 + i) * KT, 2 + i);
+            fetch_v(lo + i * KT, i);
+        }
+        wait_loads<(kBufs - 2) * 2 * LOADS>();
         __syncthreads();
         v16f even[KB], odd[KB];
         each<PV>([&](auto at) {
             constexpr int i = PV + decltype(at)::value;
-            even[i % KB] = Half<T>::mfma(operand(i, 0), qf[(i - PV) / KB], i < PV + KB ? v16f{} : even[i % KB]);
+            constexpr int qs = (i - PV) / KB;
+            v8 q;
+            if constexpr (qs < QR) q = qf[qs];
+            else q = query(qs);
+            even[i % KB] = Half<T>::mfma(operand(i, 0), q, i < PV + KB ? v16f{} : even[i % KB]);
         });
         mask(lo, even);
         __syncthreads();
@@ -334,10 +356,12 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attention_prompt_ker
             if (behind(0)) break;
             step(key0, std::integral_constant<int, 1>{}, odd, even);
             if (behind(1)) break;
-            step(key0, std::integral_constant<int, 2>{}, even, odd);
-            if (behind(2)) break;
-            step(key0, std::integral_constant<int, 3>{}, odd, even);
-            if (behind(3)) break;
+            if constexpr (kBufs == 4) {
+                step(key0, std::integral_constant<int, 2>{}, even, odd);
+                if (behind(2)) break;
+                step(key0, std::integral_constant<int, 3>{}, odd, even);
+                if (behind(3)) break;
+            }
         }
         each<PV>([&](auto at) {
             constexpr int i = decltype(at)::value;
@@ -362,7 +386,7 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attention_prompt_ker
 template <int D, typename T, int W>
 void start(PromptArgs a, hipStream_t stream) {
     a.tiles = (a.rows_q + 32 * W - 1) / (32 * W) + a.seqs;
-    const size_t lds = 2 * kBufs * (size_t)(D == 256 ? 32 : 64) * D * 2;
+    const size_t lds = 2 * bufs_of(D) * (size_t)(D == 256 ? 32 : 64) * D * 2 + (size_t)q_lds_of(D) * 1024 * W;
     hipLaunchKernelGGL((attention_prompt_kernel<D, T, W>), dim3((unsigned)a.tiles, (unsigned)a.heads), dim3(64 * W), lds, stream, a);
 }
 
@@ -371,7 +395,7 @@ void start(const PromptArgs& a, int d, hipStream_t stream) {
     const bool few = ((a.rows_q + 255) / 256) * a.heads < 512;
     if (d == 64) few ? start<64, T, 4>(a, stream) : start<64, T, 8>(a, stream);
     else if (d == 128) few ? start<128, T, 4>(a, stream) : start<128, T, 8>(a, stream);
-    else start<256, T, 4>(a, stream);
+    else few ? start<256, T, 4>(a, stream) : start<256, T, 8>(a, stream);
 }
 
 }  // namespace
