@@ -35,7 +35,7 @@ struct PromptArgs {
     int64_t q_stride, q_head, k_stride, k_head, v_stride, v_head, out_stride, out_head;
     const int32_t* starts_q;
     const int32_t* starts_k;
-    int rows_q, rows_k, seqs, heads, group, window, causal, tiles;
+    int rows_q, rows_k, seqs, heads, group, window, causal;
     float scale2, slack;  // scale * log2(e); how far scores may pass a row's reference (in scores)
 };
 
@@ -106,20 +106,20 @@ __device__ __forceinline__ void each(F&& f) {
     each_of(f, std::make_integer_sequence<int, N>{});
 }
 
-// The first of a sequence's places among the workgroups of a head: places
-// starts[s] / BM + s, enough for its tiles of BM rows, whatever the lengths.
+// The first of a sequence's places among the workgroups of a key-value head:
+// starts[s] * group / BM + s, enough for its tiles of BM rows, whatever the lengths.
 template <int BM>
-__device__ __forceinline__ int first_place(int start, int s) { return (int)((uint32_t)start / BM) + s; }
+__device__ __forceinline__ int first_place(int start, int group, int s) { return (int)((uint32_t)(start * group) / BM) + s; }
 
 // The sequence at `place`: the last one whose first place is not behind it, 64
 // sequences a step of the search.
 template <int BM>
-__device__ __forceinline__ int sequence_at(const int32_t* starts, int seqs, int place) {
+__device__ __forceinline__ int sequence_at(const int32_t* starts, int group, int seqs, int place) {
     const int lane = threadIdx.x & 63;
     int lo = 0, count = seqs;
     while (true) {
         const int step = (count + 63) >> 6, at = lane * step;
-        const bool below = at < count && first_place<BM>(starts[lo + at], lo + at) <= place;
+        const bool below = at < count && first_place<BM>(starts[lo + at], group, lo + at) <= place;
         lo += max((int)__popcll(__ballot(below)) - 1, 0) * step;
         if (step == 1) return __builtin_amdgcn_readfirstlane(lo);
         count = min(step, seqs - lo);
@@ -147,25 +147,28 @@ __global__ __launch_bounds__(64 * W, 2) void attention_prompt_kernel(PromptArgs 
     constexpr int kBufs = bufs_of(D), kAhead = ahead_of(D), QR = D / 16 - q_lds_of(D);  // QR: pieces of q in registers
     extern __shared__ uint4 lds[];               // kBufs K tiles, kBufs V tiles, pieces of q
 
-    // Items: heads of a key-value head next to each other, then its tiles.
+    // A key-value head's tiles follow each other on an XCD.
     const int item = item_of(blockIdx.y * gridDim.x + blockIdx.x, gridDim.x * gridDim.y);
-    const int per = a.tiles * a.group, kvh = item / per, head = kvh * a.group + item % a.group;
-    const int place = item % per / a.group, seq = a.seqs == 1 ? 0 : sequence_at<BM>(a.starts_q, a.seqs, place);
+    const int kvh = item / gridDim.x, place = item % gridDim.x;
+    const int seq = a.seqs == 1 ? 0 : sequence_at<BM>(a.starts_q, a.group, a.seqs, place);
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int row = lane & 31, half = lane >> 5;
     // Queries and keys of the sequence, kept inside the tensors.
     const int qs = a.starts_q[seq], ks = a.starts_k[seq];
     const int nq = a.starts_q[seq + 1] - qs;
     // The longest tile first; places behind a sequence's last tile have no work.
-    const int tile = (max(nq, 0) + BM - 1) / BM - 1 - (place - first_place<BM>(qs, seq));
-    if (tile < 0 || place < first_place<BM>(qs, seq)) return;
+    const int before = first_place<BM>(qs, a.group, seq);
+    const int tile = (max(nq, 0) * a.group + BM - 1) / BM - 1 - (place - before);
+    if (tile < 0 || place < before) return;
     const int nk = ks < 0 ? 0 : max(0, min(a.starts_k[seq + 1], a.rows_k) - ks);
-    const int q0 = tile * BM;
+    // Rows are queries, each with the grouped heads next to each other: a tile
+    // holds few tokens, so that little of it lies behind a causal mask or a sequence's end.
     const int offset = nk - nq;  // a query's position is its index + offset
-    const int hi = a.causal ? min(nk, offset + min(q0 + BM, nq)) : nk;
-    const int lo = a.window ? max(0, offset + q0 - a.window + 1) & ~(KT - 1) : 0;
+    const int q_first = tile * BM / a.group, q_last = min(nq - 1, (tile * BM + BM - 1) / a.group);
+    const int hi = a.causal ? min(nk, offset + q_last + 1) : nk;
+    const int lo = a.window ? max(0, offset + q_first - a.window + 1) & ~(KT - 1) : 0;
 
-    const int qi = q0 + 32 * wave + row;
+    const int r0 = tile * BM + 32 * wave, qi = (r0 + row) / a.group, head = kvh * a.group + (r0 + row) % a.group;
     const bool valid = qi < nq && qs + qi >= 0 && qs + qi < a.rows_q;
     v8 qf[QR];
     uint4* q_lds = lds + 2 * kBufs * (TILE / 16) + wave * 64 + lane;
@@ -184,9 +187,8 @@ __global__ __launch_bounds__(64 * W, 2) void attention_prompt_kernel(PromptArgs 
     // Keys that this row, and the wave's rows all together, see.
     const int seen_hi = a.causal ? min(nk, qi + offset + 1) : nk;
     const int seen_lo = a.window ? qi + offset - a.window + 1 : 0;
-    const int wave_first = q0 + 32 * wave + offset;
-    const int all_hi = a.causal ? min(nk, wave_first + 1) : nk;
-    const int all_lo = a.window ? wave_first + 31 - a.window + 1 : 0;
+    const int all_hi = a.causal ? min(nk, r0 / a.group + offset + 1) : nk;
+    const int all_lo = a.window ? (r0 + 31) / a.group + offset - a.window + 1 : 0;
 
     // Loads: chunk `lane` of load i of this wave is row lrow + i * W * LROWS of
     // the tile (a multiple of eight apart: one swizzle).  Rows behind the last key repeat it.
@@ -385,14 +387,14 @@ __global__ __launch_bounds__(64 * W, 2) void attention_prompt_kernel(PromptArgs 
 
 template <int D, typename T, int W>
 void start(PromptArgs a, hipStream_t stream) {
-    a.tiles = (a.rows_q + 32 * W - 1) / (32 * W) + a.seqs;
+    const int tiles = (int)(((int64_t)a.rows_q * a.group + 32 * W - 1) / (32 * W)) + a.seqs;
     const size_t lds = 2 * bufs_of(D) * (size_t)(D == 256 ? 32 : 64) * D * 2 + (size_t)q_lds_of(D) * 1024 * W;
-    hipLaunchKernelGGL((attention_prompt_kernel<D, T, W>), dim3((unsigned)a.tiles, (unsigned)a.heads), dim3(64 * W), lds, stream, a);
+    hipLaunchKernelGGL((attention_prompt_kernel<D, T, W>), dim3((unsigned)tiles, (unsigned)(a.heads / a.group)), dim3(64 * W), lds, stream, a);
 }
 
 template <typename T>
 void start(const PromptArgs& a, int d, hipStream_t stream) {
-    const bool few = ((a.rows_q + 255) / 256) * a.heads < 512;
+    const bool few = (int64_t)a.rows_q * a.heads < 512 * 256;
     if (d == 64) few ? start<64, T, 4>(a, stream) : start<64, T, 8>(a, stream);
     else if (d == 128) few ? start<128, T, 4>(a, stream) : start<128, T, 8>(a, stream);
     else few ? start<256, T, 4>(a, stream) : start<256, T, 8>(a, stream);
@@ -406,7 +408,7 @@ hipError_t launch_attention_prompt(const pq2_attention_prompt_args& a, hipStream
                        static_cast<const uint16_t*>(a.v), static_cast<uint16_t*>(a.out), a.q_stride, a.q_head, a.k_stride,
                        a.k_head, a.v_stride, a.v_head, a.out_stride, a.out_head, a.starts_q, a.starts_k, (int)a.rows_q,
                        (int)a.rows_k, (int)a.seqs, (int)a.heads, (int)(a.heads / a.kv_heads),
-                       (int)std::min<int64_t>(a.window, 0x40000000), a.causal, 0, scale2, kSlack / scale2};
+                       (int)std::min<int64_t>(a.window, 0x40000000), a.causal, scale2, kSlack / scale2};
     clear_stale_error();
     a.dtype == PQ2_F16 ? start<_Float16>(k, (int)a.head_dim, stream) : start<__bf16>(k, (int)a.head_dim, stream);
     return hipGetLastError();
