@@ -21,7 +21,7 @@ namespace {
 // Tiles of keys, and of values, in LDS; products that an operand is read ahead;
 // 16-column pieces of the queries in LDS instead of registers (of 256 columns: or a SIMD
 // holds one wave, which alone issues a vector instruction only every second time).
-constexpr int bufs_of(int d) { return d == 256 ? 2 : 4; }
+constexpr int bufs_of(int d, int waves) { return d == 256 || waves == 4 ? 2 : 4; }
 constexpr int ahead_of(int d) { return d == 256 ? 3 : 4; }
 constexpr int q_lds_of(int d) { return d == 256 ? 8 : 0; }
 constexpr float kLog2e = 1.4426950408889634f;
@@ -144,7 +144,7 @@ __global__ __launch_bounds__(64 * W, 2) void attention_prompt_kernel(PromptArgs 
     constexpr int TILE = KT * D * 2;             // bytes of a tile in LDS
     constexpr int LOADS = TILE / 1024 / W;       // 1 KB loads of a wave for a tile
     constexpr int LROWS = 512 / D;               // rows of such a load
-    constexpr int kBufs = bufs_of(D), kAhead = ahead_of(D), QR = D / 16 - q_lds_of(D);  // QR: pieces of q in registers
+    constexpr int kBufs = bufs_of(D, W), kAhead = ahead_of(D), QR = D / 16 - q_lds_of(D);  // QR: pieces of q in registers
     extern __shared__ uint4 lds[];               // kBufs K tiles, kBufs V tiles, pieces of q
 
     // A key-value head's tiles follow each other on an XCD.
@@ -388,16 +388,21 @@ __global__ __launch_bounds__(64 * W, 2) void attention_prompt_kernel(PromptArgs 
 template <int D, typename T, int W>
 void start(PromptArgs a, hipStream_t stream) {
     const int tiles = (int)(((int64_t)a.rows_q * a.group + 32 * W - 1) / (32 * W)) + a.seqs;
-    const size_t lds = 2 * bufs_of(D) * (size_t)(D == 256 ? 32 : 64) * D * 2 + (size_t)q_lds_of(D) * 1024 * W;
+    const size_t lds = 2 * bufs_of(D, W) * (size_t)(D == 256 ? 32 : 64) * D * 2 + (size_t)q_lds_of(D) * 1024 * W;
     hipLaunchKernelGGL((attention_prompt_kernel<D, T, W>), dim3((unsigned)tiles, (unsigned)(a.heads / a.group)), dim3(64 * W), lds, stream, a);
 }
 
+// Workgroups of four waves, of which several share a compute unit (one starts
+// while another computes), or of eight, one a unit, which read each tile of keys for twice
+// the rows. us with four / eight, 40 heads of 128: 24 prompts of 500 tokens 134 / 155, one of 2048 58 / 63,
+// of 8192 662 / 644; 24 heads of 256 (four: one workgroup a unit all the same):
+// 1024 tokens 41 / 57, 2048 98 / 96, 8192 1201 / 989; 40 heads of 64: 8192 tokens 380 / 410.
 template <typename T>
 void start(const PromptArgs& a, int d, hipStream_t stream) {
-    const bool few = (int64_t)a.rows_q * a.heads < 512 * 256;
-    if (d == 64) few ? start<64, T, 4>(a, stream) : start<64, T, 8>(a, stream);
-    else if (d == 128) few ? start<128, T, 4>(a, stream) : start<128, T, 8>(a, stream);
-    else few ? start<256, T, 4>(a, stream) : start<256, T, 8>(a, stream);
+    const int64_t rows = (int64_t)a.rows_q * a.heads;
+    if (d == 64) start<64, T, 4>(a, stream);
+    else if (d == 128) rows >= 128 << 10 && a.rows_k >= (int64_t)4096 * a.seqs ? start<128, T, 8>(a, stream) : start<128, T, 4>(a, stream);
+    else rows >= 48 << 10 ? start<256, T, 8>(a, stream) : start<256, T, 4>(a, stream);
 }
 
 }  // namespace
