@@ -265,6 +265,16 @@ def test_attention_paged_strides_bad_pages_bounds(d, dt):
     within(*paged_case([800, 40], [1, 2], 4, 1, d, 32, dt, 0, scale=3.0), "sharp softmax")
 
 
+@pytest.mark.parametrize("dt,d", [("bf16", 128), ("f16", 64)])
+def test_attention_paged_many_sequences(dt, d):
+    """More sequences than one group of 64 workgroups' places; some empty, some long."""
+    announce(f"paged many sequences d={d} {dt}")
+    lengths = [(7 * i * i) % 300 for i in range(150)]
+    lengths[3], lengths[70], lengths[149] = 5000, 2600, 4100
+    new = [1 + i % 3 if i % 11 else 0 for i in range(150)]
+    within(*paged_case(lengths, new, 4, 2, d, 16, dt, 0, max_new=3), "o")
+
+
 def test_attention_paged_rows_do_not_depend_on_the_batch():
     announce("paged batch invariance")
     pq2 = _pq2()
@@ -348,6 +358,21 @@ PROMPTS = [
 @pytest.mark.parametrize("nq,nk,heads,kv,dt,causal,window", PROMPTS)
 def test_attention_prompt(nq, nk, heads, kv, dt, causal, window, d):
     announce(f"prompt nq={nq[:6]} nk={nk[:6]} heads={heads}/{kv} d={d} {dt} causal={causal} window={window}")
+    within(*prompt_case(nq, nk, heads, kv, d, dt, causal, window, seed=d), "o")
+
+
+@pytest.mark.parametrize("nq,nk,heads,kv,d,dt,causal,window", [
+    ([4200], [4200], 32, 2, 128, "bf16", True, 0),
+    ([4100, 100], [8300, 133], 32, 4, 128, "f16", True, 3000),
+    ([4100], [4133], 33, 3, 128, "bf16", False, 0),
+    ([2000, 0, 77, 333], [2100, 5, 77, 300], 24, 4, 256, "f16", True, 0),
+    ([900, 1300], [1000, 1300], 24, 3, 256, "bf16", True, 500),
+    ([2200], [40], 24, 2, 256, "bf16", False, 0),
+    ([3000], [3000], 16, 16, 64, "bf16", True, 0),
+])
+def test_attention_prompt_large(nq, nk, heads, kv, d, dt, causal, window):
+    """The workgroups of eight waves, many steps."""
+    announce(f"prompt large nq={nq} nk={nk} heads={heads}/{kv} d={d} {dt} causal={causal} window={window}")
     within(*prompt_case(nq, nk, heads, kv, d, dt, causal, window, seed=d), "o")
 
 
