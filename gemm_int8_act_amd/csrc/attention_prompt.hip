@@ -63,7 +63,7 @@ template <int D>
 __device__ __forceinline__ int k_chunk(int r, int c) { return r * (D / 8) + (c ^ (r & 7)); }
 template <int D>
 __device__ __forceinline__ int v_chunk(int r, int c) {
-    return r * (D / 8) + (c ^ (D == 64 ? ((r >> 1) & 1) << 2 : (r & 3) << 2));
+    return r * (D / 8) + (c ^ ((D == 64 ? ((r >> 1) & 1) << 2 : (r & 3) << 2) | ((r >> 2) & 1) << 1));
 }
 
 __device__ __forceinline__ float max_halves(float v) {
@@ -229,7 +229,7 @@ __global__ __launch_bounds__(64 * W, 2) void attention_prompt_kernel(PromptArgs 
 #pragma unroll
         for (int x = 0; x < (DB < 4 ? DB : 4); ++x)
             vat[x] = (lds_char*)lds + kBufs * TILE + (4 * half + r3) * RB +
-                     16 * (4 * (x ^ swz) + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1)) + 8 * (lane & 1);
+                     16 * (4 * (x ^ swz) + 2 * (((lane >> 4) & 1) ^ half) + ((lane & 3) >> 1)) + 8 * (lane & 1);
     }
     auto operand = [&](int i, int buf) -> v8 {
         if (i < PV) {
