@@ -178,18 +178,19 @@ __device__ __forceinline__ void join(const PagedArgs& a, float* first, int count
 
 // A sequence as its tiles of `rows` query rows see it: all are split into parts
 // of `chunk` keys, the one that sees most into `parts` (at least one; none
-// without new tokens).
+// without new tokens).  Keys end at `end`, the length or what the table holds.
 struct Sequence {
-    int len, start, n, chunk, parts;
+    int len, end, start, n, chunk, parts;
 };
 
 __device__ __forceinline__ Sequence sequence(const PagedArgs& a, int seq, int rows) {
     Sequence s;
-    s.len = max(0, (int)min((int64_t)a.lens[seq], (int64_t)a.table_pages << a.page_shift));
+    s.len = max(0, a.lens[seq]);
+    s.end = min(s.len, a.table_pages << a.page_shift);
     s.start = a.starts ? a.starts[seq] : seq;
     s.n = a.starts ? a.starts[seq + 1] - s.start : 1;
     // Of a window: the rows' own distance, and the alignment to 16 keys.
-    const int most = a.window ? (int)min((int64_t)s.len, (int64_t)a.window + (rows + a.group - 1) / a.group + 16) : s.len;
+    const int most = a.window ? (int)min((int64_t)s.end, (int64_t)a.window + (rows + a.group - 1) / a.group + 16) : s.end;
     s.chunk = max(a.min_chunk, (((most + a.splits - 1) >> a.split_shift) + kStep - 1) & ~(kStep - 1));
     // (most - 1) / chunk, below 128: the reciprocal's quotient is off by one at most.
     int p = (int)((float)(most - 1) * __builtin_amdgcn_rcpf((float)s.chunk));
@@ -227,7 +228,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 || RT > 1 ? 2 : D == 128 ? 3 
     // starts for nothing takes the dispatcher 2.4 ns, behind the others.
     const int head_tile = blockIdx.x % (a.kv_heads * a.row_tiles), item = blockIdx.x / (a.kv_heads * a.row_tiles);
     const int rt = head_tile % a.row_tiles, kvh = head_tile / a.row_tiles, s0 = blockIdx.y * 64;
-    Sequence own_seq{0, 0, 0, 1, 0};
+    Sequence own_seq{0, 0, 0, 0, 1, 0};
     if (s0 + lane < a.seqs) own_seq = sequence(a, s0 + lane, ROWS);
     const int sums = scan(own_seq.parts);
     if (item >= __builtin_amdgcn_readlane(sums, 63)) return;
@@ -236,15 +237,16 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 || RT > 1 ? 2 : D == 128 ? 3 
 
     // The sequence, this tile's rows and the keys that any of them sees.
     own_seq.len = __builtin_amdgcn_readlane(own_seq.len, at);
+    own_seq.end = __builtin_amdgcn_readlane(own_seq.end, at);
     own_seq.start = __builtin_amdgcn_readlane(own_seq.start, at);
     own_seq.n = __builtin_amdgcn_readlane(own_seq.n, at);
     own_seq.chunk = __builtin_amdgcn_readlane(own_seq.chunk, at);
-    const int len = own_seq.len, start = own_seq.start, nq = min(own_seq.n, a.max_new);
+    const int end = own_seq.end, start = own_seq.start, nq = min(own_seq.n, a.max_new);
     const int r0 = rt * ROWS, i0 = r0 / a.group;
     if (i0 >= nq) return;
     const int i1 = min(nq - 1, (r0 + ROWS - 1) / a.group);
-    const int first = len - own_seq.n;  // the first new token's position
-    const int hi = min(len, first + i1 + 1);
+    const int first = own_seq.len - own_seq.n;  // the first new token's position
+    const int hi = min(end, first + i1 + 1);
     const int lo = a.window ? max(0, first + i0 - a.window + 1) & ~15 : 0;
     const int span = max(0, hi - lo), parts = max(1, (span + own_seq.chunk - 1) / own_seq.chunk);
     if (split >= parts) return;
@@ -262,7 +264,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 || RT > 1 ? 2 : D == 128 ? 3 
     for (int t = 0; t < RT; ++t) {
         const int r = r0 + 16 * t + j, i = r / a.group, g = r - i * a.group;
         const bool valid = i < nq && start + i >= 0 && start + i < a.rows;
-        seen_hi[t] = valid ? min(len, first + i + 1) : 0;
+        seen_hi[t] = valid ? min(end, first + i + 1) : 0;
         seen_lo[t] = a.window ? first + i - a.window + 1 : 0;
         const uint16_t* q = a.q + (int64_t)(valid ? start + i : 0) * a.q_stride + (int64_t)(kvh * a.group + (valid ? g : 0)) * a.q_head + 16 * kb;
         T8 x[D / 32];
@@ -545,6 +547,8 @@ PagedPlan paged_plan(int64_t seqs, int64_t max_new, int64_t heads, int64_t kv_he
     p.splits = std::max(fill / base, (max_len + 2047) / 2048);
     p.splits = std::max<int64_t>(1, std::min({p.splits, (max_len + 255) / 256, (int64_t)kMaxSplits}));
     p.splits = (int64_t)1 << log2_of(p.splits);
+    // (A launch holds fewer than 2^32 threads along x.)
+    while (p.splits > 1 && kv_heads * p.row_tiles * p.splits * std::min<int64_t>(seqs, 64) > 1 << 23) p.splits >>= 1;
     p.min_chunk = base >= fill ? 2048 : base >= fill / 4 ? 1024 : base >= fill / 16 ? 512 : 256;
     p.partial_floats = p.splits > 1 ? base * p.splits * p.rows * (head_dim + 2) : 0;
     p.counter_words = p.splits > 1 ? base * kTileCounters : 0;

@@ -175,7 +175,7 @@ def test_kv_read_bits(lengths, kv, d, page, out):
 
 # ---------------------------------------------------------------- attention over the pages
 def paged_case(lengths, new, heads, kv, d, page, dt, window, seed=0, spare=3, max_len=None, max_new=None, garbage=True, strided=False,
-               bad_page=False, scale=None):
+               bad_page=False, scale=None, table_pages=None):
     """(got, want, bound) of one call; what the pages hold behind a length is garbage with NaN scales."""
     pq2 = _pq2()
     width = max(1, max((max(n, 0) + page - 1) // page for n in lengths))
@@ -192,6 +192,8 @@ def paged_case(lengths, new, heads, kv, d, page, dt, window, seed=0, spare=3, ma
                     vs[int(table[i, p]), :, first:] = float("inf")
     if bad_page:
         table[0, 0], table[-1, -1] = -1, pages
+    if table_pages:
+        table = table[:, :table_pages]              # lengths go beyond what the table holds
     starts = starts_of(new)
     rows = sum(new)
     q = randn((rows, heads, d), seed, 1.5).to(DT[dt]).to(DEV)
@@ -263,6 +265,8 @@ def test_attention_paged_strides_bad_pages_bounds(d, dt):
     within(*paged_case([6000, 3], [1, 1], 4, 2, d, 32, dt, 0, max_len=600), "beyond max_len")
     within(*paged_case([600, 3], [1, 1], 4, 2, d, 32, dt, 0, max_len=100000, max_new=5), "roomy workspace")
     within(*paged_case([800, 40], [1, 2], 4, 1, d, 32, dt, 0, scale=3.0), "sharp softmax")
+    within(*paged_case([700, 100, 490], [4, 3, 2], 4, 2, d, 16, dt, 0, table_pages=30), "beyond the table")
+    within(*paged_case([700, 100, 490], [4, 3, 2], 4, 2, d, 16, dt, 250, table_pages=30), "beyond the table, window")
 
 
 @pytest.mark.parametrize("dt,d", [("bf16", 128), ("f16", 64)])
@@ -486,6 +490,31 @@ def test_captured_and_replayed():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(cache, eager_cache) and torch.equal(out, eager), turn
+
+
+def test_two_calls_at_once():
+    """Calls on two streams, each with a workspace of its own, beside each other."""
+    announce("two paged calls at once")
+    pq2 = _pq2()
+    heads, kv, d, page, n = 16, 2, 128, 16, 20000
+    cache = ref.make_cache(1300, page, kv, d, 1, DEV)
+    table = torch.arange(1250, dtype=torch.int32, device=DEV).view(1, 1250)
+    floats, words = pq2.pq2_attention_paged_workspace(1, 1, heads, kv, d, n)
+    lens = ints([n])
+    q = [randn((1, heads, d), i).bfloat16().to(DEV) for i in range(2)]
+    work = [(torch.empty(floats, device=DEV), torch.zeros(words, dtype=torch.int32, device=DEV)) for _ in range(2)]
+    want = [torch.empty_like(x) for x in q]
+    for i in range(2):
+        pq2.pq2_attention_paged(q[i], cache, table, lens, page, want[i], *work[i])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[torch.zeros_like(x) for _ in range(20)] for x in q]
+    torch.cuda.synchronize()
+    for turn in range(20):
+        for i in range(2):
+            pq2.pq2_attention_paged(q[i], cache, table, lens, page, got[i][turn], *work[i], stream=streams[i])
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, want[i]) for i in range(2) for x in got[i])
 
 
 def test_other_stream():
