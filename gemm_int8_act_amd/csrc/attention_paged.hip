@@ -226,8 +226,10 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 || RT > 1 ? 2 : D == 128 ? 3 
     // blockIdx.x counts the parts that there are, of 64 sequences at blockIdx.y:
     // only the lengths tell how many, the grid is for the most, and a workgroup that
     // starts for nothing takes the dispatcher 2.4 ns, behind the others.
-    const int head_tile = blockIdx.x % (a.kv_heads * a.row_tiles), item = blockIdx.x / (a.kv_heads * a.row_tiles);
-    const int rt = head_tile % a.row_tiles, kvh = head_tile / a.row_tiles, s0 = blockIdx.y * 64;
+    // Workgroups go to the eight XCDs in turn: the row tiles that read the same
+    // keys follow each other on one of them.
+    const uint32_t turn = blockIdx.x >> 3, place = turn / a.row_tiles * 8 + (blockIdx.x & 7);
+    const int rt = turn % a.row_tiles, kvh = place % a.kv_heads, item = place / a.kv_heads, s0 = blockIdx.y * 64;
     Sequence own_seq{0, 0, 0, 0, 1, 0};
     if (s0 + lane < a.seqs) own_seq = sequence(a, s0 + lane, ROWS);
     const int sums = scan(own_seq.parts);
@@ -525,7 +527,8 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 || RT > 1 ? 2 : D == 128 ? 3 
 
 template <int D, typename T>
 void start(const PagedArgs& a, int64_t seqs, hipStream_t stream) {
-    const dim3 grid((unsigned)(a.kv_heads * a.row_tiles * a.splits * std::min<int64_t>(seqs, 64)), (unsigned)((seqs + 63) / 64));
+    const int64_t places = a.kv_heads * a.splits * std::min<int64_t>(seqs, 64);
+    const dim3 grid((unsigned)((places + 7) / 8 * 8 * a.row_tiles), (unsigned)((seqs + 63) / 64));
     if (D == 256 || a.tile_rows <= kRows) hipLaunchKernelGGL((attention_paged_kernel<D, T, 1>), grid, dim3(64 * kWaves), 0, stream, a);
     else hipLaunchKernelGGL((attention_paged_kernel<D, T, D == 256 ? 1 : 2>), grid, dim3(64 * kWaves), 0, stream, a);
 }
