@@ -221,7 +221,7 @@ int pq2_attention_prompt(const pq2_attention_prompt_args* a, void* stream) {
     const int64_t d = a->head_dim;
     if (a->rows_q < 1 || a->rows_q > PQ2_MAX_ATTN_ROWS || a->rows_k < 1 || a->rows_k > PQ2_MAX_ATTN_ROWS ||
         a->seqs < 1 || a->seqs > PQ2_MAX_ATTN_SEQS || !heads_ok(a->heads, a->kv_heads) || !dim_ok(d) ||
-        a->rows_q * (a->heads / a->kv_heads) > kMaxIndex)
+        a->rows_q * (a->heads / a->kv_heads) > (int64_t)1 << 30)
         return PQ2_ESHAPE;
     const struct {
         const void* p;

@@ -6,7 +6,10 @@
 // and the arithmetic between (a rotation, a maximum over the row, eight
 // quotients a lane) hides behind memory for many tokens.  For one token the
 // time is the launch and two dependent trips to memory (position, then its row
-// of the tables; the row itself loads meanwhile).
+// of the tables; the row itself loads meanwhile).  Measured: 4096 tokens of 64 + 8 +
+// 8 heads of 128 from FP32, q, k and v out in bf16, 48.5 us (265 MB, 5.4 TB/s);
+// 32768 tokens of 8 heads of 128 read back to bf16 41 to 47 us (203 MB, 4.3 to 5.0 TB/s);
+// one token 3 us either way.
 #include "attention_internal.h"
 
 #include <algorithm>
@@ -239,7 +242,9 @@ hipError_t launch_kv_write(const pq2_kv_write_args& a, hipStream_t stream) {
                 (int)a.rot_dim, (int)a.table_rows - 1, 1, a.cache ? log2_of(a.page_tokens) : 0,
                 a.cache ? a.pages * a.page_tokens : 0, a.in_dtype, a.out_dtype, a.interleaved};
     // Few tokens: one row a group of lanes, so that nothing waits for a second
-    // trip to memory.  Many: a workgroup a token, the tables read once.
+    // trip to memory.  Many: a workgroup a token, the tables read once (two or
+    // four rows of a group in flight were slower: 83 and 80 us against 68 for 4096
+    // tokens and their read-back, with fewer waves a SIMD).
     if (a.m < 512) k.parts = (rows + groups - 1) / groups;
     clear_stale_error();
     if (a.head_dim == 64) start_write<64>(k, stream);

@@ -123,8 +123,9 @@ int pq2_kv_read(const pq2_kv_read_args* args, void* stream);
  *                                               and j > p - window if window > 0
  *
  * with k_j and v_j as their codes and scales give them.  Sums and the softmax
- * are FP32; out is rounded once.  A row's bits depend on its sequence's
- * length and the call's sizes, not on the other sequences.
+ * are FP32, weights meet values with 16 bits, elements of q below 2^-14 of their row's
+ * largest are rounded to multiples of 2^-24 of it; out is rounded once.  A row's bits depend on its
+ * sequence's length and the call's sizes, not on the other sequences.
  *  - A row that sees no key is zero.
  *  - Keys in pages outside the cache are not seen, nor those beyond the table.
  *  - What the pages hold behind a sequence's length has no influence.
@@ -196,8 +197,8 @@ typedef struct pq2_attention_prompt_args {
     int causal;               /* 0 or 1                                                          */
 } pq2_attention_prompt_args;
 
-/* Errors: EINVAL (null, dtype, causal, scale, window < 0 or without causal, overlap), ESHAPE, EALIGN, ELAUNCH,
- *         EDEVICE. */
+/* Errors: EINVAL (null, dtype, causal, scale, window < 0 or without causal, overlap), ESHAPE (sizes; rows_q * heads /
+ *         kv_heads > 2^30), EALIGN, ELAUNCH, EDEVICE. */
 int pq2_attention_prompt(const pq2_attention_prompt_args* args, void* stream);
 
 #ifdef __cplusplus

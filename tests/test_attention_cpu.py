@@ -206,7 +206,7 @@ REFUSED = {
         (EINVAL, dict(q=0)), (EINVAL, dict(k=0)), (EINVAL, dict(v=0)), (EINVAL, dict(out=0)), (EINVAL, dict(starts_q=0)),
         (EINVAL, dict(starts_k=0)), (EINVAL, dict(dtype=2)), (EINVAL, dict(causal=2)), (EINVAL, dict(scale=0.0)),
         (EINVAL, dict(scale=float("inf"))), (EINVAL, dict(window=-5)), (EINVAL, dict(window=5, causal=0)), (ESHAPE, dict(rows_q=0)),
-        (ESHAPE, dict(rows_k=0)), (ESHAPE, dict(rows_q=(1 << 24) + 1)), (ESHAPE, dict(seqs=0)), (ESHAPE, dict(seqs=65536)),
+        (ESHAPE, dict(rows_k=0)), (ESHAPE, dict(rows_q=(1 << 24) + 1)), (ESHAPE, dict(rows_q=1 << 24, heads=128, kv_heads=1, q_stride=1 << 14, out_stride=1 << 14)), (ESHAPE, dict(seqs=0)), (ESHAPE, dict(seqs=65536)),
         (ESHAPE, dict(heads=5)), (ESHAPE, dict(head_dim=160)), (ESHAPE, dict(k_stride=200)), (ESHAPE, dict(v_stride=1 << 24)),
         (EALIGN, dict(v_stride=260)), (EALIGN, dict(k=B + 2)), (EALIGN, dict(out=D + 8)), (EALIGN, dict(starts_q=E + 2)),
         (EINVAL, dict(out=A)), (EINVAL, dict(out=B)), (EINVAL, dict(out=C)), (EINVAL, dict(out=F)),

@@ -138,6 +138,10 @@ READS = [
     ([31] * 70 + [0] * 70 + [3], 1, 128, 16, "bf16"),
     ([300], 4, 256, 256, "f32"),
     ([0, 77, 12], 5, 256, 64, "bf16"),
+    # two rows a lane
+    ([3000, 0, 2300], 8, 128, 16, "bf16"),
+    ([2100, 1, 33], 8, 256, 64, "f32"),
+    ([9001, 77], 8, 64, 32, "f16"),
 ]
 
 
@@ -490,6 +494,75 @@ def test_captured_and_replayed():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(cache, eager_cache) and torch.equal(out, eager), turn
+
+
+def test_offsets_beyond_32_bits():
+    """A cache of more than 4 GiB, its last pages used, and keys whose rows are 16 MiB apart."""
+    announce("offsets beyond 32 bits")
+    pq2 = _pq2()
+    heads, kv, d, page, n = 8, 4, 256, 256, 700
+    big = torch.empty((9000, pq2.pq2_kv_page_bytes(page, kv, d)), dtype=torch.uint8, device=DEV)
+    small = torch.zeros((4, big.shape[1]), dtype=torch.uint8, device=DEV)
+    big[-4:] = 0
+    assert big.numel() > 1 << 32
+    k, v, q = (randn((n, h, d), i).half().to(DEV) for i, h in enumerate((kv, kv, heads)))
+    t = torch.arange(n, device=DEV, dtype=torch.int32)
+    got = []
+    for cache, first in ((small, 0), (big, 8996)):
+        pq2.pq2_kv_write(k, v, cache, t + first * page, page)
+        table = torch.arange(4, dtype=torch.int32, device=DEV).view(1, 4) + first
+        out = torch.empty_like(q[-3:])
+        pq2.pq2_attention_paged(q[-3:], cache, table, ints([n]), page, out, starts=ints([0, 3]), max_new=3, max_len=n,
+                                partials=torch.empty(1 << 20, device=DEV), counters=torch.zeros(4096, dtype=torch.int32, device=DEV))
+        back = [torch.empty((n, kv, d), device=DEV) for _ in "kv"]
+        pq2.pq2_kv_read(cache, table, starts_of([n]), page, *back)
+        got.append([out, *back])
+    torch.cuda.synchronize()
+    assert torch.equal(small, big[-4:]) and all(torch.equal(a, b) for a, b in zip(*got))
+    del big
+    wide = torch.empty((300, 1 << 23), dtype=torch.half, device=DEV)
+    far = wide[:, 512:512 + kv * d].unflatten(1, (kv, d))
+    far.copy_(k[:300])
+    s = starts_of([300])
+    outs = [torch.empty_like(q[:300]) for _ in range(2)]
+    pq2.pq2_attention_prompt(q[:300], k[:300], v[:300], outs[0], s, s)
+    pq2.pq2_attention_prompt(q[:300], far, v[:300], outs[1], s, s)
+    torch.cuda.synchronize()
+    assert torch.equal(*outs)
+
+
+def test_prompt_captured_and_replayed():
+    announce("captured prompt")
+    pq2 = _pq2()
+    heads, kv, d, page = 4, 2, 128, 16
+    cache = ref.make_cache(60, page, kv, d, 1, DEV)
+    table = torch.arange(60, dtype=torch.int32, device=DEV).view(2, 30)
+    k, v = (torch.empty((900, kv, d), dtype=torch.bfloat16, device=DEV) for _ in "kv")
+    q = torch.empty((700, heads, d), dtype=torch.bfloat16, device=DEV)
+    out = torch.zeros_like(q)
+    starts_q, starts_k = (torch.zeros(3, dtype=torch.int32, device=DEV) for _ in range(2))
+
+    def step(k, v, out):
+        pq2.pq2_kv_read(cache, table, starts_k, page, k, v)
+        pq2.pq2_attention_prompt(q, k, v, out, starts_q, starts_k)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(k, v, out)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(k, v, out)
+    for turn, (a, b) in enumerate((([300, 400], [450, 450]), ([1, 0], [1, 0]), ([0, 700], [0, 480]))):
+        q.copy_(randn(q.shape, turn))
+        starts_q.copy_(starts_of(a))
+        starts_k.copy_(starts_of(b))
+        eager = [k.clone(), v.clone(), out.clone()]
+        step(*eager)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip((k, v, out), eager)), turn
 
 
 def test_two_calls_at_once():
