@@ -135,11 +135,22 @@ __device__ __forceinline__ int sequence_at(const int32_t* starts, int group, int
     }
 }
 
-// Workgroups go to the eight XCDs in turn: the one at `id` takes the item at
-// which its XCD's share, a stretch of neighbouring items, has come.
-__device__ __forceinline__ int item_of(int id, int total) {
-    const int xcd = id & 7, share = total >> 3, more = total & 7;
-    return xcd * share + min(xcd, more) + (id >> 3);
+// Workgroups go to the eight XCDs in turn.  Each XCD takes one key-value head
+// after the other, so that its keys and values stay in the XCD's L2, or, of fewer than eight
+// heads, every 8 / kv_heads th tile of one (the longest tiles come first, so a stretch of
+// them would be more work than the next); where that does not divide, tiles are dealt out in
+// turn.
+struct Item {
+    int kvh, place;
+};
+__device__ __forceinline__ Item item_of(int id, int tiles, int kv_heads) {
+    const int xcd = id & 7, turn = id >> 3;
+    if (kv_heads <= 8 && 8 % kv_heads == 0) {
+        const int share = 8 / kv_heads;
+        return {xcd / share, turn * share + xcd % share};
+    }
+    if (kv_heads % 8 == 0) return {turn / tiles * 8 + xcd, turn % tiles};
+    return {id % kv_heads, id / kv_heads};
 }
 
 template <int D, typename T, int W>
@@ -156,9 +167,8 @@ __global__ __launch_bounds__(64 * W, 2) void attention_prompt_kernel(PromptArgs 
     constexpr int kBufs = bufs_of(D, W), kAhead = ahead_of(D), QR = D / 16 - q_lds_of(D);  // QR: pieces of q in registers
     extern __shared__ uint4 lds[];               // kBufs K tiles, kBufs V tiles, pieces of q
 
-    // A key-value head's tiles follow each other on an XCD.
-    const int item = item_of(blockIdx.y * gridDim.x + blockIdx.x, gridDim.x * gridDim.y);
-    const int kvh = item / gridDim.x, place = item % gridDim.x;
+    const Item item = item_of(blockIdx.y * gridDim.x + blockIdx.x, gridDim.x, gridDim.y);
+    const int kvh = item.kvh, place = item.place;
     const int seq = a.seqs == 1 ? 0 : sequence_at<BM>(a.starts_q, a.group, a.seqs, place);
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int row = lane & 31, half = lane >> 5;
@@ -397,7 +407,8 @@ __global__ __launch_bounds__(64 * W, 2) void attention_prompt_kernel(PromptArgs 
 
 template <int D, typename T, int W>
 void start(PromptArgs a, hipStream_t stream) {
-    const int tiles = (int)(((int64_t)a.rows_q * a.group + 32 * W - 1) / (32 * W)) + a.seqs;
+    // (A multiple of eight, for shares of any size.)
+    const int tiles = ((int)(((int64_t)a.rows_q * a.group + 32 * W - 1) / (32 * W)) + a.seqs + 7) & ~7;
     const size_t lds = 2 * bufs_of(D, W) * (size_t)(D == 256 ? 32 : 64) * D * 2 + (size_t)q_lds_of(D) * 1024 * W;
     hipLaunchKernelGGL((attention_prompt_kernel<D, T, W>), dim3((unsigned)tiles, (unsigned)(a.heads / a.group)), dim3(64 * W), lds, stream, a);
 }
