@@ -417,13 +417,13 @@ void start(PromptArgs a, hipStream_t stream) {
 // while another computes), or of eight, one a unit, which read each tile of keys for twice
 // the rows. us with four / eight, 40 heads of 128: 24 prompts of 500 tokens 134 / 155, one of 2048 58 / 63,
 // of 8192 662 / 644; 24 heads of 256 (four: one workgroup a unit all the same):
-// 1024 tokens 41 / 57, 2048 98 / 96, 8192 1201 / 989; 40 heads of 64: 8192 tokens 380 / 410.
+// one of 1024 40 / 56, of 2048 71 / 97, four of 1500 151 / 145, 24 of 500 171 / 156; 40 heads of 64: 8192 tokens 380 / 410.
 template <typename T>
 void start(const PromptArgs& a, int d, hipStream_t stream) {
     const int64_t rows = (int64_t)a.rows_q * a.heads;
     if (d == 64) start<64, T, 4>(a, stream);
     else if (d == 128) rows >= 128 << 10 && a.rows_k >= (int64_t)4096 * a.seqs ? start<128, T, 8>(a, stream) : start<128, T, 4>(a, stream);
-    else rows >= 48 << 10 ? start<256, T, 8>(a, stream) : start<256, T, 4>(a, stream);
+    else rows >= 64 << 10 ? start<256, T, 8>(a, stream) : start<256, T, 4>(a, stream);
 }
 
 }  // namespace

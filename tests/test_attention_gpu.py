@@ -373,9 +373,9 @@ def test_attention_prompt(nq, nk, heads, kv, dt, causal, window, d):
     ([4200], [4200], 32, 2, 128, "bf16", True, 0),
     ([4100, 100], [8300, 133], 32, 4, 128, "f16", True, 3000),
     ([4100], [4133], 33, 3, 128, "bf16", False, 0),
-    ([2000, 0, 77, 333], [2100, 5, 77, 300], 24, 4, 256, "f16", True, 0),
-    ([900, 1300], [1000, 1300], 24, 3, 256, "bf16", True, 500),
-    ([2200], [40], 24, 2, 256, "bf16", False, 0),
+    ([2400, 0, 77, 333], [2500, 5, 77, 300], 24, 4, 256, "f16", True, 0),
+    ([900, 1900], [1000, 1900], 24, 3, 256, "bf16", True, 500),
+    ([2900], [40], 24, 2, 256, "bf16", False, 0),
     ([3000], [3000], 16, 16, 64, "bf16", True, 0),
 ])
 def test_attention_prompt_large(nq, nk, heads, kv, d, dt, causal, window):
