@@ -11,9 +11,9 @@
 // one value a lane.  K and V tiles go straight into LDS, rows swizzled by
 // 16-byte chunks; the values' operand is read transposed (ds_read_b64_tr_b16).
 //
-// Bound: the matrix cores (52 % of their cycles on 8192 tokens, 40 heads of
-// 128: 640 to 666 us, 1.03 to 1.07 PFLOP/s, 84 % of what a large library product reaches)
-// beside the softmax (40 % of the vector cycles) and LDS (39 %); short prompts by the
+// Bound: the matrix cores (53 % of their cycles on 8192 tokens, 40 heads of
+// 128: 640 to 666 us, 1.03 to 1.07 PFLOP/s, 82 to 84 % of what a large library product reaches;
+// 24 heads of 256 760 us, 1.08 PFLOP/s) beside the softmax (41 % of the vector cycles) and LDS (40 %); short prompts by the
 // 7 us that a workgroup's start and end take.  A step's three pieces of work are
 // independent and laid out instruction by instruction, so that matrix and
 // vector units of a SIMD work at once and no read of LDS is waited for; left to
