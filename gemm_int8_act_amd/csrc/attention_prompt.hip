@@ -20,6 +20,8 @@
 // the compiler's order the same step took 710 instead of 656 us.
 #include "attention_internal.h"
 
+#include <float.h>
+
 #include <algorithm>
 #include <utility>
 
@@ -430,11 +432,13 @@ void start(const PromptArgs& a, int d, hipStream_t stream) {
 
 hipError_t launch_attention_prompt(const pq2_attention_prompt_args& a, hipStream_t stream) {
     const float scale2 = a.scale * kLog2e;
+    // (Finite: -inf + slack, for a row's first keys, is to stay -inf.)
+    const float slack = std::min(kSlack / scale2, FLT_MAX);
     const PromptArgs k{static_cast<const uint16_t*>(a.q), static_cast<const uint16_t*>(a.k),
                        static_cast<const uint16_t*>(a.v), static_cast<uint16_t*>(a.out), a.q_stride, a.q_head, a.k_stride,
                        a.k_head, a.v_stride, a.v_head, a.out_stride, a.out_head, a.starts_q, a.starts_k, (int)a.rows_q,
                        (int)a.rows_k, (int)a.seqs, (int)a.heads, (int)(a.heads / a.kv_heads),
-                       (int)std::min<int64_t>(a.window, 0x40000000), a.causal, scale2, kSlack / scale2};
+                       (int)std::min<int64_t>(a.window, 0x40000000), a.causal, scale2, slack};
     clear_stale_error();
     a.dtype == PQ2_F16 ? start<_Float16>(k, (int)a.head_dim, stream) : start<__bf16>(k, (int)a.head_dim, stream);
     return hipGetLastError();
