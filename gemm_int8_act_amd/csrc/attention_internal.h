@@ -4,20 +4,10 @@
 #pragma once
 
 #include "../../include/pq2_attention.h"
+#include "attention_plan.h"
 #include "block_internal.h"
 
 namespace pq2 {
-
-// Sizes of one paged call that its workspace follows from: `splits` parts of
-// a row's cache at most, row tiles of `rows` query rows (new tokens x grouped
-// heads) each, `row_tiles` of them a sequence and key-value head.
-struct PagedPlan {
-    int64_t splits, row_tiles, rows, min_chunk;
-    int64_t partial_floats, counter_words;
-};
-
-PagedPlan paged_plan(int64_t seqs, int64_t max_new, int64_t heads, int64_t kv_heads, int64_t head_dim,
-                     int64_t max_len);
 
 hipError_t launch_kv_write(const pq2_kv_write_args& a, hipStream_t stream);
 hipError_t launch_kv_read(const pq2_kv_read_args& a, hipStream_t stream);
@@ -27,12 +17,6 @@ hipError_t launch_attention_prompt(const pq2_attention_prompt_args& a, hipStream
 // Bytes of one key-value head's block of a page.
 __host__ __device__ constexpr int64_t kv_block_bytes(int64_t page_tokens, int64_t head_dim) {
     return page_tokens * (2 * head_dim + 8);
-}
-
-inline int log2_of(int64_t v) {
-    int s = 0;
-    while (((int64_t)1 << s) < v) ++s;
-    return s;
 }
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));

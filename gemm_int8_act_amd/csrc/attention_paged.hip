@@ -35,13 +35,11 @@ namespace {
 
 constexpr int kWaves = 4;
 constexpr int kTile = 32;                  // keys of a wave's step
+static_assert(64 * kWaves == kPagedThreads, "attention_plan.h");
 constexpr int kStep = kWaves * kTile;      // keys of a workgroup's step
-constexpr int kRows = 16;                  // query rows of a tile
-constexpr int kMaxSplits = 128;
-constexpr int kFan = 8;                    // parts that are joined first, of more than kJoin
+constexpr int kRows = kPagedRows;
 constexpr int kJoin = 16;                  // parts that are joined at once
 constexpr int kAgent = 16;                 // cache policy of a load or store at agent scope
-constexpr int kTileCounters = 1 + kMaxSplits / kFan;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 8.0f;             // weights grow to 2^8 before a row's reference moves
 
@@ -58,6 +56,7 @@ struct PagedArgs {
     int64_t table_stride;
     int rows, table_pages, kv_heads, group, pages, page_shift, max_new, window, splits, row_tiles, tile_rows, min_chunk;
     int seqs, split_shift;  // splits: a power of two
+    int few;                // places, if fewer than eight (0: more)
     float scale2;  // scale * log2(e)
 };
 
@@ -234,8 +233,13 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 || RT > 1 ? 2 : D == 128 ? 3 
     // only the lengths tell how many, the grid is for the most, and a workgroup that
     // starts for nothing takes the dispatcher 2.4 ns, behind the others.
     // Workgroups go to the eight XCDs in turn: the row tiles that read the same
-    // keys follow each other on one of them.
-    const uint32_t turn = blockIdx.x >> 3, place = turn / a.row_tiles * 8 + (blockIdx.x & 7);
+    // keys follow each other on one of them; those of fewer than eight places go to all.
+    uint32_t turn, place;
+    if (a.few) {
+        turn = blockIdx.x / a.few, place = blockIdx.x % a.few;
+    } else {
+        turn = blockIdx.x >> 3, place = turn / a.row_tiles * 8 + (blockIdx.x & 7);
+    }
     const int rt = turn % a.row_tiles, kvh = place % a.kv_heads, item = place / a.kv_heads, s0 = blockIdx.y * 64;
     Sequence own_seq{0, 0, 0, 0, 1, 0};
     if (s0 + lane < a.seqs) own_seq = sequence(a, s0 + lane, ROWS);
@@ -533,50 +537,27 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 || RT > 1 ? 2 : D == 128 ? 3 
 }
 
 template <int D, typename T>
-void start(const PagedArgs& a, int64_t seqs, hipStream_t stream) {
-    const int64_t places = a.kv_heads * a.splits * std::min<int64_t>(seqs, 64);
-    const dim3 grid((unsigned)((places + 7) / 8 * 8 * a.row_tiles), (unsigned)((seqs + 63) / 64));
+void start(const PagedArgs& a, int64_t workgroups, hipStream_t stream) {
+    const dim3 grid((unsigned)workgroups, (unsigned)((a.seqs + 63) / 64));
     if (D == 256 || a.tile_rows <= kRows) hipLaunchKernelGGL((attention_paged_kernel<D, T, 1>), grid, dim3(64 * kWaves), 0, stream, a);
     else hipLaunchKernelGGL((attention_paged_kernel<D, T, D == 256 ? 1 : 2>), grid, dim3(64 * kWaves), 0, stream, a);
 }
 
 }  // namespace
 
-PagedPlan paged_plan(int64_t seqs, int64_t max_new, int64_t heads, int64_t kv_heads, int64_t head_dim,
-                     int64_t max_len) {
-    PagedPlan p;
-    const int64_t rows = max_new * (heads / kv_heads);
-    const int64_t most = rows > kRows && head_dim != 256 ? 2 * kRows : kRows;
-    p.rows = std::min<int64_t>(rows, most);
-    p.row_tiles = (rows + most - 1) / most;
-    // Parts: as many as fill the chip (512 workgroups, 1024 of heads of 64), or
-    // of 2048 keys where a long sequence may stand among short ones. Measured:
-    // 128 instead of 64 parts of 131072 keys of one sequence 70 us against 61; parts of 1024 keys
-    // (64 sequences of 1 to 16384) 89 against 78.
-    const int64_t base = seqs * kv_heads * p.row_tiles, fill = head_dim == 64 ? 1024 : 512;
-    p.splits = std::max(fill / base, (max_len + 2047) / 2048);
-    p.splits = std::max<int64_t>(1, std::min({p.splits, (max_len + 255) / 256, (int64_t)kMaxSplits}));
-    p.splits = (int64_t)1 << log2_of(p.splits);
-    // (A launch holds fewer than 2^32 threads along x.)
-    while (p.splits > 1 && kv_heads * p.row_tiles * p.splits * std::min<int64_t>(seqs, 64) > 1 << 23) p.splits >>= 1;
-    p.min_chunk = base >= fill ? 2048 : base >= fill / 4 ? 1024 : base >= fill / 16 ? 512 : 256;
-    p.partial_floats = p.splits > 1 ? base * p.splits * p.rows * (head_dim + 2) : 0;
-    p.counter_words = p.splits > 1 ? base * kTileCounters : 0;
-    return p;
-}
-
 hipError_t launch_attention_paged(const pq2_attention_paged_args& a, const PagedPlan& plan, hipStream_t stream) {
+    const int64_t places = paged_places(plan, a.seqs, a.kv_heads), grid = paged_workgroups(plan, a.seqs, a.kv_heads);
     const PagedArgs k{static_cast<const uint16_t*>(a.q), static_cast<uint16_t*>(a.out), a.q_stride, a.q_head,
                       a.out_stride, a.out_head, static_cast<const uint8_t*>(a.cache), a.table, a.lens, a.starts,
                       a.partials, a.counters, a.table_stride, (int)a.rows, (int)a.table_pages, (int)a.kv_heads,
                       (int)(a.heads / a.kv_heads), (int)a.pages, log2_of(a.page_tokens), (int)a.max_new,
                       (int)std::min<int64_t>(a.window, 0x40000000), (int)plan.splits, (int)plan.row_tiles, (int)plan.rows,
-                      (int)plan.min_chunk, (int)a.seqs, log2_of(plan.splits), a.scale * kLog2e};
+                      (int)plan.min_chunk, (int)a.seqs, log2_of(plan.splits), (int)(places < 8 ? places : 0), a.scale * kLog2e};
     clear_stale_error();
     const bool f16 = a.dtype == PQ2_F16;
-    if (a.head_dim == 64) f16 ? start<64, _Float16>(k, a.seqs, stream) : start<64, __bf16>(k, a.seqs, stream);
-    else if (a.head_dim == 128) f16 ? start<128, _Float16>(k, a.seqs, stream) : start<128, __bf16>(k, a.seqs, stream);
-    else f16 ? start<256, _Float16>(k, a.seqs, stream) : start<256, __bf16>(k, a.seqs, stream);
+    if (a.head_dim == 64) f16 ? start<64, _Float16>(k, grid, stream) : start<64, __bf16>(k, grid, stream);
+    else if (a.head_dim == 128) f16 ? start<128, _Float16>(k, grid, stream) : start<128, __bf16>(k, grid, stream);
+    else f16 ? start<256, _Float16>(k, grid, stream) : start<256, __bf16>(k, grid, stream);
     return hipGetLastError();
 }
 

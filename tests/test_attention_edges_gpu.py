@@ -73,3 +73,34 @@ def test_smallest_scales(d, dt, scale):
     torch.cuda.synchronize()
     _, v, _ = ref.rows_of(cache, 16, 2, d, table[0], 1400)
     lim.check_counts(out, lim.mean_of_seen(v, lim.seen_keys(2, 1400, 1398, device=DEV), 8), DT[dt], "paged")
+
+
+# ---------------------------------------------------------------- large max_new
+@pytest.mark.parametrize("d", ref.DIMS)
+@pytest.mark.parametrize("seqs,heads,kv,max_new", [(1, 64, 1, 1 << 20), (3, 16, 1, 1 << 20), (2, 15, 3, 1 << 19), (1, 1, 1, 1 << 24), (5, 24, 3, 5000)])
+def test_paged_room_for_many_new_tokens(seqs, heads, kv, max_new, d):
+    """Calls with room for far more new tokens than there are: nearly all their workgroups find no rows.  Fewer than
+    eight places among them, whose row tiles go to all XCDs."""
+    announce(f"paged max_new={max_new} seqs={seqs} heads={heads}/{kv} d={d}")
+    lengths, new = [700, 45, 300, 16, 1][:seqs], [3, 1, 2, 0, 1][:seqs]
+    page = 16
+    cache = ref.make_cache(seqs * 44, page, kv, d, d, DEV)
+    ref.parts(cache, page, kv, d)[3].fill_(2.0 ** -6)
+    table = torch.arange(seqs * 44, dtype=torch.int32, device=DEV).view(seqs, 44)
+    q = randn((sum(new), heads, d), 2).bfloat16().to(DEV)
+    pq2 = _pq2()
+    floats, words = pq2.pq2_attention_paged_workspace(seqs, max_new, heads, kv, d, 700)
+    assert floats < 1 << 29
+    work = torch.empty(floats, device=DEV), torch.zeros(words, dtype=torch.int32, device=DEV)
+    zero, got = (torch.full_like(q, float("nan")) for _ in range(2))
+    for x, out in ((torch.zeros_like(q), zero), (q, got)):
+        pq2.pq2_attention_paged(x, cache, table, ints(lengths), page, out, *work, starts=starts_of(new), max_new=max_new, max_len=700)
+    torch.cuda.synchronize()
+    at = 0
+    for i, (n, t) in enumerate(zip(lengths, new)):
+        k, v, _ = ref.rows_of(cache, page, kv, d, table[i], n)
+        seen = lim.seen_keys(t, n, n - t, device=DEV)
+        if t:
+            lim.check_counts(zero[at:at + t], lim.mean_of_seen(v, seen, heads), torch.bfloat16, f"sequence {i}")
+            lim.check_norm(got[at:at + t], q[at:at + t], k, v, seen, scale=d ** -0.5, dtype=torch.bfloat16, paged=True, what=f"sequence {i}")
+        at += t
