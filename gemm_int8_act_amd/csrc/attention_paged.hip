@@ -199,9 +199,8 @@ __device__ __forceinline__ Sequence sequence(const PagedArgs& a, int seq, int ro
     const int most = a.window ? (int)min((int64_t)s.end, (int64_t)a.window + (rows + a.group - 1) / a.group + 16) : s.end;
     s.chunk = max(a.min_chunk, (((most + a.splits - 1) >> a.split_shift) + kStep - 1) & ~(kStep - 1));
     // (most - 1) / chunk, below 128: the reciprocal's quotient is off by one at most.
-    int p = (int)((float)(most - 1) * __builtin_amdgcn_rcpf((float)s.chunk));
-    p += (p + 1) * s.chunk < most ? 1 : p * s.chunk >= most && p > 0 ? -1 : 0;
-    s.parts = s.n <= 0 ? 0 : p + 1;
+    const int about = (int)((float)(most - 1) * __builtin_amdgcn_rcpf((float)s.chunk));
+    s.parts = s.n <= 0 ? 0 : parts_of(most, s.chunk, about);
     return s;
 }
 

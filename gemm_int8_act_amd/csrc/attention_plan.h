@@ -6,6 +6,12 @@
 
 #include <algorithm>
 
+#ifdef __HIPCC__
+#define PQ2_BOTH_SIDES __host__ __device__
+#else
+#define PQ2_BOTH_SIDES
+#endif
+
 namespace pq2 {
 
 constexpr int kPagedThreads = 256;         // threads of a workgroup
@@ -65,6 +71,15 @@ inline int64_t paged_places(const PagedPlan& p, int64_t seqs, int64_t kv_heads) 
 inline int64_t paged_workgroups(const PagedPlan& p, int64_t seqs, int64_t kv_heads) {
     const int64_t places = paged_places(p, seqs, kv_heads);
     return (places < 8 ? places : (places + 7) / 8 * 8) * p.row_tiles;
+}
+
+// Parts of `chunk` keys that `most` keys are, at least one; `about` is
+// (most - 1) / chunk, off by one at most.  Unsigned: most and chunk go up to
+// 2^30, the products up to 3 * 2^30.
+PQ2_BOTH_SIDES inline int parts_of(int most, int chunk, int about) {
+    const uint32_t all = (uint32_t)(most > 1 ? most : 1), next = (uint32_t)(about + 1) * (uint32_t)chunk;
+    if (next < all) return about + 2;
+    return about > 0 && next - (uint32_t)chunk >= all ? about : about + 1;
 }
 
 }  // namespace pq2

@@ -78,3 +78,28 @@ def test_launches_fit(tmp_path):
         largest = max(largest, workgroups)
     assert largest > 1 << 23           # (the padding is among the cases)
     assert len(out.splitlines()) == len(accepted)
+
+
+PARTS = r"""
+#include "attention_plan.h"
+#include <cstdio>
+int main() {
+    long long most, chunk, about;
+    while (std::scanf("%lld %lld %lld", &most, &chunk, &about) == 3)
+        std::printf("%d\n", pq2::parts_of((int)most, (int)chunk, (int)about));
+}
+"""
+
+
+def test_parts_of_the_longest_tables(tmp_path):
+    """Parts from a quotient that is off by one at most, up to the 2^30 keys that a table may hold in one part."""
+    exe = compiled(tmp_path, PARTS)
+    cases = []
+    for splits in (1, 2, 8, 128):
+        for most in (0, 1, 2, 127, 128, 129, 255, 256, 257, 5000, (1 << 23) + 1, (1 << 30) - 129, (1 << 30) - 1, 1 << 30):
+            for least in (256, 2048):
+                chunk = max(least, ((most + splits - 1) // splits + 127) & ~127)
+                exact = max(most - 1, 0) // chunk
+                cases += [(most, chunk, about, exact + 1) for about in (exact - 1, exact, exact + 1) if about >= 0]
+    out = subprocess.run([exe], input="".join(f"{m} {c} {a}\n" for m, c, a, _ in cases), capture_output=True, text=True, check=True).stdout
+    assert [int(v) for v in out.split()] == [want for *_, want in cases]
