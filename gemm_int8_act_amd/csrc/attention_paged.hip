@@ -13,7 +13,7 @@
 // whole 16-byte (keys) and head_dim/16-byte (values) stretches of the cache and
 // no transposition is left.
 //
-// Precision: key codes are exact in fp16, as 1152 + c; the queries, scaled by
+// Precision: key codes are exact in fp16; the queries, scaled by
 // a power of two, are fp16 too.  Key scales multiply the FP32 scores, value scales the FP32 weights,
 // which then meet the value codes (exact in bf16) as the sum of two bf16 (16
 // bits of the weight, at twice the cheap second product).
@@ -62,17 +62,18 @@ struct PagedArgs {
 
 __device__ __forceinline__ float code_at(uint32_t w, int i) { return (float)(int8_t)(w >> (8 * i)); }
 
-// Eight key codes (two dwords) as fp16 numbers 1152 + c, exact: a code's byte
-// with its top bit flipped, c + 128, below the high byte of 1024, one
-// instruction for two.
-constexpr float kBias = 1152.0f;
+// Eight key codes (two dwords) as fp16 numbers, exact: a code's byte with its
+// top bit flipped, c + 128, below the high byte of 1024 is 1152 + c (one
+// instruction for two), which one more brings back to c.  (Left to the end, with
+// 1152 times the sum of q taken off a score, the bias costs a score four to ten of its
+// bits where queries have a common offset.)
 __device__ __forceinline__ f16x8 widen(uint32_t a, uint32_t b) {
     constexpr uint32_t kSign = 0x80808080u, kHigh = 0x64646464u;
     a ^= kSign;
     b ^= kSign;
     const u32x4_t v = {__builtin_amdgcn_perm(a, kHigh, 0x00050004u), __builtin_amdgcn_perm(a, kHigh, 0x00070006u),
                        __builtin_amdgcn_perm(b, kHigh, 0x00050004u), __builtin_amdgcn_perm(b, kHigh, 0x00070006u)};
-    return __builtin_bit_cast(f16x8, v);
+    return __builtin_bit_cast(f16x8, v) - (_Float16)1152.0f;
 }
 
 // Maximum and sum over the four lanes (16 apart) that share a query row.
@@ -269,9 +270,9 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 || RT > 1 ? 2 : D == 128 ? 3 
     // This lane's query rows, one a tile.
     int seen_hi[RT], seen_lo[RT];
     // Its queries as fp16, scaled by a power of two to a largest element in
-    // [1, 2) (what that rounds is below 2^-24 of it); q_off takes the keys' bias off a score.
+    // [1, 2) (what that rounds is below 2^-24 of it).
     f16x8 qf[RT][D / 32];
-    float q_off[RT], q_scale[RT];
+    float q_scale[RT];
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
         const int r = r0 + 16 * t + j, i = r / a.group, g = r - i * a.group;
@@ -289,16 +290,11 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 || RT > 1 ? 2 : D == 128 ? 3 
         }
         const int exp = __builtin_amdgcn_frexp_expf(max_row(valid ? top : 0.0f)) - 1;  // (of 0: -1)
         q_scale[t] = __builtin_ldexpf(a.scale2, exp);
-        q_off[t] = 0.0f;
 #pragma unroll
         for (int c = 0; c < D / 32; ++c)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const _Float16 v = valid ? (_Float16)__builtin_ldexpf((float)x[c][e], -exp) : (_Float16)0.0f;
-                qf[t][c][e] = v;
-                q_off[t] -= (float)v;
-            }
-        q_off[t] = kBias * sum_row(q_off[t]);
+            for (int e = 0; e < 8; ++e)
+                qf[t][c][e] = valid ? (_Float16)__builtin_ldexpf((float)x[c][e], -exp) : (_Float16)0.0f;
     }
 
     const int64_t block_bytes = kv_block_bytes(1, D) << a.page_shift;
@@ -377,7 +373,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 || RT > 1 ? 2 : D == 128 ? 3 
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
 #pragma unroll
-            for (int t = 0; t < RT; ++t) sc[t][s] = v4f{q_off[t], q_off[t], q_off[t], q_off[t]};
+            for (int t = 0; t < RT; ++t) sc[t][s] = v4f{0, 0, 0, 0};
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
                 const uint4 k = w.k[s][c / 2];

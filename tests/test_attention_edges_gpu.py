@@ -104,3 +104,59 @@ def test_paged_room_for_many_new_tokens(seqs, heads, kv, max_new, d):
             lim.check_counts(zero[at:at + t], lim.mean_of_seen(v, seen, heads), torch.bfloat16, f"sequence {i}")
             lim.check_norm(got[at:at + t], q[at:at + t], k, v, seen, scale=d ** -0.5, dtype=torch.bfloat16, paged=True, what=f"sequence {i}")
         at += t
+
+
+# ---------------------------------------------------------------- scores over the pages
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("d", ref.DIMS)
+def test_paged_scores_of_queries_with_an_offset(d, dt):
+    """Queries with a common offset, as projections with a bias give them, and keys with an outlier channel, whose other
+    codes are small: scores are off by no more than FP32 sums of q k are."""
+    announce(f"paged, queries with an offset d={d} {dt}")
+    pq2 = _pq2()
+    heads, kv, page, lengths = 16, 2, 16, [300, 77, 1000]
+    width = 63
+    cache = ref.make_cache(3 * width, page, kv, d, 6, DEV)
+    kc, _, ks, _ = ref.parts(cache, page, kv, d)
+    small = (randn(kc.shape, 7) * 5).round().clamp(-127, 127)
+    small[..., 3] = 127 * randint(0, 1, kc.shape[:-1], 8) * 2 - 127
+    kc.copy_(small.to(torch.int8))
+    ks.fill_(0.25)
+    table = torch.arange(3 * width, dtype=torch.int32, device=DEV).view(3, width)
+    sign = 2.0 * randint(0, 1, (1, heads, 1), 9) - 1
+    q = randn((3, heads, d), 10) + 8 * sign
+    q[..., 3] = 0.1
+    q = q.to(DT[dt]).to(DEV)
+    out = torch.full_like(q, float("nan"))
+    floats, words = pq2.pq2_attention_paged_workspace(3, 1, heads, kv, d, width * page)
+    pq2.pq2_attention_paged(q, cache, table, ints(lengths), page, out, torch.empty(floats, device=DEV),
+                            torch.zeros(words, dtype=torch.int32, device=DEV))
+    torch.cuda.synchronize()
+    for i, n in enumerate(lengths):
+        k, v, _ = ref.rows_of(cache, page, kv, d, table[i], n)
+        seen = lim.seen_keys(1, n, n - 1, device=DEV)
+        o, spread, largest = lim.exact_and_spread(q[i:i + 1], k, v, seen, d ** -0.5)
+        print(f"  n={n} off {float((out[i:i + 1].double() - o).norm() / o.norm()):.2e} A={largest:.1f}", flush=True)
+        lim.check_norm(out[i:i + 1], q[i:i + 1], k, v, seen, scale=d ** -0.5, dtype=DT[dt], paged=True, what=f"sequence {i}")
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("d", ref.DIMS)
+def test_paged_elements_far_below_the_largest(d, dt):
+    """Elements of q between 2^-24 and 2^-14 of the row's largest count as multiples of 2^-24 of it: here they alone make
+    the scores, the largest meets codes of zero."""
+    announce(f"paged, small elements of q d={d} {dt}")
+    pq2 = _pq2()
+    heads, page, n = 8, 16, 130
+    cache = ref.make_cache(9, page, 1, d, 6, DEV)
+    kc, _, ks, _ = ref.parts(cache, page, 1, d)
+    kc[..., 5] = 0
+    ks.fill_(2.0 ** 8)
+    table = torch.arange(9, dtype=torch.int32, device=DEV).view(1, 9)
+    q = (randint(-31, 31, (1, heads, d), 9) * 2.0 ** -22).to(DT[dt]).to(DEV)     # multiples of 2^-24 of 1
+    q[..., 5] = 1.0
+    out = torch.full_like(q, float("nan"))
+    pq2.pq2_attention_paged(q, cache, table, ints([n]), page, out, max_len=144, scale=0.5)
+    torch.cuda.synchronize()
+    k, v, _ = ref.rows_of(cache, page, 1, d, table[0], n)
+    lim.check_norm(out, q, k, v, lim.seen_keys(1, n, n - 1, device=DEV), scale=0.5, dtype=DT[dt], paged=True, what="o")
