@@ -36,7 +36,7 @@ constexpr int bufs_of(int d, int waves) { return d == 256 || waves == 4 ? 2 : 4;
 constexpr int ahead_of(int d) { return d == 256 ? 3 : 4; }
 constexpr int q_lds_of(int d) { return d == 256 ? 8 : 0; }
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kSlack = 8.0f;      // weights grow to 2^8 before a row's reference moves
+constexpr float kSlack = 8.0f;      // weights grow by 2^8 before a row's reference moves
 
 struct PromptArgs {
     const uint16_t* q;
@@ -53,14 +53,20 @@ struct PromptArgs {
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 
+// kRaise: weights are 2^kRaise for a score at the row's reference.  fp16 has
+// room for 2^15, of which scores that pass the reference take 2^8; at 1, the weights
+// below 2^-25 would be lost: thousands of them beside one leading key, a part of
+// the result.
 template <typename T> struct Half;
 template <> struct Half<__bf16> {
+    static constexpr float kRaise = 0.0f;
     typedef bf16x8 v8;
     typedef __bf16 v2 __attribute__((ext_vector_type(2)));
     static __device__ __forceinline__ v16f mfma(v8 a, v8 b, v16f c) { return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0); }
     static __device__ __forceinline__ float add2(v2 e, float s) { return __builtin_amdgcn_fdot2_f32_bf16(e, v2{(__bf16)1.0f, (__bf16)1.0f}, s, false); }
 };
 template <> struct Half<_Float16> {
+    static constexpr float kRaise = 7.0f;
     typedef f16x8 v8;
     typedef _Float16 v2 __attribute__((ext_vector_type(2)));
     static __device__ __forceinline__ v16f mfma(v8 a, v8 b, v16f c) { return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0); }
@@ -317,7 +323,7 @@ __global__ __launch_bounds__(64 * W, 2) void attention_prompt_kernel(PromptArgs 
                 if (top > m + a.slack) m = top;
                 const float ref = m == -INFINITY ? 0.0f : m;
                 alpha = __builtin_amdgcn_exp2f((old - ref) * a.scale2);
-                bias = ref * a.scale2;
+                bias = ref * a.scale2 - Half<T>::kRaise;
                 l *= alpha;
             } else {
 #pragma unroll

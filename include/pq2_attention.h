@@ -177,7 +177,8 @@ int pq2_attention_paged(const pq2_attention_paged_args* args, void* stream);
  *                  with causal over j <= p, with window > 0 (causal only) also j > p - window
  *
  * Scores, softmax and sums are FP32; the weights are rounded to dtype before
- * they meet the values, as matrix cores take them, and normalised by the sum
+ * they meet the values, as matrix cores take them (an fp16 weight below 2^-21 of its
+ * row's largest to a multiple of 2^-31 of that), and normalised by the sum
  * of the rounded ones; out is rounded once.
  *  - A row that sees no key is zero.  Rows of other sequences have no influence.
  *  - starts begin at 0 and never fall; rows of q behind the last sequence are left as

@@ -160,3 +160,34 @@ def test_paged_elements_far_below_the_largest(d, dt):
     torch.cuda.synchronize()
     k, v, _ = ref.rows_of(cache, page, 1, d, table[0], n)
     lim.check_norm(out, q, k, v, lim.seen_keys(1, n, n - 1, device=DEV), scale=0.5, dtype=DT[dt], paged=True, what="o")
+
+
+# ---------------------------------------------------------------- small weights of prompts
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("d", ref.DIMS)
+@pytest.mark.parametrize("below", [14, 15, 16, 18, 20, 23, 24, 25, 26, 28, 30])
+def test_prompt_weights_far_below_the_largest(below, d, dt):
+    """One leading key whose value is zero, thousands of others with weights 2^-below of its: the output is theirs alone.
+    Weights are powers of two (the scale is ln 2), exact in 16 bits as far as they reach; the sums err by at most n u, the
+    scores by 4 roundings of `below`."""
+    announce(f"prompt, weights 2^-{below} d={d} {dt}")
+    pq2 = _pq2()
+    for n, nq, heads, kv in ((4000, 40, 2, 1), (8200, 4100, 32, 1)):      # the second: eight waves
+        if nq > 1000 and below not in (16, 26):
+            continue
+        for lead in (0, n - 5, n // 2):
+            q = torch.zeros((nq, heads, d), dtype=DT[dt], device=DEV)
+            q[..., 0] = 1.0
+            k = randn((n, kv, d), 2).to(DT[dt]).to(DEV)
+            k[..., 0] = -below
+            k[lead, :, 0] = 0.0
+            v = randint(100, 250, (n, kv, d), 3).to(DT[dt]).to(DEV)
+            v[lead] = 0.0
+            out = torch.full_like(q, float("nan"))
+            pq2.pq2_attention_prompt(q, k, v, out, starts_of([nq]), starts_of([n]), causal=False, scale=0.6931471805599453)
+            torch.cuda.synchronize()
+            w = 2.0 ** -below
+            want = (v.double().sum(0) * w / (1 + (n - 1) * w)).repeat_interleave(heads // kv, 0)[None]
+            limit = (lim.half(DT[dt]) + (n + 16 + 8 * below) * lim.U) * want
+            over = (out.double() - want).abs() - limit
+            assert float(over.max()) <= 0, (f"n={n} leading key {lead}: {float(out[0, 0, 0])!r} instead of {float(want[0, 0, 0])!r}")
