@@ -6,7 +6,9 @@ it calls and only marshals arguments: torch tensors give device pointers and
 shapes, the current torch stream gives the HIP stream.  All arithmetic runs
 in the HIP kernels; there is no CPU or PyTorch fallback.  If the library is
 missing, importing the package raises ImportError; build it with
-``python gemm_int8_act_amd/build.py``.
+``python gemm_int8_act_amd/build.py``.  The attention operators also need
+``_marshal.so``, which is built for one torch: without it only their calls
+raise ImportError.
 
 Status codes map to exceptions: EINVAL, ESHAPE and EALIGN raise ValueError;
 ELAUNCH and EDEVICE raise RuntimeError.

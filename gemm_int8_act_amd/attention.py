@@ -15,10 +15,11 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import os
 
 import torch
 
-from . import _check, _marshal, lib
+from . import _check, lib
 from .block import _raw_stream
 
 ATTENTION_EXPORTED = (
@@ -29,6 +30,34 @@ ATTENTION_EXPORTED = (
     "pq2_attention_paged",
     "pq2_attention_prompt",
 )
+
+
+class _NoMarshal:
+    """In place of ``_marshal`` where it does not load: the rest of the package needs no more than libpq2.so, so only
+    the attention calls raise."""
+
+    def __init__(self, reason):
+        self._reason = reason
+
+    def __getattr__(self, name):
+        raise ImportError(f"{os.path.join(os.path.dirname(__file__), '_marshal.so')}: {self._reason}; the attention "
+                          "operators' binding must be built with the installed torch (python gemm_int8_act_amd/build.py); "
+                          "there is no fallback path")
+
+
+def _load_marshal():
+    try:
+        from . import _marshal
+    except ImportError as e:
+        return _NoMarshal(str(e))
+    # It reads torch's tensors in place, so it holds for the torch that it was compiled against.
+    if _marshal.torch_version != torch.__version__:
+        return _NoMarshal(f"built for torch {_marshal.torch_version}, not {torch.__version__}")
+    return _marshal
+
+
+_marshal = _load_marshal()
+
 
 def _bind():
     p, i64, i32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int

@@ -70,7 +70,7 @@ def _marshal_module() -> None:
     root = os.path.dirname(torch.__file__)
     tmp = MARSHAL + ".tmp"
     cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-DUSE_ROCM",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f'-DPQ2_TORCH_VERSION="{torch.__version__}"',
            "-I", sysconfig.get_path("include"), "-isystem", os.path.join(root, "include"),
            os.path.join(CSRC, "marshal.cpp"), "-o", tmp, "-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu",
            "-lc10", "-L", HERE, "-lpq2", "-Wl,-rpath,$ORIGIN"]
