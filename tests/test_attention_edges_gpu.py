@@ -191,3 +191,141 @@ def test_prompt_weights_far_below_the_largest(below, d, dt):
             limit = (lim.half(DT[dt]) + (n + 16 + 8 * below) * lim.U) * want
             over = (out.double() - want).abs() - limit
             assert float(over.max()) <= 0, (f"n={n} leading key {lead}: {float(out[0, 0, 0])!r} instead of {float(want[0, 0, 0])!r}")
+
+
+# ---------------------------------------------------------------- every key, once
+PAGES = [
+    # lengths, new tokens, heads, kv, page, window, more
+    ([1], [1], 1, 1, 16, 0, {}),
+    ([0, 1, 2, 15, 16, 17, 31, 32, 33, 255, 256, 257], [1] * 12, 8, 2, 16, 0, {}),
+    ([517, 700, 2000], [1, 1, 1], 10, 2, 16, 0, {}),
+    ([700, 90, 1500], [2, 1, 3], 6, 2, 16, 0, dict(bad_page=True)),
+    ([6000, 3], [1, 1], 4, 2, 32, 0, dict(max_len=600)),
+    ([600, 3], [1, 1], 4, 2, 32, 0, dict(max_len=100000, max_new=5)),
+    ([700, 100, 490], [4, 3, 2], 4, 2, 16, 0, dict(table_pages=30)),
+    ([700, 100, 490], [4, 3, 2], 4, 2, 16, 250, dict(table_pages=30)),
+    ([600, 20, 3, 0], [16, 9, 5, 2], 10, 2, 64, 0, {}),
+    ([3000, 100, 7], [4, 7, 1], 24, 4, 32, 0, {}),
+    ([1000, 900], [2, 1], 34, 2, 64, 0, {}),
+    ([4000, 300, 50], [3, 1, 8], 5, 5, 128, 100, {}),
+    ([9000, 40], [8, 8], 8, 1, 256, 1024, {}),
+    ([2500, 2500], [1, 0], 16, 2, 16, 1, {}),
+    ([20000, 17, 9000], [1, 1, 1], 8, 8, 32, 0, {}),
+    ([33000], [1], 16, 2, 64, 0, {}),
+    ([70000], [1], 4, 1, 256, 0, {}),
+    ([5000 if i == 3 else 2600 if i == 70 else 4100 if i == 149 else 7 * i * i % 300 for i in range(150)],
+     [1 + i % 3 if i % 11 else 0 for i in range(150)], 4, 2, 16, 0, {}),
+]
+
+
+def paged_call(lengths, new, heads, kv, d, page, dt, window, q, cache, table, max_new=None, max_len=None, scale=None):
+    pq2 = _pq2()
+    out = torch.full_like(q, float("nan"))
+    max_new, max_len = max_new or max(max(new), 1), max_len or max(1, max(lengths))
+    floats, words = pq2.pq2_attention_paged_workspace(len(lengths), max_new, heads, kv, d, max_len)
+    pq2.pq2_attention_paged(q, cache, table, ints(lengths), page, out, torch.full((floats,), float("nan"), device=DEV),
+                            torch.zeros(words, dtype=torch.int32, device=DEV), starts=starts_of(new), max_new=max_new, max_len=max_len,
+                            window=window, scale=scale)
+    torch.cuda.synchronize()
+    return out
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("d", ref.DIMS)
+@pytest.mark.parametrize("lengths,new,heads,kv,page,window,more", PAGES)
+def test_paged_every_key_once(lengths, new, heads, kv, page, window, more, d, dt):
+    """Every key of a row counts once (queries of zero), and with ordinary queries no sequence's norm misses one."""
+    announce(f"paged counts lengths={lengths[:12]} new={new[:8]} heads={heads}/{kv} d={d} page={page} {dt} window={window} {more}")
+    more = dict(more)
+    width = max(1, max((n + page - 1) // page for n in lengths))
+    pages = len(lengths) * width + 3
+    cache = ref.make_cache(pages, page, kv, d, d + 1, DEV)
+    _, _, ks, vs = ref.parts(cache, page, kv, d)
+    vs.fill_(2.0 ** -6)
+    table = torch.randperm(pages, generator=torch.Generator().manual_seed(5))[:len(lengths) * width].to(torch.int32).view(-1, width).to(DEV)
+    for i, n in enumerate(lengths):                 # behind the lengths: anything
+        last = table[i, n // page:].long() if n % page == 0 else table[i, n // page + 1:].long()
+        ks[last], vs[last] = float("nan"), float("inf")
+        if n % page:
+            ks[int(table[i, n // page]), :, n % page:], vs[int(table[i, n // page]), :, n % page:] = float("nan"), float("inf")
+    if more.pop("bad_page", False):
+        table[0, 0], table[-1, -1] = -1, pages
+    table = table[:, :more.pop("table_pages", width)]
+    rows = sum(new)
+    q = randn((rows, heads, d), 9, 1.2).to(DT[dt]).to(DEV)
+    zero, got = (paged_call(lengths, new, heads, kv, d, page, dt, window, x, cache, table, **more) for x in (torch.zeros_like(q), q))
+    at = 0
+    for i, (n, t) in enumerate(zip(lengths, new)):
+        k, v, there = ref.rows_of(cache, page, kv, d, table[i], n)
+        k, v = (torch.where(there[:, None, None], x, torch.zeros_like(x)) for x in (k, v))
+        seen = lim.seen_keys(t, n, n - t, window=window, there=there, device=DEV)
+        if t:
+            lim.check_counts(zero[at:at + t], lim.mean_of_seen(v, seen, heads), DT[dt], f"sequence {i}")
+            if len(lengths) < 100 or n > 2000 or i % 10 == 1:
+                lim.check_norm(got[at:at + t], q[at:at + t], k, v, seen, scale=d ** -0.5, dtype=DT[dt], paged=True, what=f"sequence {i}")
+        at += t
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("d", ref.DIMS)
+@pytest.mark.parametrize("n,page,max_len", [(300, 16, 300), (2000, 32, 2000), (5000, 64, 5000), (5000, 16, 300), (40000, 256, 40000)])
+def test_paged_needles(n, page, max_len, d, dt):
+    """Each head's query is one key's codes, and its output that key's value: at the edges of pages, tiles, steps and
+    parts.  The key's score leads by far more than ln n, so that all but the last rounding is below 2^-8 of the largest value."""
+    announce(f"paged needles n={n} page={page} d={d} {dt}")
+    heads, kv = 64, 4
+    width = (n + page - 1) // page
+    cache = ref.make_cache(width, page, kv, d, 3, DEV)
+    kc, vc, ks, vs = ref.parts(cache, page, kv, d)
+    ks.fill_(1.0 / 64)
+    vs.fill_(1.0 / 64)
+    table = torch.randperm(width, generator=torch.Generator().manual_seed(4)).to(torch.int32).view(1, -1).to(DEV)
+    edges = [0, 1, 15, 16, 17, 31, 32, 33, 63, 64, 127, 128, 129, 255, 256, 257, 383, 384, 511, 512, 1023, 1024, 2047, 2048, 4095, 4096]
+    edges = [e for e in edges if e < n] + [n - 1, n - 2, n // 2, (n - 1) // 128 * 128, (n - 1) // page * page, (n - 1) // page * page - 1]
+    at = torch.tensor((edges * heads)[:heads], device=DEV)
+    k, v, _ = ref.rows_of(cache, page, kv, d, table[0], n)
+    g = torch.arange(heads, device=DEV) // (heads // kv)
+    q = k[at, g][None].to(DT[dt])
+    got = paged_call([n], [1], heads, kv, d, page, dt, 0, q, cache, table, max_len=max_len, scale=4 / d ** 0.5)
+    assert float((got[0].double() - v[at, g]).abs().max()) <= 2 * 2.0 ** -8 * float(v.abs().max())
+
+
+PROMPTS = [
+    # queries, keys, heads, kv, causal, window
+    ([1], [1], 1, 1, True, 0),
+    ([64, 1, 0, 129, 65, 31], [64, 1, 0, 129, 65, 31], 4, 2, True, 0),
+    ([5, 100, 130, 0], [300, 100, 513, 70], 6, 2, True, 0),
+    ([40, 90], [7, 0], 2, 1, True, 0),
+    ([300, 77], [300, 500], 4, 4, False, 0),
+    ([10, 3], [0, 65], 4, 1, False, 0),
+    ([700, 20], [700, 400], 5, 1, True, 100),
+    ([300, 150], [333, 150], 2, 2, True, 1),
+    ([3] * 150, [4] * 150, 2, 1, True, 0),
+    ([4100, 100], [8300, 133], 32, 4, True, 3000),
+    ([4200], [4200], 32, 2, True, 0),
+]
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("d", ref.DIMS)
+@pytest.mark.parametrize("nq,nk,heads,kv,causal,window", PROMPTS)
+def test_prompt_every_key_once(nq, nk, heads, kv, causal, window, d, dt):
+    announce(f"prompt counts nq={nq[:6]} nk={nk[:6]} heads={heads}/{kv} d={d} {dt} causal={causal} window={window}")
+    pq2 = _pq2()
+    rq, rk = sum(nq), max(1, sum(nk))
+    q = randn((rq, heads, d), d, 1.2).to(DT[dt]).to(DEV)
+    k = randn((rk, kv, d), d + 1).to(DT[dt]).to(DEV)
+    v = randint(-127, 127, (rk, kv, d), d + 2).to(DT[dt]).to(DEV)
+    zero, got = (torch.full_like(q, 7.0) for _ in range(2))
+    for x, out in ((torch.zeros_like(q), zero), (q, got)):
+        pq2.pq2_attention_prompt(x, k, v, out, starts_of(nq), starts_of(nk), causal=causal, window=window)
+    torch.cuda.synchronize()
+    a = b = 0
+    for i, (n, m) in enumerate(zip(nq, nk)):
+        seen = lim.seen_keys(n, m, m - n, causal=causal, window=window, device=DEV)
+        if n:
+            lim.check_counts(zero[a:a + n], lim.mean_of_seen(v[b:b + m], seen, heads), DT[dt], f"sequence {i}")
+            if n < 1000 or d == 128:
+                lim.check_norm(got[a:a + n], q[a:a + n], k[b:b + m], v[b:b + m], seen, scale=d ** -0.5, dtype=DT[dt], paged=False,
+                               what=f"sequence {i}")
+        a, b = a + n, b + m
