@@ -16,6 +16,8 @@ bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p % a) == 0; }
 bool dtype_ok(int d) { return d == PQ2_BF16 || d == PQ2_F16 || d == PQ2_F32; }
 bool half_ok(int d) { return d == PQ2_BF16 || d == PQ2_F16; }
 int esize(int d) { return d == PQ2_F32 ? 4 : 2; }
+// (The kernels take exp2 of scores times scale * log2(e).)
+bool scale_ok(float s) { return s > 0.0f && isfinite(s * 1.4426950408889634f); }
 bool dim_ok(int64_t d) { return d == 64 || d == 128 || d == 256; }
 bool page_ok(int64_t p) { return p == 16 || p == 32 || p == 64 || p == 128 || p == 256; }
 bool heads_ok(int64_t heads, int64_t kv) { return kv >= 1 && heads >= kv && heads <= PQ2_MAX_ATTN_HEADS && heads % kv == 0; }
@@ -181,7 +183,7 @@ int pq2_attention_paged_workspace(int64_t seqs, int64_t max_new, int64_t heads, 
 
 int pq2_attention_paged(const pq2_attention_paged_args* a, void* stream) {
     if (!a || !a->q || !a->out || !a->cache || !a->table || !a->lens) return PQ2_EINVAL;
-    if (!half_ok(a->dtype) || !(a->scale > 0.0f) || !isfinite(a->scale) || a->window < 0) return PQ2_EINVAL;
+    if (!half_ok(a->dtype) || !scale_ok(a->scale) || a->window < 0) return PQ2_EINVAL;
     const int64_t d = a->head_dim;
     if (!paged_sizes_ok(a->seqs, a->max_new, a->heads, a->kv_heads, d, a->max_len)) return PQ2_ESHAPE;
     if (a->rows < 1 || a->rows > PQ2_MAX_ATTN_ROWS || (!a->starts && a->rows != a->seqs)) return PQ2_ESHAPE;
@@ -216,7 +218,7 @@ int pq2_attention_paged(const pq2_attention_paged_args* a, void* stream) {
 
 int pq2_attention_prompt(const pq2_attention_prompt_args* a, void* stream) {
     if (!a || !a->q || !a->k || !a->v || !a->out || !a->starts_q || !a->starts_k) return PQ2_EINVAL;
-    if (!half_ok(a->dtype) || !(a->scale > 0.0f) || !isfinite(a->scale) || (a->causal != 0 && a->causal != 1)) return PQ2_EINVAL;
+    if (!half_ok(a->dtype) || !scale_ok(a->scale) || (a->causal != 0 && a->causal != 1)) return PQ2_EINVAL;
     if (a->window < 0 || (a->window > 0 && !a->causal)) return PQ2_EINVAL;
     const int64_t d = a->head_dim;
     if (a->rows_q < 1 || a->rows_q > PQ2_MAX_ATTN_ROWS || a->rows_k < 1 || a->rows_k > PQ2_MAX_ATTN_ROWS ||

@@ -152,7 +152,7 @@ typedef struct pq2_attention_paged_args {
     int64_t max_new;          /* most new tokens of a sequence: later ones are not computed      */
     int64_t max_len;          /* longest length expected; a longer one is computed, more slowly  */
     int64_t window;           /* keys that a token sees, itself among them; 0: all               */
-    float scale;              /* > 0, finite                                                       */
+    float scale;              /* > 0; finite, also times log2(e)                                   */
     int dtype;                /* PQ2_BF16 or PQ2_F16                                             */
 } pq2_attention_paged_args;
 
@@ -193,7 +193,7 @@ typedef struct pq2_attention_prompt_args {
     const int32_t* starts_k;  /* [seqs + 1]                                                      */
     int64_t rows_q, rows_k, seqs, heads, kv_heads, head_dim;
     int64_t window;
-    float scale;              /* > 0, finite                                                       */
+    float scale;              /* > 0; finite, also times log2(e)                                   */
     int dtype;                /* PQ2_BF16 or PQ2_F16                                             */
     int causal;               /* 0 or 1                                                          */
 } pq2_attention_prompt_args;
