@@ -137,7 +137,9 @@ def pq2_attention_paged(q, cache, table, lens, page_tokens: int, out, partials=N
     """Attention of new tokens over the paged cache: q and out [rows][heads][head_dim], bf16 or f16.
 
     lens int32 [sequences]: tokens of each in the cache, the new ones (already written) among them; table int32
-    [sequences][pages].  starts int32 [sequences + 1]: rows of each sequence's new tokens, at most max_new each; None: one each.
+    [sequences][pages].  starts int32 [sequences + 1]: rows of each sequence's new tokens; None: one each.
+    max_new goes with starts: the most new tokens of a sequence (the default, 1, too: rows behind a sequence's first max_new are left
+    as they were).
     max_len: the longest length expected (None: what the table holds); with seqs, max_new and the heads it gives the
     workspace's sizes, pq2_attention_paged_workspace: partials float32, counters int32, zero before the first call.  scale: 1 /
     sqrt(head_dim) if None.  window: keys that a token sees, itself among them (0: all)."""

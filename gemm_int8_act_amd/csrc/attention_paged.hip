@@ -19,9 +19,9 @@
 // bits of the weight, at twice the cheap second product).
 //
 // Bound: the cache's bytes where there is enough of it (64 sequences of 16384
-// keys, heads of 128: 401 us, 5.5 TB/s; one of 131071 keys 60 us, 4.6 TB/s, of
+// keys, heads of 128: 401 us, 5.5 TB/s; one of 131071 keys 54 to 61 us, 4.6 to 5.1 TB/s, of
 // which some 8 us are the start and the join), else the latency of a few dependent steps: a
-// wave's 32 keys take about 300 vector instructions, and a wave alone on its SIMD issues
+// wave's 32 keys take about 330 vector instructions, and a wave alone on its SIMD issues
 // one in 8 cycles (1.3 us a step).  Hence workgroups of four waves, of which
 // three or four share a compute unit (512 to 1024 at once), and parts of a
 // length that gives each of them work: 517 keys of one sequence 9.6 us, 2000 keys 9.6.
@@ -65,8 +65,8 @@ __device__ __forceinline__ float code_at(uint32_t w, int i) { return (float)(int
 // Eight key codes (two dwords) as fp16 numbers, exact: a code's byte with its
 // top bit flipped, c + 128, below the high byte of 1024 is 1152 + c (one
 // instruction for two), which one more brings back to c.  (Left to the end, with
-// 1152 times the sum of q taken off a score, the bias costs a score four to ten of its
-// bits where queries have a common offset.)
+// 1152 times the sum of q taken off a score, the bias costs a score three to ten of its
+// bits, most where queries have a common offset.)
 __device__ __forceinline__ f16x8 widen(uint32_t a, uint32_t b) {
     constexpr uint32_t kSign = 0x80808080u, kHigh = 0x64646464u;
     a ^= kSign;

@@ -11,9 +11,17 @@
 // one value a lane.  K and V tiles go straight into LDS, rows swizzled by
 // 16-byte chunks; the values' operand is read transposed (ds_read_b64_tr_b16).
 //
-// Bound: the matrix cores (53 % of their cycles on 8192 tokens, 40 heads of
-// 128: 640 to 666 us, 1.03 to 1.07 PFLOP/s, 82 to 84 % of what a large library product reaches;
-// 24 heads of 256 760 us, 1.08 PFLOP/s) beside the softmax (41 % of the vector cycles) and LDS (40 %); short prompts by the
+// Precision: scores, references and sums are FP32.  The weights are rounded to the
+// tensors' type, what the second product's operand holds, and their sum takes the
+// rounded ones: against 64 bits the result is 1.25 to 1.3 times as far off as its own
+// last rounding makes it (bf16 0.0020 to 0.0021 of the norm, fp16 0.00027).  Weights as two numbers, as
+// over the pages, would double the second product, half of the matrix cores' work.
+//
+// Bound: the matrix cores (54 % of their cycles on 8192 tokens, 40 heads of
+// 128: 624 to 666 us, 1.03 to 1.1 PFLOP/s, 82 to 87 % of what a large library product reaches;
+// 24 heads of 256 733 to 764 us, 1.08 to 1.13 PFLOP/s) beside the softmax (41 % of the vector cycles) and LDS (40 %);
+// heads of 64 by the softmax (64 % of the vector cycles, matrix cores 46 %: 371 to 395 us, 0.87 to 0.93 PFLOP/s), which is
+// as long for half the products; short prompts by the
 // 7 us that a workgroup's start and end take.  A step's three pieces of work are
 // independent and laid out instruction by instruction, so that matrix and
 // vector units of a SIMD work at once and no read of LDS is waited for; left to
@@ -423,8 +431,8 @@ void start(PromptArgs a, hipStream_t stream) {
 
 // Workgroups of four waves, of which several share a compute unit (one starts
 // while another computes), or of eight, one a unit, which read each tile of keys for twice
-// the rows. us with four / eight, 40 heads of 128: 24 prompts of 500 tokens 134 / 155, one of 2048 58 / 63,
-// of 8192 662 / 644; 24 heads of 256 (four: one workgroup a unit all the same):
+// the rows. us with four / eight, 40 heads of 128: 24 prompts of 500 tokens 134 / 155, one of 2048 66 / 68,
+// of 3000 116 / 113, of 4096 186 / 187, of 6000 359 / 349, of 8192 639 / 620 (around 4096 it makes no difference); 24 heads of 256 (four: one workgroup a unit all the same):
 // one of 1024 40 / 56, of 2048 71 / 97, four of 1500 151 / 145, 24 of 500 171 / 156; 40 heads of 64: 8192 tokens 380 / 410.
 template <typename T>
 void start(const PromptArgs& a, int d, hipStream_t stream) {

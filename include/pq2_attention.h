@@ -18,6 +18,13 @@
  * check every one that becomes an address: what each entry point does with a
  * value out of range is stated there, and none reads or writes outside the
  * buffers given.
+ *
+ * Attention takes finite queries, keys and values: a NaN or infinity among a
+ * sequence's own tokens may reach other rows of that sequence, also rows whose mask
+ * hides it; other sequences, and what lies behind a sequence's end, have no
+ * influence.  Scores, and sums of weights (up to 2^8, of prompts in fp16 2^15) times
+ * values, are FP32 before they are normalised: scale * q . k and 2^40 times the
+ * largest value stay within its range.
  */
 #ifndef PQ2_ATTENTION_H
 #define PQ2_ATTENTION_H
