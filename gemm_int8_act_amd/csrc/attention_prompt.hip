@@ -45,6 +45,11 @@ constexpr int ahead_of(int d) { return d == 256 ? 3 : 4; }
 constexpr int q_lds_of(int d) { return d == 256 ? 8 : 0; }
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 8.0f;      // weights grow by 2^8 before a row's reference moves
+// A weight is exp2(score * scale - bias), bias the reference times the scale, one
+// instruction for the exponent.  The bias is rounded, by a part of its size that moves all weights
+// of the reference alike; beyond kFar the reference is taken off the scores first, or of
+// 2^24 and more that part would be more than a 16-bit weight has room for.
+constexpr float kFar = 1024.0f;
 
 struct PromptArgs {
     const uint16_t* q;
@@ -331,7 +336,13 @@ __global__ __launch_bounds__(64 * W, 2) void attention_prompt_kernel(PromptArgs 
                 if (top > m + a.slack) m = top;
                 const float ref = m == -INFINITY ? 0.0f : m;
                 alpha = __builtin_amdgcn_exp2f((old - ref) * a.scale2);
-                bias = ref * a.scale2 - Half<T>::kRaise;
+                bias = ref * a.scale2;
+                if (__any(fabsf(bias) > kFar)) {
+#pragma unroll
+                    for (int e = 0; e < 16 * KB; ++e) sc[e / 16][e % 16] -= ref;
+                    bias = 0.0f;
+                }
+                bias -= Half<T>::kRaise;
                 l *= alpha;
             } else {
 #pragma unroll

@@ -329,3 +329,81 @@ def test_prompt_every_key_once(nq, nk, heads, kv, causal, window, d, dt):
                 lim.check_norm(got[a:a + n], q[a:a + n], k[b:b + m], v[b:b + m], seen, scale=d ** -0.5, dtype=DT[dt], paged=False,
                                what=f"sequence {i}")
         a, b = a + n, b + m
+
+
+# ---------------------------------------------------------------- large scores
+@pytest.mark.parametrize("dt,size", [("f16", 30.0), ("f16", 1000.0), ("f16", 15000.0), ("bf16", 1000.0), ("bf16", 1e6), ("bf16", 1e15)])
+@pytest.mark.parametrize("d", ref.DIMS)
+def test_large_scores(d, dt, size):
+    """Scores from 1e3 to 1e30 times ln 2, far apart: rows whose largest leads by more than FP32 sums may be off, and by 40, are
+    that key's value."""
+    announce(f"large scores d={d} {dt} {size}")
+    pq2 = _pq2()
+    for n, heads, kv, causal in ((300, 4, 2, True), (4200, 32, 2, False)):
+        q, k = ((randn((n, h, d), i).clamp(-4, 4) * size).to(DT[dt]).to(DEV) for i, h in ((1, heads), (2, kv)))
+        v = randint(-100, 100, (n, kv, d), 3).to(DT[dt]).to(DEV)
+        out = torch.full_like(q, float("nan"))
+        pq2.pq2_attention_prompt(q, k, v, out, starts_of([n]), starts_of([n]), causal=causal)
+        torch.cuda.synchronize()
+        led = 0
+        for h in range(0, heads, 7):
+            led += leading_values(out[:, h], q[:, h], k[:, h // (heads // kv)], v[:, h // (heads // kv)], causal)
+        assert led > n // 2
+    cache = ref.make_cache(90, 16, 2, d, 4, DEV)
+    _, _, ks, vs = ref.parts(cache, 16, 2, d)
+    ks.mul_(size)
+    vs.fill_(1.0)
+    table = torch.arange(90, dtype=torch.int32, device=DEV).view(1, 90)
+    q = (randn((2, 8, d), 5).clamp(-4, 4) * size).to(DT[dt]).to(DEV)
+    out = torch.full_like(q, float("nan"))
+    floats, words = pq2.pq2_attention_paged_workspace(1, 2, 8, 2, d, 1440)
+    pq2.pq2_attention_paged(q, cache, table, ints([1400]), 16, out, torch.empty(floats, device=DEV),
+                            torch.zeros(words, dtype=torch.int32, device=DEV), starts=ints([0, 2]), max_new=2)
+    torch.cuda.synchronize()
+    k, v, _ = ref.rows_of(cache, 16, 2, d, table[0], 1400)
+    assert sum(leading_values(out[1:, h], q[1:, h], k[:, h // 4], v[:, h // 4], False) for h in range(8)) > 4
+
+
+def leading_values(out, q, k, v, causal):
+    """Checks the rows whose largest score leads; how many these are."""
+    a = q.double() @ k.double().t().contiguous() * q.shape[1] ** -0.5
+    if causal:
+        a = a.masked_fill(~lim.seen_keys(a.shape[0], a.shape[1], 0, device=DEV), -float("inf"))
+    most = (q.double().abs() @ k.double().abs().t().contiguous()).amax(1) * q.shape[1] ** -0.5
+    top = a.topk(min(2, a.shape[1]), dim=1)
+    lead = top.values[:, 0] - top.values[:, 1] > 40 + 2 * (q.shape[1] + 8) * lim.U * most
+    got, want = out[lead].double(), v.double()[top.indices[lead, 0]]
+    # (bf16 and fp16 hold the values; weights 2^-57 of the largest and less move nothing.)
+    assert torch.equal(got, want), (f"{int((got != want).any(1).sum())} of {int(lead.sum())} rows, first "
+                                    f"{got[(got != want).any(1)][0, :4].tolist()} instead of {want[(got != want).any(1)][0, :4].tolist()}")
+    return int(lead.sum())
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("d", ref.DIMS)
+@pytest.mark.parametrize("common", [2.0 ** 10, 2.0 ** 18, 2.0 ** 22, 2.0 ** 23])
+def test_prompt_large_scores_in_common(common, d, dt):
+    """Scores of a large common part and small integers, exact in FP32, under a scale of ln 2: weights are powers of two, and
+    the common part has no influence, also while the reference moves."""
+    announce(f"prompt, common score {common} d={d} {dt}")
+    pq2 = _pq2()
+    n = 700
+    for order in (1, -1):
+        small = torch.arange(n) * 3 // 100               # 0 .. 20
+        small = small.flip(0) if order < 0 else small
+        k = torch.zeros((n, 1, d))
+        k[:, 0, 0], k[:, 0, 1] = 2.0 ** (int(common).bit_length() // 2), small
+        q = torch.zeros((40, 2, d))
+        q[..., 0], q[..., 1] = common / k[0, 0, 0], 1.0
+        q, k = q.to(DT[dt]).to(DEV), k.to(DT[dt]).to(DEV)
+        v = randint(50, 250, (n, 1, d), 3).to(DT[dt]).to(DEV)
+        out = torch.full_like(q, float("nan"))
+        pq2.pq2_attention_prompt(q, k, v, out, starts_of([40]), starts_of([n]), causal=False, scale=0.6931471805599453)
+        torch.cuda.synchronize()
+        w = torch.exp2(small.double() - 20).to(DEV)
+        want = ((w[:, None, None] * v.double()).sum(0) / w.sum())[None]
+        # The scale's own rounding, three units of a difference of 20; sums of n terms; the output.  Up to 1024 the exponent of
+        # a weight is a product with the common part, two roundings to 2^-14.
+        limit = (lim.half(DT[dt]) + (n + 100) * lim.U + (2.0 ** -13 if common <= 2.0 ** 10 else 0)) * want
+        over = (out.double() - want).abs() - limit
+        assert float(over.max()) <= 0, f"{float(out[0, 0, 0])!r} instead of {float(want[0, 0, 0])!r}"
