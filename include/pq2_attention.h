@@ -24,7 +24,8 @@
  * hides it; other sequences, and what lies behind a sequence's end, have no
  * influence.  Scores, and sums of weights (up to 2^8, of prompts in fp16 2^15) times
  * values, are FP32 before they are normalised: q . k, scale * q . k and 2^40 times
- * the largest value stay within its range.
+ * the largest value stay within its range; products of weights and values below 2^-100
+ * lose bits.
  */
 #ifndef PQ2_ATTENTION_H
 #define PQ2_ATTENTION_H

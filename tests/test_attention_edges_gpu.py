@@ -407,3 +407,99 @@ def test_prompt_large_scores_in_common(common, d, dt):
         limit = (lim.half(DT[dt]) + (n + 100) * lim.U + (2.0 ** -13 if common <= 2.0 ** 10 else 0)) * want
         over = (out.double() - want).abs() - limit
         assert float(over.max()) <= 0, f"{float(out[0, 0, 0])!r} instead of {float(want[0, 0, 0])!r}"
+
+
+# ---------------------------------------------------------------- the ends of the ranges
+@pytest.mark.parametrize("heads,kv,d", [(1024, 1, 64), (200, 1, 128), (1024, 1024, 64), (999, 27, 256), (1024, 8, 128)])
+def test_many_heads(heads, kv, d):
+    announce(f"many heads {heads}/{kv} d={d}")
+    pq2 = _pq2()
+    nq, nk = [5, 0, 40], [77, 9, 40]
+    q = torch.zeros((sum(nq), heads, d), dtype=torch.bfloat16, device=DEV)
+    k = randn((sum(nk), kv, d), 1).bfloat16().to(DEV)
+    v = randint(-127, 127, (sum(nk), kv, d), 2).bfloat16().to(DEV)
+    out = torch.full_like(q, float("nan"))
+    pq2.pq2_attention_prompt(q, k, v, out, starts_of(nq), starts_of(nk))
+    cache = ref.make_cache(12, 16, kv, d, 4, DEV)
+    ref.parts(cache, 16, kv, d)[3].fill_(2.0 ** -6)
+    table = torch.arange(12, dtype=torch.int32, device=DEV).view(2, 6)
+    lengths, new = [90, 33], [2, 1]
+    got = paged_call(lengths, new, heads, kv, d, 16, "bf16", 0, q[:3], cache, table)
+    a = b = at = 0
+    for n, m in zip(nq, nk):
+        if n:
+            seen = lim.seen_keys(n, m, m - n, device=DEV)
+            lim.check_counts(out[a:a + n], lim.mean_of_seen(v[b:b + m], seen, heads), torch.bfloat16, "prompt")
+        a, b = a + n, b + m
+    for i, (n, t) in enumerate(zip(lengths, new)):
+        _, vv, _ = ref.rows_of(cache, 16, kv, d, table[i], n)
+        lim.check_counts(got[at:at + t], lim.mean_of_seen(vv, lim.seen_keys(t, n, n - t, device=DEV), heads), torch.bfloat16, "paged")
+        at += t
+
+
+def test_most_sequences():
+    """65535 sequences of none to three tokens."""
+    announce("65535 sequences")
+    pq2 = _pq2()
+    heads, kv, d, seqs = 2, 1, 64, 65535
+    n = randint(0, 3, (seqs,), 1).to(DEV)
+    starts = torch.zeros(seqs + 1, dtype=torch.int32, device=DEV)
+    starts[1:] = n.cumsum(0)
+    rows = int(starts[-1])
+    seq = torch.repeat_interleave(torch.arange(seqs, device=DEV), n)
+    t = torch.arange(rows, device=DEV) - starts[seq]
+    v = randint(-127, 127, (rows, kv, d), 2).to(DEV)
+    # Row t of a sequence sees t + 1 values: their mean.
+    sums = v.double().cumsum(0)
+    before = torch.cat([torch.zeros_like(sums[:1]), sums])[starts[seq].long()]
+    mean = ((sums - before) / (t + 1).double()[:, None, None]).repeat_interleave(heads, 1)
+    q = torch.zeros((rows, heads, d), dtype=torch.bfloat16, device=DEV)
+    k = randn((rows, kv, d), 3).bfloat16().to(DEV)
+    out = torch.full_like(q, float("nan"))
+    pq2.pq2_attention_prompt(q, k, v.bfloat16(), out, starts, starts)
+    torch.cuda.synchronize()
+    lim.check_counts(out, mean, torch.bfloat16, "prompt")
+    # The same tokens in a cache, a page for each sequence.
+    page = 16
+    cache = torch.zeros((seqs, pq2.pq2_kv_page_bytes(page, kv, d)), dtype=torch.uint8, device=DEV)
+    kc, vc, ks, vs = ref.parts(cache, page, kv, d)
+    vc[seq, :, t] = v.to(torch.int8)
+    vs[seq, :, t] = 1.0
+    table = torch.arange(seqs, dtype=torch.int32, device=DEV).flip(0).contiguous().view(seqs, 1)
+    cache = cache.flip(0).contiguous()
+    got = torch.full_like(q, float("nan"))
+    floats, words = pq2.pq2_attention_paged_workspace(seqs, 3, heads, kv, d, 16)
+    assert (floats, words) == (0, 0)
+    pq2.pq2_attention_paged(q, cache, table, n.int(), page, got, starts=starts, max_new=3, max_len=16)
+    back = [torch.full((rows, kv, d), float("nan"), device=DEV) for _ in "kv"]
+    pq2.pq2_kv_read(cache, table, starts, page, *back)
+    torch.cuda.synchronize()
+    lim.check_counts(got, mean, torch.bfloat16, "paged")
+    assert torch.equal(back[1], v.float()) and not bool(back[0].any())
+
+
+@pytest.mark.parametrize("d", ref.DIMS)
+def test_kv_write_rows_of_every_size(d):
+    """Rows from the smallest FP32 numbers to the largest: codes and scales by the definition."""
+    announce(f"kv write, rows of every size d={d}")
+    pq2 = _pq2()
+    sizes = [2.0 ** e for e in range(-149, 127, 3)]
+    m = len(sizes)
+    x = randn((m, 2, d), 1).clamp(-2, 2).double() * torch.tensor(sizes, dtype=torch.float64)[:, None, None]
+    x = x.float()
+    assert bool(torch.isfinite(x).all())
+    page = 16
+    pages = (m + page - 1) // page
+    cache = torch.full((pages, pq2.pq2_kv_page_bytes(page, 1, d)), 0xA5, dtype=torch.uint8, device=DEV)
+    xd = x.to(DEV)
+    pq2.pq2_kv_write(xd[:, :1], xd[:, 1:], cache, torch.arange(m, dtype=torch.int32, device=DEV), page)
+    torch.cuda.synchronize()
+    want = torch.full(cache.shape, 0xA5, dtype=torch.uint8)
+    kc, vc, ks, vs = ref.parts(want, page, 1, d)
+    pg, at = torch.arange(m) // page, torch.arange(m) % page
+    (kc[pg, :, at], ks[pg, :, at]), (vc[pg, :, at], vs[pg, :, at]) = ref.codes(x[:, :1]), ref.codes(x[:, 1:])
+    got = ref.parts(cache.cpu(), page, 1, d)
+    for name, a, b in zip(("k codes", "v codes", "k scales", "v scales"), got, (kc, vc, ks, vs)):
+        a, b = a[pg, :, at], b[pg, :, at]
+        bad = (a != b).flatten(1).any(1)
+        assert not bool(bad.any()), f"{name} of rows of size {[sizes[i] for i in bad.nonzero().flatten().tolist()][:6]}"
