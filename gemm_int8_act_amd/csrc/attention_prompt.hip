@@ -13,8 +13,8 @@
 //
 // Precision: scores, references and sums are FP32.  The weights are rounded to the
 // tensors' type, what the second product's operand holds, and their sum takes the
-// rounded ones: against 64 bits the result is 1.25 to 1.3 times as far off as its own
-// last rounding makes it (bf16 0.0020 to 0.0021 of the norm, fp16 0.00027).  Weights as two numbers, as
+// rounded ones: against 64 bits the result is 1.2 to 1.35 times as far off as its own
+// last rounding makes it (bf16 0.0020 to 0.0022 of the norm, fp16 0.00024 to 0.00028).  Weights as two numbers, as
 // over the pages, would double the second product, half of the matrix cores' work.
 //
 // Bound: the matrix cores (54 % of their cycles on 8192 tokens, 40 heads of
